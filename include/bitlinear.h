@@ -103,6 +103,7 @@ extern "C" {
 
 #define BL_DTYPE_F32 0
 #define BL_DTYPE_BF16 1
+#define BL_DTYPE_I8 2         /* key-value caches only: int8 with a scale per token and head */
 
 /* Sizes of the packed buffers of an n x K master under (N, M, layout), in bytes, the packed K
  * axis K_eff, and the workspace bytes bitlinear_pack needs.  Any output pointer may be NULL.
@@ -523,6 +524,134 @@ int bitlinear_bwd_group_build(const bl_bwd_desc* descs, int64_t count, int64_t T
 
 /* Enqueues the grouped backward of a built table on `stream`. */
 int bitlinear_bwd_group(const void* table, const bl_bwd_group_plan* plan, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Between the projections of a decoder block: the residual's addition, RMS norm and quantization
+ * in front of a projection (BitNet b1.58 page, "The mechanism": a norm precedes every activation
+ * quantization), rotary positions, a paged key-value cache and the decode attention over it.
+ *
+ * bitlinear_norm_quant, per token t:
+ *   h    = x + res rounded once to res_dtype (res NULL: h is x, and the h argument must be NULL)
+ *   rstd = fl32(1 / sqrt(sum(h^2) / K + eps)): squares in fp32, their sum and the root in fp64
+ *   n    = fl32(fl32(h * rstd) * w)                 (w fp32 [K]; NULL: fl32(h * rstd))
+ *   xq, x_scale = what act_quant_i8 writes for the fp32 rows n with this lift_M, bit for bit.
+ * x is x_dtype [T][K], res and h res_dtype [T][K], xq [T][K_eff] int8, x_scale [T] fp32, rstd_opt
+ * (or NULL) [T] fp32, kept for the gradient.  K % 8 == 0 (lifted: act_quant_i8's rule),
+ * K <= 32768 (BL_ENOTSUP beyond), eps > 0.  h may be res itself, or x where the types agree
+ * (in place); no other output may overlap an input or an output (BL_EINVAL).  One launch. */
+int bitlinear_norm_quant(const void* x, int x_dtype, const void* res, int res_dtype,
+                         const float* w, double eps, int64_t T, int64_t K, int lift_M, void* h,
+                         int8_t* xq, float* x_scale, float* rstd_opt, void* stream);
+
+/* Gradient of bitlinear_norm_quant, straight through the quantizer (and through the rounding of
+ * h), from dn, the gradient of the rows n (the dx of bitlinear_bwd; dn_dtype [T][K]), and the
+ * forward's h (h_dtype) and rstd:
+ *   dh = rstd * (dn*w - h*rstd * mean_k(dn*w * h*rstd)) + dres   (grad_dtype; dres, the gradient
+ *        that reaches h along the residual stream, may be NULL) -- the gradient of x and of res
+ *   dw = sum_t dn * h*rstd   (fp32 [K]; NULL: not computed)
+ * Sums are fp32 in a fixed order: results do not vary from run to run.  dh may be dres itself, or
+ * dn where the types agree.  ws: bitlinear_norm_quant_bwd_workspace_bytes of device scratch (16-byte
+ * aligned; contents on entry irrelevant), not needed (NULL, 0) without dw.  T == 0 writes dw = 0.
+ * One launch, and a second one for dw. */
+int bitlinear_norm_quant_bwd_workspace_bytes(int64_t T, int64_t K, size_t* ws_bytes);
+int bitlinear_norm_quant_bwd(const void* dn, int dn_dtype, const void* h, int h_dtype,
+                             const float* rstd, const float* w, const void* dres, void* dh,
+                             int grad_dtype, float* dw, int64_t T, int64_t K, void* ws,
+                             size_t ws_bytes, void* stream);
+
+/* cos and sin by position: table[p][i] = {mscale * cos(p * freq[i]), mscale * sin(p * freq[i])},
+ * p < positions, i < half, computed in fp64 and rounded once.  freq is fp64 on the device; table is
+ * fp32 [positions][half][2], 16-byte aligned. */
+int bitlinear_rope_table(const double* freq, int64_t half, int64_t positions, double mscale,
+                         float* table, void* stream);
+
+/* One tensor of heads: element d of head h of token t is at t * tok + h * head + d (strides in
+ * elements; x may be a slice of a fused projection's rows, or broadcast along tokens or heads). */
+typedef struct bl_rope_desc {
+  const void* x;
+  void* y;                           /* NULL for the keys and values of bitlinear_rope_append */
+  int64_t x_tok, x_head, y_tok, y_head;
+  int64_t heads;
+} bl_rope_desc;
+
+/* Rotary positions on count (1 to 4) tensors of T tokens and head dimension D in one launch.  The
+ * first R elements of a head (R even, R <= D) are R/2 pairs -- (i, i + R/2), or (2i, 2i + 1) if
+ * interleaved -- and with {c, s} = table[pos[t]][i]
+ *   y_a = x_a c - x_b s     y_b = x_b c + x_a s     (inverse: s negated, which is the gradient)
+ * with separate fp32 products and sums, rounded once to y_dtype; the other elements are copied.
+ * pos is int32 [T].  A token at a position below 0 is padding: its rows become 0.  One at a
+ * position of `positions` or more has no table entry: its rows become NaN.  y may be x itself with
+ * the same type and strides; otherwise no row of a y may overlap a row of an x or y.  Any alignment
+ * of the elements; rows of 8-multiples (D, R) aligned to four elements take the vector path.
+ * 1 <= D <= 256. */
+int bitlinear_rope(const bl_rope_desc* descs, int64_t count, int64_t T, int64_t D, int64_t R,
+                   int interleaved, int inverse, int x_dtype, int y_dtype, const int32_t* pos,
+                   const float* table, int64_t positions, void* stream);
+
+/* A paged key-value cache.  Element d of head h of slot o of page p is at p * page_stride +
+ * h * head_stride + o * tok_stride + d of k and of v (strides in elements, the same for both; the
+ * rows must not overlap).  dtype BL_DTYPE_BF16, or BL_DTYPE_I8 with k_scale and v_scale fp32
+ * [pages][heads][page_size] contiguous: an element stands for its int8 value times its row's scale.
+ * head_dim: a multiple of 8 (BF16) or 16 (I8), at most 256; strides multiples of the same; k and v
+ * 16-byte aligned. */
+typedef struct bl_kv_cache {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t page_stride, head_stride, tok_stride;
+  int64_t pages;
+  int32_t page_size, heads, head_dim, dtype;
+} bl_kv_cache;
+
+/* bitlinear_rope on the queries and keys of T tokens, and the keys and values into the cache, in
+ * one launch.  qkv[0] = queries (y of q_dtype), qkv[1] = keys, qkv[2] = values (y unused), all of
+ * x_dtype; keys and values have kv->heads heads.  Token t belongs to sequence seq[t] (seq NULL:
+ * sequence t) at position pos[t], whose page is blocks[seq][pos / page_size] (int32
+ * [seqs][blocks_per_seq]) and whose slot is pos % page_size.  BF16 caches hold the rotated key and
+ * the value rounded once; I8 caches what act_quant_i8 writes for them per token and head.  Nothing
+ * is written for a token whose position is below 0 or has no table entry, whose sequence or block
+ * is out of range, or whose page is not in [0, pages); its query row is as bitlinear_rope's.  Two
+ * tokens of one call must not name the same slot.  R % 8 == 0; input and query rows aligned to four
+ * elements. */
+int bitlinear_rope_append(const bl_rope_desc* qkv, int64_t T, int64_t R, int interleaved,
+                          int x_dtype, int q_dtype, const int32_t* pos, const int32_t* seq,
+                          const int32_t* blocks, int64_t seqs, int64_t blocks_per_seq,
+                          const float* table, int64_t positions, const bl_kv_cache* kv,
+                          void* stream);
+
+/* Decode attention: one query token per sequence over the cache.  With G = q_heads / kv->heads,
+ * query head h attends key head h / G:
+ *   s_j = scale * (q . k_j),  out = sum_j softmax(s)_j v_j,  lse = log sum_j exp(s_j)
+ * over the sequence's positions j < lens[b] (the last `window` of them if window > 0) whose page
+ * blocks[b][j / page_size] lies in [0, pages): a page outside is a hole, and its keys are masked.
+ * What masked slots hold (NaN included) never reaches a result; a live key or value that is not
+ * finite makes its heads' results not finite, except that keys whose score is -inf weigh nothing.  A
+ * sequence without live keys, or of such keys alone, gives out = 0 and lse = -inf.  lens is int32 [B]; lengths past blocks_per_seq * page_size are cut there.
+ *
+ * The plan splits the work by max_len, an upper bound of the lengths it is tuned for (longer
+ * sequences are computed as well, less evenly).  ws is the plan's ws_bytes of device scratch
+ * (256-byte aligned), zeroed by the caller once before its first use; launches that share it must
+ * be ordered on one stream.  Scores and sums are fp32; probabilities enter the product with the
+ * values as two bf16 terms, fp32 queries as three.  The result does not depend on the order in which
+ * blocks run. */
+typedef struct bl_attn_plan {
+  int64_t B, max_len;
+  int32_t q_heads, kv_heads, head_dim, window;
+  int32_t splits, chunk;             /* runs per sequence and head group; keys per run */
+  size_t ws_bytes;
+} bl_attn_plan;
+
+int bitlinear_paged_attn_plan(int64_t B, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                              int64_t max_len, int64_t window, bl_attn_plan* plan);
+
+/* q is q_dtype (F32 or BF16): head h of sequence b at b * q_tok + h * q_head (16-byte aligned,
+ * strides multiples of 8); out is q_dtype [B][q_heads][head_dim], lse_opt fp32 [B][q_heads] or
+ * NULL. */
+int bitlinear_paged_attn(const bl_attn_plan* plan, const void* q, int q_dtype, int64_t q_tok,
+                         int64_t q_head, float scale, const bl_kv_cache* kv, const int32_t* blocks,
+                         int64_t blocks_per_seq, const int32_t* lens, void* out, float* lse_opt,
+                         void* ws, size_t ws_bytes, void* stream);
 
 /* Static description of a status code. */
 const char* bitlinear_strerror(int status);

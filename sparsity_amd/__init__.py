@@ -20,3 +20,9 @@ from .bitlinear import (  # noqa: F401
     bitlinear_chain_build, bitlinear_fwd_chain, BL_LAYOUT_SPARSE6, bitlinear_transcode6,
     transcode6,
 )
+from .block import (  # noqa: F401
+    BL_DTYPE_I8, BlAttnPlan, BlKvCache, BlRopeDesc, PagedAttn, bitlinear_norm_quant,
+    bitlinear_norm_quant_bwd, bitlinear_norm_quant_bwd_workspace_bytes, bitlinear_paged_attn,
+    bitlinear_paged_attn_plan, bitlinear_rope, bitlinear_rope_append, bitlinear_rope_table,
+    norm_quant, norm_quant_bwd, rope, rope_append, rope_frequencies, rope_table,
+)

@@ -1,0 +1,358 @@
+// C ABI of the operators between a decoder block's projections: host-side validation, then launches
+// on the caller's stream.  Every check runs before anything is enqueued.
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "bitlinear.h"
+#include "block_ops.hpp"
+#include "device_common.hpp"
+
+namespace {
+
+bool aligned(const void* p, uintptr_t a) { return p && ((uintptr_t)p & (a - 1)) == 0; }
+bool float_dtype(int d) { return d == BL_DTYPE_F32 || d == BL_DTYPE_BF16; }
+int64_t esize(int d) { return d == BL_DTYPE_F32 ? 4 : d == BL_DTYPE_BF16 ? 2 : 1; }
+int status_of(hipError_t e) { return e == hipSuccess ? BL_OK : BL_EIO; }
+
+// A buffer of a call; NULL buffers do not take part.
+struct Span {
+  const void* p;
+  uint64_t bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+  if (!a.p || !b.p || !a.bytes || !b.bytes) return false;
+  const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+  return x < y + b.bytes && y < x + a.bytes;
+}
+
+// [T][K] sizes whose element count stays addressable and whose rows fit a grid.
+bool rows_ok(int64_t T, int64_t K) { return T >= 0 && T <= INT32_MAX && K >= 8 && K % 8 == 0; }
+
+}  // namespace
+
+extern "C" {
+
+int bitlinear_norm_quant(const void* x, int x_dtype, const void* res, int res_dtype,
+                         const float* w, double eps, int64_t T, int64_t K, int lift_M, void* h,
+                         int8_t* xq, float* x_scale, float* rstd_opt, void* stream) {
+  if (!float_dtype(x_dtype) || (res && !float_dtype(res_dtype))) return BL_ENOTSUP;
+  if (lift_M != 0) {
+    if (lift_M < 6 || lift_M > 16 || lift_M % 2) return BL_EINVAL;
+    if (K % bl::lcm_i(lift_M, 8) != 0) return BL_EINVAL;
+  }
+  if (!rows_ok(T, K) || !(eps > 0.0) || !isfinite(eps)) return BL_EINVAL;
+  if (K > bl::kNormMaxK) return BL_ENOTSUP;
+  if (T == 0) return BL_OK;
+  if (!aligned(x, 16) || !aligned(xq, 16) || !aligned(x_scale, 4)) return BL_EINVAL;
+  if ((res != nullptr) != (h != nullptr)) return BL_EINVAL;
+  if (res && (!aligned(res, 16) || !aligned(h, 16))) return BL_EINVAL;
+  if ((w && !aligned(w, 16)) || (rstd_opt && !aligned(rstd_opt, 4))) return BL_EINVAL;
+  const uint64_t n = (uint64_t)T * (uint64_t)K;
+  const uint64_t keff = lift_M ? (uint64_t)K / lift_M * (2 * lift_M - 4) : (uint64_t)K;
+  const Span in[3] = {{x, n * esize(x_dtype)}, {res, res ? n * esize(res_dtype) : 0}, {w, (uint64_t)K * 4}};
+  const Span out[4] = {{h, h ? n * esize(res_dtype) : 0}, {xq, T * keff}, {x_scale, (uint64_t)T * 4},
+                       {rstd_opt, (uint64_t)T * 4}};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < 3; ++j) {
+      const bool in_place = i == 0 && out[i].p == in[j].p && (j == 1 || (j == 0 && x_dtype == res_dtype));
+      if (!in_place && overlap(out[i], in[j])) return BL_EINVAL;
+    }
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return BL_EINVAL;
+  }
+  const bl::NormArgs a = {x, res, w, h, xq, x_scale, rstd_opt, eps, (int32_t)T, (int32_t)K, lift_M};
+  return status_of(bl::launch_norm_quant(a, x_dtype == BL_DTYPE_BF16, res_dtype == BL_DTYPE_BF16,
+                                         (hipStream_t)stream));
+}
+
+int bitlinear_norm_quant_bwd_workspace_bytes(int64_t T, int64_t K, size_t* ws_bytes) {
+  if (!rows_ok(T, K) || !ws_bytes) return BL_EINVAL;
+  if (K > bl::kNormMaxK) return BL_ENOTSUP;
+  *ws_bytes = (size_t)bl::norm_bwd_blocks(T, K) * (size_t)K * 4;
+  return BL_OK;
+}
+
+int bitlinear_norm_quant_bwd(const void* dn, int dn_dtype, const void* h, int h_dtype,
+                             const float* rstd, const float* w, const void* dres, void* dh,
+                             int grad_dtype, float* dw, int64_t T, int64_t K, void* ws,
+                             size_t ws_bytes, void* stream) {
+  if (!float_dtype(dn_dtype) || !float_dtype(h_dtype) || !float_dtype(grad_dtype)) return BL_ENOTSUP;
+  size_t need = 0;
+  const int st = bitlinear_norm_quant_bwd_workspace_bytes(T, K, &need);
+  if (st != BL_OK) return st;
+  if (T == 0 && !dw) return BL_OK;
+  if (T > 0 && (!aligned(dn, 16) || !aligned(h, 16) || !aligned(rstd, 4) || !aligned(dh, 16)))
+    return BL_EINVAL;
+  if ((w && !aligned(w, 16)) || (dres && !aligned(dres, 16)) || (dw && !aligned(dw, 16))) return BL_EINVAL;
+  if (dw && !aligned(ws, 16)) return BL_EINVAL;
+  if (dw && ws_bytes < need) return BL_ENOSPC;
+  if (!dw) { ws = nullptr; need = 0; }
+  const uint64_t n = (uint64_t)T * (uint64_t)K;
+  const Span in[5] = {{dn, n * esize(dn_dtype)}, {dres, n * esize(grad_dtype)}, {h, n * esize(h_dtype)},
+                      {rstd, (uint64_t)T * 4}, {w, (uint64_t)K * 4}};
+  const Span out[3] = {{dh, n * esize(grad_dtype)}, {dw, (uint64_t)K * 4}, {ws, need}};
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < 5; ++j) {
+      const bool in_place = i == 0 && out[i].p == in[j].p && (j == 1 || (j == 0 && dn_dtype == grad_dtype));
+      if (!in_place && overlap(out[i], in[j])) return BL_EINVAL;
+    }
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return BL_EINVAL;
+  }
+  const bl::NormBwdArgs a = {dn, h, rstd, w, dres, dh, dw, (float*)ws, (int32_t)T, (int32_t)K,
+                             bl::norm_bwd_blocks(T, K)};
+  return status_of(bl::launch_norm_bwd(a, dn_dtype == BL_DTYPE_BF16, h_dtype == BL_DTYPE_BF16,
+                                       grad_dtype == BL_DTYPE_BF16, (hipStream_t)stream));
+}
+
+int bitlinear_rope_table(const double* freq, int64_t half, int64_t positions, double mscale,
+                         float* table, void* stream) {
+  if (half < 1 || half > 128 || positions < 0 || positions > INT32_MAX) return BL_EINVAL;
+  if (!isfinite(mscale)) return BL_EINVAL;
+  if (positions == 0) return BL_OK;
+  if (!aligned(freq, 8) || !aligned(table, 16)) return BL_EINVAL;
+  if (overlap({freq, (uint64_t)half * 8}, {table, (uint64_t)half * positions * 8})) return BL_EINVAL;
+  return status_of(bl::launch_rope_table(freq, half, positions, mscale, table, (hipStream_t)stream));
+}
+
+}  // extern "C"
+
+namespace {
+
+// Whether a strided [T][heads][D] tensor can be read (strides, alignment to one element), and
+// whether its rows are aligned to four.
+bool strided_ok(const void* p, int64_t tok, int64_t head, int dtype) {
+  const int64_t lim = (int64_t)1 << 46;
+  return aligned(p, esize(dtype)) && tok >= 0 && head >= 0 && tok < lim && head < lim;
+}
+bool vec4(const void* p, int64_t tok, int64_t head, int dtype) {
+  return aligned(p, 4 * esize(dtype)) && tok % 4 == 0 && head % 4 == 0;
+}
+// Rows of an output lie apart: heads inside a token, or tokens inside a head.
+bool apart(int64_t T, int64_t heads, int64_t D, int64_t tok, int64_t head) {
+  if (T > 1 && tok < D) return false;
+  if (heads > 1 && head < D) return false;
+  if (T > 1 && heads > 1) return tok <= head ? head / tok >= T - 1 && head >= (T - 1) * tok + D
+                                             : tok / head >= heads - 1 && tok >= (heads - 1) * head + D;
+  return true;
+}
+
+// Checks common to both rope calls; fills the tensors.
+int rope_tensors(const bl_rope_desc* d, int64_t count, int64_t T, int64_t D, int64_t R, int x_dtype,
+                 int y_dtype, const int32_t* pos, const float* table, int64_t positions, int writes,
+                 bl::RopeArgs* a, bool* vec) {
+  int64_t heads = 0;
+  *vec = D % 8 == 0 && R % 8 == 0;
+  for (int64_t i = 0; i < count; ++i) {
+    if (d[i].heads < 1 || heads + d[i].heads > (1 << 20)) return BL_EINVAL;
+    if (T > 0) {
+      if (!strided_ok(d[i].x, d[i].x_tok, d[i].x_head, x_dtype)) return BL_EINVAL;
+      *vec = *vec && vec4(d[i].x, d[i].x_tok, d[i].x_head, x_dtype);
+      if (i < writes) {
+        if (!strided_ok(d[i].y, d[i].y_tok, d[i].y_head, y_dtype)) return BL_EINVAL;
+        if (!apart(T, d[i].heads, D, d[i].y_tok, d[i].y_head)) return BL_EINVAL;
+        if (d[i].x == d[i].y && (x_dtype != y_dtype || (T > 1 && d[i].x_tok != d[i].y_tok) ||
+                                 (d[i].heads > 1 && d[i].x_head != d[i].y_head)))
+          return BL_EINVAL;
+        *vec = *vec && vec4(d[i].y, d[i].y_tok, d[i].y_head, y_dtype);
+      }
+    }
+    a->t[i] = {d[i].x, i < writes ? d[i].y : nullptr, d[i].x_tok, d[i].x_head, d[i].y_tok, d[i].y_head,
+               (int32_t)heads, (int32_t)d[i].heads};
+    heads += d[i].heads;
+  }
+  if (T > 0 && (!aligned(pos, 4) || !aligned(table, 16))) return BL_EINVAL;
+  a->pos = pos;
+  a->table = table;
+  a->positions = positions;
+  a->T = T;
+  a->count = (int32_t)count;
+  a->heads = (int32_t)heads;
+  a->D = (int32_t)D;
+  a->R = (int32_t)R;
+  return BL_OK;
+}
+
+int check_cache(const bl_kv_cache* kv, bool scales) {
+  if (!kv) return BL_EINVAL;
+  if (kv->dtype != BL_DTYPE_BF16 && kv->dtype != BL_DTYPE_I8) return BL_ENOTSUP;
+  const int64_t q = kv->dtype == BL_DTYPE_I8 ? 16 : 8;
+  if (kv->pages < 1 || kv->pages > INT32_MAX || kv->page_size < 1 || kv->heads < 1 ||
+      kv->heads > (1 << 16) || kv->head_dim < 1 || kv->head_dim > 256 || kv->head_dim % q)
+    return BL_EINVAL;
+  // rows apart: in the order of their strides, each axis steps over all of the one before
+  struct Axis { int64_t stride, count; } ax[3] = {{kv->page_stride, kv->pages},
+                                                   {kv->head_stride, kv->heads},
+                                                   {kv->tok_stride, kv->page_size}};
+  for (auto& x : ax)
+    if (x.stride < 0 || x.stride % q || x.stride > ((int64_t)1 << 46)) return BL_EINVAL;
+  std::sort(ax, ax + 3, [](const Axis& p, const Axis& r) { return p.stride < r.stride; });
+  int64_t span = kv->head_dim;   // elements one step of the axes so far covers
+  for (auto& x : ax) {
+    if (x.count == 1) continue;
+    if (x.stride < span) return BL_EINVAL;
+    if (x.stride > ((int64_t)1 << 60) / x.count) return BL_EINVAL;
+    span += (x.count - 1) * x.stride;
+  }
+  if (!aligned(kv->k, 16) || !aligned(kv->v, 16)) return BL_EINVAL;
+  if (scales && kv->dtype == BL_DTYPE_I8 && (!aligned(kv->k_scale, 4) || !aligned(kv->v_scale, 4)))
+    return BL_EINVAL;
+  return BL_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int bitlinear_rope(const bl_rope_desc* descs, int64_t count, int64_t T, int64_t D, int64_t R,
+                   int interleaved, int inverse, int x_dtype, int y_dtype, const int32_t* pos,
+                   const float* table, int64_t positions, void* stream) {
+  if (!float_dtype(x_dtype) || !float_dtype(y_dtype)) return BL_ENOTSUP;
+  if (!descs || count < 1 || count > bl::kRopeMax) return BL_EINVAL;
+  if (T < 0 || T > INT32_MAX || D < 1 || D > 256 || R < 2 || R > D || R % 2 || positions < 0 ||
+      positions > INT32_MAX)
+    return BL_EINVAL;
+  bl::RopeArgs a = {};
+  bool vec = false;
+  const int st = rope_tensors(descs, count, T, D, R, x_dtype, y_dtype, pos, table, positions,
+                              (int)count, &a, &vec);
+  if (st != BL_OK) return st;
+  if (T == 0) return BL_OK;
+  a.interleaved = interleaved != 0;
+  a.inverse = inverse != 0;
+  return status_of(bl::launch_rope(a, x_dtype == BL_DTYPE_BF16, y_dtype == BL_DTYPE_BF16, vec,
+                                   (hipStream_t)stream));
+}
+
+int bitlinear_rope_append(const bl_rope_desc* qkv, int64_t T, int64_t R, int interleaved,
+                          int x_dtype, int q_dtype, const int32_t* pos, const int32_t* seq,
+                          const int32_t* blocks, int64_t seqs, int64_t blocks_per_seq,
+                          const float* table, int64_t positions, const bl_kv_cache* kv,
+                          void* stream) {
+  if (!float_dtype(x_dtype) || !float_dtype(q_dtype)) return BL_ENOTSUP;
+  const int cs = check_cache(kv, true);
+  if (cs != BL_OK) return cs;
+  const int64_t D = kv->head_dim;
+  if (!qkv || T < 0 || T > INT32_MAX || R < 8 || R > D || R % 8 || positions < 0 ||
+      positions > INT32_MAX || seqs < 1 || blocks_per_seq < 1 || seqs > INT32_MAX ||
+      blocks_per_seq > INT32_MAX)
+    return BL_EINVAL;
+  if (qkv[1].heads != kv->heads || qkv[2].heads != kv->heads) return BL_EINVAL;
+  bl::RopeArgs a = {};
+  bool vec = false;
+  const int st = rope_tensors(qkv, 3, T, D, R, x_dtype, q_dtype, pos, table, positions, 1, &a, &vec);
+  if (st != BL_OK) return st;
+  if (T == 0) return BL_OK;
+  if (!vec || !aligned(blocks, 4) || (seq && !aligned(seq, 4))) return BL_EINVAL;
+  a.interleaved = interleaved != 0;
+  a.kv = *kv;
+  a.blocks = blocks;
+  a.seq = seq;
+  a.seqs = seqs;
+  a.blocks_per_seq = blocks_per_seq;
+  return status_of(bl::launch_rope_append(a, x_dtype == BL_DTYPE_BF16, q_dtype == BL_DTYPE_BF16,
+                                          (hipStream_t)stream));
+}
+
+}  // extern "C"
+
+namespace {
+
+constexpr int64_t kQRows = 16;             // query heads per block
+constexpr int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
+
+struct AttnWs {
+  int64_t groups, ticket, ml, part, total;
+};
+AttnWs attn_ws(const bl_attn_plan& p) {
+  const int64_t G = p.q_heads / p.kv_heads, qt = (G + kQRows - 1) / kQRows;
+  AttnWs w;
+  w.groups = p.B * p.kv_heads * qt;
+  w.ticket = 0;
+  w.ml = up256(w.groups * 4);
+  w.part = w.ml + up256(w.groups * p.splits * 2 * kQRows * 4);
+  w.total = w.part + up256(w.groups * p.splits * std::min(G, kQRows) * p.head_dim * 4);
+  if (p.splits == 1) w.total = w.ml;       // no partial sums
+  return w;
+}
+
+}  // namespace
+
+extern "C" {
+
+int bitlinear_paged_attn_plan(int64_t B, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                              int64_t max_len, int64_t window, bl_attn_plan* plan) {
+  if (!plan || B < 0 || B > (1 << 20) || kv_heads < 1 || kv_heads > (1 << 16) || q_heads < kv_heads ||
+      q_heads > (1 << 20) || q_heads % kv_heads || head_dim < 8 || head_dim > 256 || head_dim % 8 ||
+      max_len < 1 || max_len > INT32_MAX || window < 0 || window > INT32_MAX)
+    return BL_EINVAL;
+  const int64_t G = q_heads / kv_heads, qt = (G + kQRows - 1) / kQRows;
+  const int64_t groups = B * kv_heads * qt;
+  if (groups > ((int64_t)1 << 22)) return BL_EINVAL;
+  const int64_t keys = window ? std::min(window, max_len) : max_len;
+  // enough blocks for several rounds over the chip, runs of at least 256 keys, at most 256 runs
+  int64_t splits = std::min<int64_t>(256, (keys + 255) / 256);
+  splits = std::max<int64_t>(1, std::min(splits, (4096 + groups - 1) / std::max<int64_t>(groups, 1)));
+  const int64_t chunk = ((keys + splits - 1) / splits + 127) / 128 * 128;
+  splits = (keys + chunk - 1) / chunk;
+  *plan = {B, max_len, (int32_t)q_heads, (int32_t)kv_heads, (int32_t)head_dim, (int32_t)window,
+           (int32_t)splits, (int32_t)chunk, 0};
+  plan->ws_bytes = (size_t)std::max<int64_t>(256, attn_ws(*plan).total);
+  return BL_OK;
+}
+
+int bitlinear_paged_attn(const bl_attn_plan* plan, const void* q, int q_dtype, int64_t q_tok,
+                         int64_t q_head, float scale, const bl_kv_cache* kv, const int32_t* blocks,
+                         int64_t blocks_per_seq, const int32_t* lens, void* out, float* lse_opt,
+                         void* ws, size_t ws_bytes, void* stream) {
+  if (!plan) return BL_EINVAL;
+  if (!float_dtype(q_dtype)) return BL_ENOTSUP;
+  bl_attn_plan p;
+  const int st = bitlinear_paged_attn_plan(plan->B, plan->q_heads, plan->kv_heads, plan->head_dim,
+                                           plan->max_len, plan->window, &p);
+  if (st != BL_OK) return st;
+  if (p.splits != plan->splits || p.chunk != plan->chunk) return BL_EINVAL;   // not this build's plan
+  const int cs = check_cache(kv, true);
+  if (cs != BL_OK) return cs;
+  if (kv->heads != p.kv_heads || kv->head_dim != p.head_dim) return BL_EINVAL;
+  if (!isfinite(scale) || blocks_per_seq < 0 || blocks_per_seq > INT32_MAX) return BL_EINVAL;
+  if (p.B == 0) return BL_OK;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lens, 4) || (lse_opt && !aligned(lse_opt, 4)) ||
+      (blocks_per_seq > 0 && !aligned(blocks, 4)))
+    return BL_EINVAL;
+  if (!strided_ok(q, q_tok, q_head, q_dtype) || q_tok % 8 || q_head % 8) return BL_EINVAL;
+  if (!aligned(ws, 256)) return BL_EINVAL;
+  if (ws_bytes < p.ws_bytes) return BL_ENOSPC;
+  const AttnWs w = attn_ws(p);
+  if (w.groups * p.splits > INT32_MAX) return BL_EINVAL;
+  const int64_t rows = p.B * p.q_heads;
+  const Span o = {out, (uint64_t)(rows * p.head_dim * esize(q_dtype))}, l = {lse_opt, (uint64_t)rows * 4},
+             s = {ws, p.ws_bytes};
+  if (overlap(o, l) || overlap(o, s) || overlap(l, s)) return BL_EINVAL;
+  bl::AttnArgs a = {};
+  a.kv = *kv;
+  a.q = q;
+  a.q_tok = q_tok;
+  a.q_head = q_head;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.blocks = blocks;
+  a.lens = lens;
+  a.blocks_per_seq = blocks_per_seq;
+  a.out = out;
+  a.lse = lse_opt;
+  a.ticket = (uint32_t*)((char*)ws + w.ticket);
+  a.ml = (float*)((char*)ws + w.ml);
+  a.part = (float*)((char*)ws + w.part);
+  a.B = p.B;
+  a.Hq = p.q_heads;
+  a.G = p.q_heads / p.kv_heads;
+  a.qtiles = (int32_t)((a.G + kQRows - 1) / kQRows);
+  a.splits = p.splits;
+  a.chunk = p.chunk;
+  a.window = p.window;
+  return status_of(bl::launch_paged_attn(a, q_dtype == BL_DTYPE_BF16, (hipStream_t)stream));
+}
+
+}  // extern "C"
