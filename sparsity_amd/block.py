@@ -347,30 +347,33 @@ def rope(xs, pos, table, interleaved: bool = False, inverse: bool = False, dtype
     return outs
 
 
-def _cache(k, v, k_scale, v_scale, device) -> BlKvCache:
+def _cache_check(k, v, k_scale, v_scale, device):
     """Checks of a cache's tensors [pages][heads][page_size][D] (any strides but the last, the same
-    for both) and scales [pages][heads][page_size]."""
+    for both) and scales [pages][heads][page_size]; returns the shape."""
     import torch
     if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
         raise ValueError("k_cache, v_cache: must be [pages][heads][page_size][D] with the same "
                          "shape, strides and dtype")
     if not k.is_cuda or k.device != device or v.device != device:
         raise ValueError(f"k_cache, v_cache: must be CUDA tensors on {device}")
-    pages, heads, ps, D = k.shape
-    s = k.stride()
-    if s[3] != 1 and D > 1:
+    pages, heads, ps, D = shape = k.shape
+    if k.stride(3) != 1 and D > 1:
         raise ValueError("k_cache: the last dimension must be contiguous")
     if k.dtype == torch.int8:
         _need(k_scale, torch.float32, pages * heads * ps, device, "k_scale")
         _need(v_scale, torch.float32, pages * heads * ps, device, "v_scale")
-        return BlKvCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), s[0],
-                         s[1], s[2], pages, ps, heads, D, BL_DTYPE_I8)
-    if k.dtype != torch.bfloat16:
+    elif k.dtype != torch.bfloat16:
         raise ValueError(f"k_cache: dtype must be bfloat16 or int8, got {k.dtype}")
-    if k_scale is not None or v_scale is not None:
+    elif k_scale is not None or v_scale is not None:
         raise ValueError("k_scale, v_scale: only for int8 caches")
-    return BlKvCache(k.data_ptr(), v.data_ptr(), None, None, s[0], s[1], s[2], pages, ps, heads, D,
-                     BL_DTYPE_BF16)
+    return shape
+
+
+def _cache(k, v, k_scale, v_scale) -> BlKvCache:
+    pages, heads, ps, D = k.shape
+    s = k.stride()
+    return BlKvCache(k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale), s[0], s[1], s[2], pages,
+                     ps, heads, D, BL_DTYPE_BF16 if k_scale is None else BL_DTYPE_I8)
 
 
 def rope_append(q, k, v, pos, table, k_cache, v_cache, blocks, seq=None, k_scale=None, v_scale=None,
@@ -388,7 +391,7 @@ def rope_append(q, k, v, pos, table, k_cache, v_cache, blocks, seq=None, k_scale
         raise ValueError(f"q: must be [T][heads][D], got {tuple(q.shape)}")
     T, _, D = q.shape
     dev, xdt = q.device, q.dtype
-    kv = _cache(k_cache, v_cache, k_scale, v_scale, dev)
+    _, heads, _, cache_D = _cache_check(k_cache, v_cache, k_scale, v_scale, dev)
     positions, R = _table(table, dev)
     _need(pos, torch.int32, T, dev, "pos")
     if blocks.dim() != 2:
@@ -403,15 +406,16 @@ def rope_append(q, k, v, pos, table, k_cache, v_cache, blocks, seq=None, k_scale
         out = torch.empty(q.shape, dtype=dtype, device=dev)
     sq, so = _heads(q, T, D, dev, "q", xdt), _heads(out, T, D, dev, "out", dtype)
     sk, sv = _heads(k, T, D, dev, "k", xdt), _heads(v, T, D, dev, "v", xdt)
-    if out.shape[1] != q.shape[1] or k.shape[1] != kv.heads or v.shape[1] != kv.heads or D != kv.head_dim:
+    if out.shape[1] != q.shape[1] or k.shape[1] != heads or v.shape[1] != heads or D != cache_D:
         raise ValueError("heads or head dimension of out, k, v and the cache do not fit")
     arr = (BlRopeDesc * 3)(
         BlRopeDesc(q.data_ptr(), out.data_ptr(), sq[0], sq[1], so[0], so[1], q.shape[1]),
-        BlRopeDesc(k.data_ptr(), None, sk[0], sk[1], 0, 0, kv.heads),
-        BlRopeDesc(v.data_ptr(), None, sv[0], sv[1], 0, 0, kv.heads))
+        BlRopeDesc(k.data_ptr(), None, sk[0], sk[1], 0, 0, heads),
+        BlRopeDesc(v.data_ptr(), None, sv[0], sv[1], 0, 0, heads))
     _check(bitlinear_rope_append(arr, T, R, interleaved, _dt(xdt, "q"), _dt(dtype, "dtype"),
                                  pos.data_ptr(), _ptr(seq), blocks.data_ptr(), seqs, per,
-                                 table.data_ptr(), positions, kv, _stream()),
+                                 table.data_ptr(), positions,
+                                 _cache(k_cache, v_cache, k_scale, v_scale), _stream()),
            "bitlinear_rope_append")
     return out
 
@@ -445,9 +449,9 @@ class PagedAttn:
             raise ValueError(f"q: must be [{p.B}][{p.q_heads}][{p.head_dim}], got {tuple(q.shape)}")
         s = _heads(q, p.B, p.head_dim, dev, "q")
         qd = _dt(q.dtype, "q")
-        kv = _cache(k_cache, v_cache, k_scale, v_scale, dev)
-        if kv.page_size != self.page_size:
-            raise ValueError(f"k_cache: page size must be {self.page_size}, got {kv.page_size}")
+        page = _cache_check(k_cache, v_cache, k_scale, v_scale, dev)[2]
+        if page != self.page_size:
+            raise ValueError(f"k_cache: page size must be {self.page_size}, got {page}")
         if blocks.dim() != 2 or blocks.shape[0] != p.B:
             raise ValueError(f"blocks: must be [{p.B}][blocks per sequence]")
         _need(blocks, torch.int32, 0, dev, "blocks")
@@ -461,8 +465,8 @@ class PagedAttn:
         elif want_lse:
             lse = torch.empty((p.B, p.q_heads), dtype=torch.float32, device=dev)
         _check(bitlinear_paged_attn(p, q.data_ptr(), qd, s[0], s[1],
-                                    p.head_dim ** -0.5 if scale is None else scale, kv,
-                                    blocks.data_ptr(), blocks.shape[1], lens.data_ptr(),
+                                    p.head_dim ** -0.5 if scale is None else scale,
+                                    _cache(k_cache, v_cache, k_scale, v_scale), blocks.data_ptr(), blocks.shape[1], lens.data_ptr(),
                                     out.data_ptr(), _ptr(lse), self.ws.data_ptr(), p.ws_bytes,
                                     _stream()), "bitlinear_paged_attn")
         return out if lse is None else (out, lse)
