@@ -629,16 +629,18 @@ int bitlinear_rope_append(const bl_rope_desc* qkv, int64_t T, int64_t R, int int
  * finite makes its heads' results not finite, except that keys whose score is -inf weigh nothing.  A
  * sequence without live keys, or of such keys alone, gives out = 0 and lse = -inf.  lens is int32 [B]; lengths past blocks_per_seq * page_size are cut there.
  *
- * The plan splits the work by max_len, an upper bound of the lengths it is tuned for (longer
- * sequences are computed as well, less evenly).  ws is the plan's ws_bytes of device scratch
+ * The launch shares the live keys of all sequences evenly among the plan's workgroups, by the lengths
+ * it finds on the device; runs of one sequence in several workgroups are joined in the same launch.
+ * max_len only keeps the launch of short sequences small (longer ones are computed as well).  ws is the plan's ws_bytes of device scratch
  * (256-byte aligned), zeroed by the caller once before its first use; launches that share it must
  * be ordered on one stream.  Scores and sums are fp32; probabilities enter the product with the
- * values as two bf16 terms, fp32 queries as three.  The result does not depend on the order in which
+ * values as two bf16 terms (three for fp32 queries, which enter theirs as three).  The result does not depend on the order in which
  * blocks run. */
 typedef struct bl_attn_plan {
   int64_t B, max_len;
   int32_t q_heads, kv_heads, head_dim, window;
-  int32_t splits, chunk;             /* runs per sequence and head group; keys per run */
+  int32_t blocks;                    /* workgroups, which share the keys of all sequences evenly */
+  int32_t reserved;
   size_t ws_bytes;
 } bl_attn_plan;
 

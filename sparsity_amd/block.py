@@ -14,7 +14,7 @@ import ctypes
 import math
 
 from . import bitlinear as _B
-from .bitlinear import BL_DTYPE_BF16, BL_DTYPE_F32, _check, _need, _ptr, _stream
+from .bitlinear import BL_DTYPE_BF16, BL_DTYPE_F32, _check, _ptr
 
 BL_DTYPE_I8 = 2
 _I64, _I32, _VP, _SZ, _F64, _F32 = (ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t,
@@ -39,7 +39,7 @@ class BlAttnPlan(ctypes.Structure):
     """bl_attn_plan: the split of a decode attention and its workspace."""
     _fields_ = [("B", _I64), ("max_len", _I64), ("q_heads", ctypes.c_int32),
                 ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
-                ("window", ctypes.c_int32), ("splits", ctypes.c_int32), ("chunk", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("blocks", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("ws_bytes", _SZ)]
 
 
@@ -131,26 +131,50 @@ def bitlinear_paged_attn(plan, q, q_dtype, q_tok, q_head, scale, kv, blocks, blo
 
 # ---------------------------------------------------------------------------------------------
 # torch convenience wrappers
+#
+# A decode step makes a few of these calls per layer with microseconds of GPU work each, so the
+# checks read each tensor property once and name a fault only after one was found.
 # ---------------------------------------------------------------------------------------------
+
+def _stream(index: int) -> int:
+    """torch's current stream of a device."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(index)
+
 
 def _dt(dtype, name: str) -> int:
     import torch
-    if dtype == torch.float32:
+    if dtype is torch.float32:
         return BL_DTYPE_F32
-    if dtype == torch.bfloat16:
+    if dtype is torch.bfloat16:
         return BL_DTYPE_BF16
     raise ValueError(f"{name}: dtype must be float32 or bfloat16, got {dtype}")
 
 
-def _need2(t, T: int, K: int, device, name: str, dtype=None) -> int:
-    """A contiguous [T][K] tensor; returns its dtype code."""
-    if dtype is not None and t.dtype != dtype:
+def _buf(t, dtype, numel: int, index: int, name: str) -> None:
+    """A contiguous tensor of a dtype with at least numel elements on CUDA device `index`."""
+    if t is None:
+        raise ValueError(f"{name}: buffer missing")
+    if t.dtype is not dtype or t.get_device() != index or t.numel() < numel or not t.is_contiguous():
+        raise ValueError(f"{name}: must be a contiguous {dtype} tensor of at least {numel} elements on "
+                         f"cuda:{index}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _rows(t, shape, index: int, name: str, dtype=None) -> int:
+    """A contiguous tensor of exactly this shape; returns its dtype code."""
+    if t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous {tuple(shape)} on cuda:{index}, got "
+                         f"{tuple(t.shape)} on {t.device}")
+    if dtype is not None and t.dtype is not dtype:
         raise ValueError(f"{name}: dtype must be {dtype}, got {t.dtype}")
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name}: must be a CUDA tensor on {device}, got {t.device}")
-    if tuple(t.shape) != (T, K) or not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous [{T}][{K}], got {tuple(t.shape)}")
     return _dt(t.dtype, name)
+
+
+def _device(t, name: str) -> int:
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name}: must be a CUDA tensor, got {t.device}")
+    return index
 
 
 def norm_quant(x, weight=None, residual=None, eps: float = 1e-6, lift_M: int = 0,
@@ -160,37 +184,41 @@ def norm_quant(x, weight=None, residual=None, eps: float = 1e-6, lift_M: int = 0
     h = x + residual in residual's dtype; the normed rows h * rstd * weight (fp32 weight[K]) are
     quantized as ``act_quant(..., lift_M)`` would.  Returns (xq int8 [T][K_eff], scale fp32 [T], h,
     rstd); h is x itself without a residual, rstd (fp32 [T], for ``norm_quant_bwd``) is None unless
-    wanted.  ``out`` may supply (xq, scale, h, rstd); its h may be ``residual`` (in place), or None
-    without a residual.
+    wanted.  ``out`` may supply (xq, scale, h, rstd); its h may be ``residual`` (in place), and is
+    None without a residual.
     """
     import torch
-    if x.dim() != 2:
-        raise ValueError(f"x: must be [T][K], got {tuple(x.shape)}")
-    T, K = x.shape
-    dev = x.device
-    xd = _need2(x, T, K, dev, "x")
-    rd = 0 if residual is None else _need2(residual, T, K, dev, "residual")
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError(f"x: must be [T][K], got {tuple(shape)}")
+    T, K = shape
+    ix = _device(x, "x")
+    xd = _rows(x, shape, ix, "x")
+    rd, h = 0, None
+    if residual is not None:
+        rd = _rows(residual, shape, ix, "residual")
     if weight is not None:
-        _need(weight, torch.float32, K, dev, "weight")
+        _buf(weight, torch.float32, K, ix, "weight")
     ke = K // lift_M * (2 * lift_M - 4) if lift_M else K
     if out is None:
-        xq = torch.empty((T, ke), dtype=torch.int8, device=dev)
-        scale = torch.empty(T, dtype=torch.float32, device=dev)
-        h = None if residual is None else torch.empty_like(residual)
-        rstd = torch.empty(T, dtype=torch.float32, device=dev) if want_rstd else None
+        xq = x.new_empty((T, ke), dtype=torch.int8)
+        scale = x.new_empty(T, dtype=torch.float32)
+        if residual is not None:
+            h = torch.empty_like(residual)
+        rstd = torch.empty_like(scale) if want_rstd else None
     else:
         xq, scale, h, rstd = out
-        _need(xq, torch.int8, T * ke, dev, "xq")
-        _need(scale, torch.float32, T, dev, "scale")
+        _buf(xq, torch.int8, T * ke, ix, "xq")
+        _buf(scale, torch.float32, T, ix, "scale")
         if (h is None) != (residual is None):
             raise ValueError("h: given exactly with a residual")
         if h is not None:
-            _need2(h, T, K, dev, "h", residual.dtype)
+            _rows(h, shape, ix, "h", residual.dtype)
         if rstd is not None:
-            _need(rstd, torch.float32, T, dev, "rstd")
-    _check(bitlinear_norm_quant(x.data_ptr(), xd, _ptr(residual), rd, _ptr(weight), eps, T, K,
-                                lift_M, _ptr(h), xq.data_ptr(), scale.data_ptr(), _ptr(rstd),
-                                _stream()), "bitlinear_norm_quant")
+            _buf(rstd, torch.float32, T, ix, "rstd")
+    _check(_lib().bitlinear_norm_quant(x.data_ptr(), xd, _ptr(residual), rd, _ptr(weight), eps, T, K,
+                                       lift_M, _ptr(h), xq.data_ptr(), scale.data_ptr(), _ptr(rstd),
+                                       _stream(ix)), "bitlinear_norm_quant")
     return xq, scale, x if h is None else h, rstd
 
 
@@ -205,39 +233,44 @@ def norm_quant_bwd(dn, h, rstd, weight=None, dres=None, dtype=None, want_dw: boo
     a uint8 workspace.
     """
     import torch
-    if dn.dim() != 2:
-        raise ValueError(f"dn: must be [T][K], got {tuple(dn.shape)}")
-    T, K = dn.shape
-    dev = dn.device
-    gd = _need2(dn, T, K, dev, "dn")
-    hd = _need2(h, T, K, dev, "h")
-    _need(rstd, torch.float32, T, dev, "rstd")
+    shape = dn.shape
+    if len(shape) != 2:
+        raise ValueError(f"dn: must be [T][K], got {tuple(shape)}")
+    T, K = shape
+    ix = _device(dn, "dn")
+    gd = _rows(dn, shape, ix, "dn")
+    hd = _rows(h, shape, ix, "h")
+    _buf(rstd, torch.float32, T, ix, "rstd")
     if weight is not None:
-        _need(weight, torch.float32, K, dev, "weight")
+        _buf(weight, torch.float32, K, ix, "weight")
     if dtype is None:
         dtype = dn.dtype if dres is None else dres.dtype
+    od = _dt(dtype, "dtype")
     if dres is not None:
-        _need2(dres, T, K, dev, "dres", dtype)
+        _rows(dres, shape, ix, "dres", dtype)
     if out is None:
-        dh = torch.empty((T, K), dtype=dtype, device=dev)
-        dw = torch.empty(K, dtype=torch.float32, device=dev) if want_dw else None
+        dh = dn.new_empty(shape, dtype=dtype)
+        dw = dn.new_empty(K, dtype=torch.float32) if want_dw else None
     else:
         dh, dw = out
-        _need2(dh, T, K, dev, "dh", dtype)
+        _rows(dh, shape, ix, "dh", dtype)
         if dw is not None:
-            _need(dw, torch.float32, K, dev, "dw")
+            _buf(dw, torch.float32, K, ix, "dw")
     wsb = 0
     if dw is not None:
         st, wsb = bitlinear_norm_quant_bwd_workspace_bytes(T, K)
         _check(st, "bitlinear_norm_quant_bwd_workspace_bytes")
         if ws is None:
-            ws = torch.empty(wsb, dtype=torch.uint8, device=dev)
-        _need(ws, torch.uint8, wsb, dev, "ws")
-        wsb = ws.numel()
-    _check(bitlinear_norm_quant_bwd(dn.data_ptr(), gd, h.data_ptr(), hd, rstd.data_ptr(),
-                                    _ptr(weight), _ptr(dres), dh.data_ptr(), _dt(dtype, "dtype"),
-                                    _ptr(dw), T, K, _ptr(ws) if dw is not None else None, wsb,
-                                    _stream()), "bitlinear_norm_quant_bwd")
+            ws = dn.new_empty(wsb, dtype=torch.uint8)
+        else:
+            _buf(ws, torch.uint8, wsb, ix, "ws")
+            wsb = ws.numel()
+    else:
+        ws = None
+    _check(_lib().bitlinear_norm_quant_bwd(dn.data_ptr(), gd, h.data_ptr(), hd, rstd.data_ptr(),
+                                           _ptr(weight), _ptr(dres), dh.data_ptr(), od, _ptr(dw), T,
+                                           K, _ptr(ws), wsb, _stream(ix)),
+           "bitlinear_norm_quant_bwd")
     return dh, dw
 
 
@@ -281,35 +314,38 @@ def rope_table(positions: int, freq, mscale: float = 1.0, device="cuda", out=Non
     import torch
     if isinstance(freq, (list, tuple)):
         freq = torch.tensor(freq, dtype=torch.float64, device=device)
-    _need(freq, torch.float64, 1, freq.device, "freq")
+    ix = _device(freq, "freq")
+    _buf(freq, torch.float64, 1, ix, "freq")
     half = freq.numel()
     if out is None:
-        out = torch.empty((positions, half, 2), dtype=torch.float32, device=freq.device)
-    _need(out, torch.float32, positions * half * 2, freq.device, "out")
-    _check(bitlinear_rope_table(freq.data_ptr(), half, positions, mscale, out.data_ptr(),
-                                _stream()), "bitlinear_rope_table")
+        out = freq.new_empty((positions, half, 2), dtype=torch.float32)
+    _buf(out, torch.float32, positions * half * 2, ix, "out")
+    _check(_lib().bitlinear_rope_table(freq.data_ptr(), half, positions, mscale, out.data_ptr(),
+                                       _stream(ix)), "bitlinear_rope_table")
     return out
 
 
-def _heads(t, T: int, D: int, device, name: str, dtype=None):
-    """Checks of a [T][heads][D] tensor (any strides but the last)."""
-    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != D:
-        raise ValueError(f"{name}: must be [{T}][heads][{D}], got {tuple(t.shape)}")
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name}: must be a CUDA tensor on {device}, got {t.device}")
-    if dtype is not None and t.dtype != dtype:
+def _heads(t, T: int, D: int, index: int, name: str, dtype):
+    """A [T][heads][D] tensor (any strides but the last): (token stride, head stride, heads)."""
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != T or shape[2] != D or t.get_device() != index:
+        raise ValueError(f"{name}: must be [{T}][heads][{D}] on cuda:{index}, got {tuple(shape)} on "
+                         f"{t.device}")
+    if t.dtype is not dtype:
         raise ValueError(f"{name}: dtype must be {dtype}, got {t.dtype}")
-    if t.stride(2) != 1 and D > 1:
+    s = t.stride()
+    if s[2] != 1 and D > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    return t.stride()
+    return s[0], s[1], shape[1]
 
 
-def _table(table, device):
+def _table(table, index: int):
     import torch
-    if table.dim() != 3 or table.shape[2] != 2:
-        raise ValueError(f"table: must be [positions][pairs][2], got {tuple(table.shape)}")
-    _need(table, torch.float32, 0, device, "table")
-    return table.shape[0], 2 * table.shape[1]
+    shape = table.shape
+    if len(shape) != 3 or shape[2] != 2:
+        raise ValueError(f"table: must be [positions][pairs][2], got {tuple(shape)}")
+    _buf(table, torch.float32, 0, index, "table")
+    return shape[0], 2 * shape[1]
 
 
 def rope(xs, pos, table, interleaved: bool = False, inverse: bool = False, dtype=None, outs=None):
@@ -321,59 +357,60 @@ def rope(xs, pos, table, interleaved: bool = False, inverse: bool = False, dtype
     itself (in place).
     """
     import torch
-    if not xs or xs[0].dim() != 3:
+    if not xs or len(xs[0].shape) != 3:
         raise ValueError("xs: must be tensors [T][heads][D]")
     T, _, D = xs[0].shape
-    dev, xdt = xs[0].device, xs[0].dtype
-    positions, R = _table(table, dev)
-    _need(pos, torch.int32, T, dev, "pos")
+    xdt = xs[0].dtype
+    ix = _device(xs[0], "xs")
+    positions, R = _table(table, ix)
+    _buf(pos, torch.int32, T, ix, "pos")
     if dtype is None:
         dtype = xdt if outs is None else outs[0].dtype
-    if outs is None:
-        outs = [torch.empty(x.shape, dtype=dtype, device=dev) for x in xs]
-    elif len(outs) != len(xs):
+    xd, yd = _dt(xdt, "xs"), _dt(dtype, "dtype")
+    if outs is not None and len(outs) != len(xs):
         raise ValueError("outs: one per tensor")
     strides = []
-    for i, (x, y) in enumerate(zip(xs, outs)):
-        sx = _heads(x, T, D, dev, f"xs[{i}]", xdt)
-        sy = _heads(y, T, D, dev, f"outs[{i}]", dtype)
-        if x.shape[1] != y.shape[1]:
-            raise ValueError(f"outs[{i}]: heads differ from xs[{i}]")
-        strides.append((sx[0], sx[1], sy[0], sy[1], x.shape[1]))
-    arr = (BlRopeDesc * len(xs))(*(BlRopeDesc(x.data_ptr(), y.data_ptr(), *s)
-                                   for x, y, s in zip(xs, outs, strides)))
-    _check(bitlinear_rope(arr, T, D, R, interleaved, inverse, _dt(xdt, "xs"), _dt(dtype, "dtype"),
-                          pos.data_ptr(), table.data_ptr(), positions, _stream()), "bitlinear_rope")
+    for i, x in enumerate(xs):
+        xt, xh, n = _heads(x, T, D, ix, "xs", xdt)
+        if outs is None:
+            strides.append((xt, xh, n * D, D, n))
+        else:
+            yt, yh, m = _heads(outs[i], T, D, ix, "outs", dtype)
+            if m != n:
+                raise ValueError("outs: heads differ from xs")
+            strides.append((xt, xh, yt, yh, n))
+    if outs is None:
+        outs = [x.new_empty(x.shape, dtype=dtype) for x in xs]
+    arr = (BlRopeDesc * len(xs))(*[(x.data_ptr(), y.data_ptr(), *s)
+                                   for x, y, s in zip(xs, outs, strides)])
+    _check(_lib().bitlinear_rope(arr, len(xs), T, D, R, interleaved, inverse, xd, yd, pos.data_ptr(),
+                                 table.data_ptr(), positions, _stream(ix)), "bitlinear_rope")
     return outs
 
 
-def _cache_check(k, v, k_scale, v_scale, device):
+def _cache_check(k, v, k_scale, v_scale, index: int):
     """Checks of a cache's tensors [pages][heads][page_size][D] (any strides but the last, the same
-    for both) and scales [pages][heads][page_size]; returns the shape."""
+    for both) and scales [pages][heads][page_size]; returns the fields of a BlKvCache behind its
+    pointers."""
     import torch
-    if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
+    shape, s, dtype = k.shape, k.stride(), k.dtype
+    if len(shape) != 4 or shape != v.shape or s != v.stride() or dtype is not v.dtype:
         raise ValueError("k_cache, v_cache: must be [pages][heads][page_size][D] with the same "
                          "shape, strides and dtype")
-    if not k.is_cuda or k.device != device or v.device != device:
-        raise ValueError(f"k_cache, v_cache: must be CUDA tensors on {device}")
-    pages, heads, ps, D = shape = k.shape
-    if k.stride(3) != 1 and D > 1:
+    if k.get_device() != index or v.get_device() != index:
+        raise ValueError(f"k_cache, v_cache: must be CUDA tensors on cuda:{index}")
+    pages, heads, ps, D = shape
+    if s[3] != 1 and D > 1:
         raise ValueError("k_cache: the last dimension must be contiguous")
-    if k.dtype == torch.int8:
-        _need(k_scale, torch.float32, pages * heads * ps, device, "k_scale")
-        _need(v_scale, torch.float32, pages * heads * ps, device, "v_scale")
-    elif k.dtype != torch.bfloat16:
-        raise ValueError(f"k_cache: dtype must be bfloat16 or int8, got {k.dtype}")
-    elif k_scale is not None or v_scale is not None:
+    if dtype is torch.int8:
+        _buf(k_scale, torch.float32, pages * heads * ps, index, "k_scale")
+        _buf(v_scale, torch.float32, pages * heads * ps, index, "v_scale")
+        return s[0], s[1], s[2], pages, ps, heads, D, BL_DTYPE_I8
+    if dtype is not torch.bfloat16:
+        raise ValueError(f"k_cache: dtype must be bfloat16 or int8, got {dtype}")
+    if k_scale is not None or v_scale is not None:
         raise ValueError("k_scale, v_scale: only for int8 caches")
-    return shape
-
-
-def _cache(k, v, k_scale, v_scale) -> BlKvCache:
-    pages, heads, ps, D = k.shape
-    s = k.stride()
-    return BlKvCache(k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale), s[0], s[1], s[2], pages,
-                     ps, heads, D, BL_DTYPE_BF16 if k_scale is None else BL_DTYPE_I8)
+    return s[0], s[1], s[2], pages, ps, heads, D, BL_DTYPE_BF16
 
 
 def rope_append(q, k, v, pos, table, k_cache, v_cache, blocks, seq=None, k_scale=None, v_scale=None,
@@ -387,44 +424,51 @@ def rope_append(q, k, v, pos, table, k_cache, v_cache, blocks, seq=None, k_scale
     rotated queries, in ``dtype`` (that of q); ``out`` may supply them.
     """
     import torch
-    if q.dim() != 3:
+    if len(q.shape) != 3:
         raise ValueError(f"q: must be [T][heads][D], got {tuple(q.shape)}")
     T, _, D = q.shape
-    dev, xdt = q.device, q.dtype
-    _, heads, _, cache_D = _cache_check(k_cache, v_cache, k_scale, v_scale, dev)
-    positions, R = _table(table, dev)
-    _need(pos, torch.int32, T, dev, "pos")
-    if blocks.dim() != 2:
+    xdt = q.dtype
+    ix = _device(q, "q")
+    cache = _cache_check(k_cache, v_cache, k_scale, v_scale, ix)
+    positions, R = _table(table, ix)
+    _buf(pos, torch.int32, T, ix, "pos")
+    if len(blocks.shape) != 2:
         raise ValueError("blocks: must be [seqs][blocks per sequence]")
-    _need(blocks, torch.int32, 1, dev, "blocks")
     seqs, per = blocks.shape
+    _buf(blocks, torch.int32, 1, ix, "blocks")
     if seq is not None:
-        _need(seq, torch.int32, T, dev, "seq")
+        _buf(seq, torch.int32, T, ix, "seq")
     if dtype is None:
         dtype = xdt if out is None else out.dtype
+    xd, qd = _dt(xdt, "q"), _dt(dtype, "dtype")
+    qt, qh, nq = _heads(q, T, D, ix, "q", xdt)
+    kt, kh, nk = _heads(k, T, D, ix, "k", xdt)
+    vt, vh, nv = _heads(v, T, D, ix, "v", xdt)
     if out is None:
-        out = torch.empty(q.shape, dtype=dtype, device=dev)
-    sq, so = _heads(q, T, D, dev, "q", xdt), _heads(out, T, D, dev, "out", dtype)
-    sk, sv = _heads(k, T, D, dev, "k", xdt), _heads(v, T, D, dev, "v", xdt)
-    if out.shape[1] != q.shape[1] or k.shape[1] != heads or v.shape[1] != heads or D != cache_D:
+        ot, oh, no = nq * D, D, nq
+    else:
+        ot, oh, no = _heads(out, T, D, ix, "out", dtype)
+    heads = cache[5]
+    if no != nq or nk != heads or nv != heads or D != cache[6]:
         raise ValueError("heads or head dimension of out, k, v and the cache do not fit")
-    arr = (BlRopeDesc * 3)(
-        BlRopeDesc(q.data_ptr(), out.data_ptr(), sq[0], sq[1], so[0], so[1], q.shape[1]),
-        BlRopeDesc(k.data_ptr(), None, sk[0], sk[1], 0, 0, heads),
-        BlRopeDesc(v.data_ptr(), None, sv[0], sv[1], 0, 0, heads))
-    _check(bitlinear_rope_append(arr, T, R, interleaved, _dt(xdt, "q"), _dt(dtype, "dtype"),
-                                 pos.data_ptr(), _ptr(seq), blocks.data_ptr(), seqs, per,
-                                 table.data_ptr(), positions,
-                                 _cache(k_cache, v_cache, k_scale, v_scale), _stream()),
-           "bitlinear_rope_append")
+    if out is None:
+        out = q.new_empty(q.shape, dtype=dtype)
+    arr = (BlRopeDesc * 3)((q.data_ptr(), out.data_ptr(), qt, qh, ot, oh, nq),
+                           (k.data_ptr(), None, kt, kh, 0, 0, nk),
+                           (v.data_ptr(), None, vt, vh, 0, 0, nv))
+    _check(_lib().bitlinear_rope_append(
+        arr, T, R, interleaved, xd, qd, pos.data_ptr(), _ptr(seq), blocks.data_ptr(), seqs, per,
+        table.data_ptr(), positions,
+        BlKvCache(k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale), _ptr(v_scale), *cache),
+        _stream(ix)), "bitlinear_rope_append")
     return out
 
 
 class PagedAttn:
     """Decode attention over a paged cache: ``PagedAttn(B, q_heads, heads, D, page_size, max_len)``
-    plans the split and holds the workspace; calling it attends one query token per sequence.
+    sizes the launch and holds its workspace; calling it attends one query token per sequence.
 
-    max_len is the length the split is tuned for (an upper bound of the sequences'); window > 0
+    max_len bounds the sequences' lengths (longer ones only run on too few workgroups); window > 0
     attends the last ``window`` positions only.  Calls of one object are ordered on one stream.
     """
 
@@ -434,6 +478,8 @@ class PagedAttn:
         st, self.plan = bitlinear_paged_attn_plan(B, q_heads, heads, D, max_len, window)
         _check(st, "bitlinear_paged_attn_plan")
         self.page_size = page_size
+        self.shape = torch.Size((B, q_heads, D))
+        self.scale = D ** -0.5
         self.ws = torch.zeros(self.plan.ws_bytes, dtype=torch.uint8, device=device)
 
     def __call__(self, q, k_cache, v_cache, blocks, lens, scale=None, k_scale=None, v_scale=None,
@@ -444,29 +490,32 @@ class PagedAttn:
         or given.  scale: D ** -0.5 by default.  ``out`` and ``lse`` may supply buffers.
         """
         import torch
-        p, dev = self.plan, self.ws.device
-        if tuple(q.shape) != (p.B, p.q_heads, p.head_dim):
-            raise ValueError(f"q: must be [{p.B}][{p.q_heads}][{p.head_dim}], got {tuple(q.shape)}")
-        s = _heads(q, p.B, p.head_dim, dev, "q")
-        qd = _dt(q.dtype, "q")
-        page = _cache_check(k_cache, v_cache, k_scale, v_scale, dev)[2]
-        if page != self.page_size:
-            raise ValueError(f"k_cache: page size must be {self.page_size}, got {page}")
-        if blocks.dim() != 2 or blocks.shape[0] != p.B:
-            raise ValueError(f"blocks: must be [{p.B}][blocks per sequence]")
-        _need(blocks, torch.int32, 0, dev, "blocks")
-        _need(lens, torch.int32, p.B, dev, "lens")
-        if out is None:
-            out = torch.empty((p.B, p.q_heads, p.head_dim), dtype=q.dtype, device=dev)
-        else:
-            _need(out, q.dtype, p.B * p.q_heads * p.head_dim, dev, "out")
+        ws, shape = self.ws, self.shape
+        B, heads, D = shape
+        ix = _device(ws, "workspace")
+        if q.shape != shape:
+            raise ValueError(f"q: must be {tuple(shape)}, got {tuple(q.shape)}")
+        dtype = q.dtype
+        qd = _dt(dtype, "q")
+        qt, qh, _ = _heads(q, B, D, ix, "q", dtype)
+        cache = _cache_check(k_cache, v_cache, k_scale, v_scale, ix)
+        if cache[4] != self.page_size:
+            raise ValueError(f"k_cache: page size must be {self.page_size}, got {cache[4]}")
+        if len(blocks.shape) != 2 or blocks.shape[0] != B:
+            raise ValueError(f"blocks: must be [{B}][blocks per sequence]")
+        _buf(blocks, torch.int32, 0, ix, "blocks")
+        _buf(lens, torch.int32, B, ix, "lens")
+        if out is not None:
+            _buf(out, dtype, B * heads * D, ix, "out")
         if lse is not None:
-            _need(lse, torch.float32, p.B * p.q_heads, dev, "lse")
+            _buf(lse, torch.float32, B * heads, ix, "lse")
         elif want_lse:
-            lse = torch.empty((p.B, p.q_heads), dtype=torch.float32, device=dev)
-        _check(bitlinear_paged_attn(p, q.data_ptr(), qd, s[0], s[1],
-                                    p.head_dim ** -0.5 if scale is None else scale,
-                                    _cache(k_cache, v_cache, k_scale, v_scale), blocks.data_ptr(), blocks.shape[1], lens.data_ptr(),
-                                    out.data_ptr(), _ptr(lse), self.ws.data_ptr(), p.ws_bytes,
-                                    _stream()), "bitlinear_paged_attn")
+            lse = q.new_empty((B, heads), dtype=torch.float32)
+        if out is None:
+            out = q.new_empty(shape)
+        _check(_lib().bitlinear_paged_attn(
+            self.plan, q.data_ptr(), qd, qt, qh, self.scale if scale is None else scale,
+            BlKvCache(k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale), _ptr(v_scale), *cache),
+            blocks.data_ptr(), blocks.shape[1], lens.data_ptr(), out.data_ptr(), _ptr(lse),
+            ws.data_ptr(), ws.numel(), _stream(ix)), "bitlinear_paged_attn")
         return out if lse is None else (out, lse)

@@ -264,17 +264,15 @@ constexpr int64_t kQRows = 16;             // query heads per block
 constexpr int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 
 struct AttnWs {
-  int64_t groups, ticket, ml, part, total;
+  int64_t ticket, ml, part, total;
 };
 AttnWs attn_ws(const bl_attn_plan& p) {
   const int64_t G = p.q_heads / p.kv_heads, qt = (G + kQRows - 1) / kQRows;
   AttnWs w;
-  w.groups = p.B * p.kv_heads * qt;
   w.ticket = 0;
-  w.ml = up256(w.groups * 4);
-  w.part = w.ml + up256(w.groups * p.splits * 2 * kQRows * 4);
-  w.total = w.part + up256(w.groups * p.splits * std::min(G, kQRows) * p.head_dim * 4);
-  if (p.splits == 1) w.total = w.ml;       // no partial sums
+  w.ml = up256(p.B * p.kv_heads * qt * 4);
+  w.part = w.ml + up256((int64_t)p.blocks * 2 * 2 * kQRows * 4);
+  w.total = w.part + up256((int64_t)p.blocks * 2 * std::min(G, kQRows) * p.head_dim * 4);
   return w;
 }
 
@@ -291,14 +289,12 @@ int bitlinear_paged_attn_plan(int64_t B, int64_t q_heads, int64_t kv_heads, int6
   const int64_t G = q_heads / kv_heads, qt = (G + kQRows - 1) / kQRows;
   const int64_t groups = B * kv_heads * qt;
   if (groups > ((int64_t)1 << 22)) return BL_EINVAL;
+  // a block per resident place of the chip, fewer where there is less work: tiles of 128 keys, and
+  // the start of a group as so many more (at most six: see paged_attn.hip)
   const int64_t keys = window ? std::min(window, max_len) : max_len;
-  // enough blocks for several rounds over the chip, runs of at least 256 keys, at most 256 runs
-  int64_t splits = std::min<int64_t>(256, (keys + 255) / 256);
-  splits = std::max<int64_t>(1, std::min(splits, (4096 + groups - 1) / std::max<int64_t>(groups, 1)));
-  const int64_t chunk = ((keys + splits - 1) / splits + 127) / 128 * 128;
-  splits = (keys + chunk - 1) / chunk;
+  const int64_t blocks = std::min<int64_t>(bl::paged_attn_blocks(head_dim), groups * ((keys + 127) / 128 + 6));
   *plan = {B, max_len, (int32_t)q_heads, (int32_t)kv_heads, (int32_t)head_dim, (int32_t)window,
-           (int32_t)splits, (int32_t)chunk, 0};
+           (int32_t)std::max<int64_t>(1, blocks), 0, 0};
   plan->ws_bytes = (size_t)std::max<int64_t>(256, attn_ws(*plan).total);
   return BL_OK;
 }
@@ -313,7 +309,7 @@ int bitlinear_paged_attn(const bl_attn_plan* plan, const void* q, int q_dtype, i
   const int st = bitlinear_paged_attn_plan(plan->B, plan->q_heads, plan->kv_heads, plan->head_dim,
                                            plan->max_len, plan->window, &p);
   if (st != BL_OK) return st;
-  if (p.splits != plan->splits || p.chunk != plan->chunk) return BL_EINVAL;   // not this build's plan
+  if (p.blocks != plan->blocks) return BL_EINVAL;   // not this build's plan
   const int cs = check_cache(kv, true);
   if (cs != BL_OK) return cs;
   if (kv->heads != p.kv_heads || kv->head_dim != p.head_dim) return BL_EINVAL;
@@ -326,7 +322,6 @@ int bitlinear_paged_attn(const bl_attn_plan* plan, const void* q, int q_dtype, i
   if (!aligned(ws, 256)) return BL_EINVAL;
   if (ws_bytes < p.ws_bytes) return BL_ENOSPC;
   const AttnWs w = attn_ws(p);
-  if (w.groups * p.splits > INT32_MAX) return BL_EINVAL;
   const int64_t rows = p.B * p.q_heads;
   const Span o = {out, (uint64_t)(rows * p.head_dim * esize(q_dtype))}, l = {lse_opt, (uint64_t)rows * 4},
              s = {ws, p.ws_bytes};
@@ -349,8 +344,7 @@ int bitlinear_paged_attn(const bl_attn_plan* plan, const void* q, int q_dtype, i
   a.Hq = p.q_heads;
   a.G = p.q_heads / p.kv_heads;
   a.qtiles = (int32_t)((a.G + kQRows - 1) / kQRows);
-  a.splits = p.splits;
-  a.chunk = p.chunk;
+  a.nblocks = p.blocks;
   a.window = p.window;
   return status_of(bl::launch_paged_attn(a, q_dtype == BL_DTYPE_BF16, (hipStream_t)stream));
 }

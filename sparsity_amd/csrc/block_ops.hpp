@@ -117,12 +117,13 @@ struct AttnArgs {
   int64_t blocks_per_seq;
   void* out;             // [B][Hq][D]
   float* lse;            // [B][Hq] or nullptr
-  float* part;           // [groups][splits][group rows][D] unnormalised sums
-  float* ml;             // [groups][splits][2][16] running maximum and sum
-  uint32_t* ticket;      // [groups], zero between launches
+  float* part;           // [2 * nblocks][min(G, 16)][D] sums of runs of keys
+  float* ml;             // [2 * nblocks][2][16] their running maximum and sum
+  uint32_t* ticket;      // [B * key heads * qtiles] arrivals, zero between launches
   int64_t B;
-  int32_t Hq, G, qtiles, splits, chunk, window;
+  int32_t Hq, G, qtiles, nblocks, window;
 };
+int paged_attn_blocks(int64_t head_dim);   // blocks that fill the chip
 hipError_t launch_paged_attn(const AttnArgs& a, bool q_bf16, hipStream_t s);
 
 }  // namespace bl

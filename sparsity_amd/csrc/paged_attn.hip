@@ -8,7 +8,7 @@
 // key head), so the kernel is bound by memory: the work is to keep loads in flight and to spend
 // little on each byte.
 //
-// A wave takes 32 keys at a time for up to 16 query heads of one key head, the running maximum and
+// A wave takes 32 keys at a time (64 of an int8 cache) for up to 16 query heads of one key head, the running maximum and
 // sum of the softmax in registers:
 //   S^T = K Q^T   16x16x32 MFMAs with 16 keys as rows.  A lane's operand is 16 contiguous bytes of
 //                 its key's row, straight from memory.  Lane (g, n) (g = lane / 16, n = lane % 16)
@@ -20,9 +20,9 @@
 //                 whole row), and one byte permute per two elements turns eight row pieces into
 //                 VE operands (operand j: element VE n + j of the eight keys).  No LDS, no shuffle.
 // A lane's accumulators all belong to query n, so a new maximum rescales them by one lane-local
-// factor.  Probabilities enter the product as two bf16 terms (the value and its rounding error),
-// and fp32 queries as three, so the products are good to 2^-17 and better; the matrix cores are
-// idle enough that this costs nothing.
+// factor.  Probabilities enter the product as bf16 terms (the value, and what the terms so far leave
+// of it): two where the output is bf16, good to 2^-17, three for fp32 queries and output; an fp32
+// query's three terms hold it exactly.  The matrix cores are idle enough that this costs nothing.
 //
 // The four waves of a block take quarters of the block's run of keys and join in LDS; a run's
 // partial sums go to the workspace and the last block of a (sequence, head group) to finish joins
@@ -38,6 +38,7 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kQ = 16;                      // query heads of a block
+constexpr int64_t kTile = 32 * kWaves;      // keys of a tile: one group of 32 per wave
 constexpr float kLn2 = 0.69314718055994530942f;
 
 __device__ __forceinline__ v4f mfma_bf16(const bf16x8& a, const bf16x8& b, v4f c) {
@@ -60,6 +61,28 @@ __device__ __forceinline__ void i8x4_bf16(uint32_t w, uint32_t& a, uint32_t& b) 
   b = upper_halves(i8_f32(w, 2), i8_f32(w, 3));
 }
 
+// Weight of a partial sum with running maximum m and sum l under the joint maximum.  One without live
+// keys has sums of zero and weighs nothing; any other one counts even at a weight of 0 or NaN, so that
+// a sum that is not finite is not hidden.
+__device__ __forceinline__ float weight(float m, float l, float top) {
+  if (m == -INFINITY) return l == 0.f ? 0.f : __builtin_nanf("");
+  return __builtin_amdgcn_exp2f(m - top);
+}
+
+// Device-scope accesses of the partial sums, past the caches that the XCDs do not share.
+__device__ __forceinline__ void put(float* p, float v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float get(const float* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ v4f get4(const float* p) {   // 8-byte aligned
+  const uint64_t lo = __hip_atomic_load((const uint64_t*)p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  const uint64_t hi = __hip_atomic_load((const uint64_t*)p + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return v4f{__uint_as_float((uint32_t)lo), __uint_as_float((uint32_t)(lo >> 32)),
+             __uint_as_float((uint32_t)hi), __uint_as_float((uint32_t)(hi >> 32))};
+}
+
 // VE contiguous elements of VE * BYTES bytes as dwords.
 template <int N>
 __device__ __forceinline__ void load_dw(const void* p, uint32_t* r) {
@@ -74,9 +97,50 @@ __device__ __forceinline__ void load_dw(const void* p, uint32_t* r) {
   }
 }
 
+// Resident blocks per CU (one wave of each per SIMD) that the registers allow without spilling.
+constexpr int resident(int DT) { return DT <= 128 ? 2 : 1; }
+
+// The work of a launch as one run of units: sequence after sequence, group (key head and query tile)
+// after group, each the cost of starting and ending a group, kStart units, and then its tiles of
+// kTile keys.  Every block takes an equal share, whatever the lengths; the tiles of a block fall into
+// segments, one per group it meets.  (A sequence without keys counts as one tile, so that its zeros
+// get written.)  kStart: a group costs a block about the time of 96 KB of keys and values; without it,
+// the blocks that drew the short sequences of a ragged batch ran twice as long as the others.
+constexpr int64_t start_units(int DT, int EB) {
+  const int64_t tile = kTile * 2 * DT * EB;
+  return (98304 + tile - 1) / tile;
+}
+
+struct Work {
+  int64_t total;      // units
+  int64_t blocks;     // blocks that take part
+  __device__ int64_t first(int64_t block) const { return block * total / blocks; }
+  __device__ int64_t owner(int64_t unit) const { return ((unit + 1) * blocks - 1) / total; }
+};
+
+// A value that is the same in every lane, for the compiler to know it is.
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)v >> 32));
+  return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
+// Live positions of a sequence: [first, len).
+struct Span {
+  int64_t first, len;
+  __device__ int64_t tiles() const { return max((int64_t)1, (len - first + kTile - 1) / kTile); }
+};
+__device__ __forceinline__ Span span_of(const AttnArgs& a, int64_t b) {
+  const int64_t cap = a.blocks_per_seq * a.kv.page_size;
+  Span s;
+  s.len = max((int64_t)0, min((int64_t)a.lens[b], cap));
+  s.first = a.window > 0 ? max((int64_t)0, s.len - a.window) : 0;
+  return s;
+}
+
 // DT: 64, 128 or 256, the head dimension's room.  I8: int8 cache.  QF: fp32 queries.
 template <int DT, bool I8, bool QF>
-__global__ __launch_bounds__(64 * kWaves) void paged_attn_kernel(AttnArgs a) {
+__global__ __launch_bounds__(64 * kWaves, resident(DT)) void paged_attn_kernel(AttnArgs a) {
   constexpr int EB = I8 ? 1 : 2;            // bytes per cache element
   constexpr int VE = DT / 16;               // value elements per lane and key
   constexpr int VW = VE * EB / 4;           // their dwords
@@ -84,319 +148,484 @@ __global__ __launch_bounds__(64 * kWaves) void paged_attn_kernel(AttnArgs a) {
   constexpr int KC = DT / 32;               // 32-element steps of the q . k contraction
   constexpr int KW = DT * EB / 16;          // key dwords per lane and key tile
   constexpr int QS = QF ? 3 : 1;            // bf16 terms of a query element
+  constexpr int PS = QF ? 3 : 2;            // and of a probability
+  constexpr int KG = I8 ? 2 : 1;            // runs of 32 keys a wave takes at a time: 16 KB at D = 128
+  constexpr int GK = 32 * KG;
 
-  // union: per-wave rings of two 32-key groups' row offsets, then the waves' sums
-  __shared__ __attribute__((aligned(16))) float sm_o[kWaves][kQ][DT + 4];
+  __shared__ __attribute__((aligned(16))) float sm_o[kWaves][kQ][DT + 4];   // the waves' sums
   __shared__ float sm_m[kWaves][kQ], sm_l[kWaves][kQ];
-  __shared__ __attribute__((aligned(16))) int64_t ring[kWaves][2][32];
-  __shared__ __attribute__((aligned(16))) int64_t sring[I8 ? kWaves : 1][I8 ? 2 : 1][I8 ? 32 : 1];
+  // per-wave rings of two groups of keys: byte offsets of the keys' rows (-1: masked), scales
+  __shared__ __attribute__((aligned(16))) int64_t ring[kWaves][2][GK];
+  __shared__ __attribute__((aligned(16))) float sring[I8 ? kWaves : 1][2][I8 ? GK : 1];
+  __shared__ int last_sh;
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int g = lane >> 4, n = lane & 15;
-  const int64_t grp = blockIdx.x / a.splits;          // (sequence, key head, query tile)
-  const int split = (int)(blockIdx.x - grp * a.splits);
-  const int qt = (int)(grp % a.qtiles);
-  const int64_t bh = grp / a.qtiles;
-  const int hk = (int)(bh % a.kv.heads);
-  const int64_t b = bh / a.kv.heads;
   const int D = a.kv.head_dim;
-  const int rows = min(kQ, a.G - qt * kQ);            // live query heads
-  const int hq0 = hk * a.G + qt * kQ;
+  const int per_seq = a.kv.heads * a.qtiles;   // groups per sequence
+  const int prows = min(kQ, a.G);              // rows of a partial sum
 
-  // live positions [first, len), this block's [k0, k1)
-  const int64_t cap = a.blocks_per_seq * a.kv.page_size;
-  const int64_t len = max((int64_t)0, min((int64_t)a.lens[b], cap));
-  const int64_t first = a.window > 0 ? max((int64_t)0, len - a.window) : 0;
-  const int64_t keys = len - first;
-  // a sequence longer than the plan's bound takes longer runs, in whole groups per wave
-  const int64_t per = (keys + a.splits - 1) / a.splits;
-  const int64_t chunk = max((int64_t)a.chunk, (per + 32 * kWaves - 1) / (32 * kWaves) * (32 * kWaves));
-  const int active = (int)max((int64_t)1, (keys + chunk - 1) / chunk);
-  if (split >= active) return;
-  const int64_t k0 = first + split * chunk, k1 = min(len, k0 + chunk);
-  // this wave's quarter, in whole 32-key groups
-  const int64_t quarter = ((k1 - k0 + kWaves - 1) / kWaves + 31) / 32 * 32;
-  const int64_t w0 = min(k1, k0 + wave * quarter), w1 = min(k1, w0 + quarter);
-  const int groups = (int)((w1 - w0 + 31) / 32);
-
-  // queries: operand c, lane (g, n): elements of head n (zero past the live heads and past D)
-  bf16x8 qf[QS][KC];
+  // this block's units [u0, u1), and the sequence of the first: sums over the lengths, 64 at a time
+  constexpr int64_t kStart = start_units(DT, EB);
+  auto units_of = [&](int64_t b) { return b < a.B ? (span_of(a, b).tiles() + kStart) * per_seq : 0; };
+  Work work;
+  int64_t held = units_of(lane);               // of sequence `lane`
+  int64_t mine = held;
+  for (int64_t b = lane + 64; b < a.B; b += 64) mine += units_of(b);
 #pragma unroll
-  for (int c = 0; c < KC; ++c) {
-    // the int8 cache reads 16 elements per lane, so its steps come in pairs of adjacent eights
-    const int d = I8 ? 64 * (c / 2) + 16 * g + 8 * (c & 1) : 32 * c + 8 * g;
-    float v[8] = {};
-    if (n < rows && d < D) {
-      const int64_t o = b * a.q_tok + (int64_t)(hq0 + n) * a.q_head + d;
-      load_f8<!QF>(a.q, o, v);
+  for (int s = 32; s > 0; s >>= 1) mine += __shfl_xor(mine, s, 64);
+  work.total = uniform(mine);
+  work.blocks = min((int64_t)gridDim.x, work.total);
+  if ((int64_t)blockIdx.x >= work.blocks) return;
+  const int64_t u0 = work.first(blockIdx.x), u1 = work.first(blockIdx.x + 1);
+  int64_t b = 0, seq0 = 0;                     // sequence, its first unit
+  for (int64_t base = 0; base < a.B; base += 64) {
+    int64_t end = base ? units_of(base + lane) : held;   // to inclusive sums
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) {
+      const int64_t v = __shfl_up(end, s, 64);
+      if (lane >= s) end += v;
     }
-#pragma unroll
-    for (int t = 0; t < QS; ++t) {
-      uint32_t w[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
-        v[2 * j] -= bf16_lo(w[j]);
-        v[2 * j + 1] -= bf16_hi(w[j]);
-      }
-      qf[t][c] = frag(w[0], w[1], w[2], w[3]);
-    }
+    const uint64_t past = __ballot(seq0 + end <= u0 && base + lane < a.B);   // a prefix of the lanes
+    const int skip = __popcll(past);
+    if (skip > 0) seq0 += uniform(__shfl(end, skip - 1, 64));
+    b = base + skip;
+    if (skip < 64) break;
   }
 
-  const int32_t* table = a.blocks + b * a.blocks_per_seq;
-  const int ps = a.kv.page_size;
-  const int64_t head_off = hk * a.kv.head_stride;
-  const char* kbase = (const char*)a.kv.k + head_off * EB;
-  const char* vbase = (const char*)a.kv.v + head_off * EB;
+  for (int64_t unit = u0; unit < u1;) {
+    const Span sp = span_of(a, b);
+    const int64_t tiles = sp.tiles(), units = tiles + kStart;
+    const int in_seq = (int)((unit - seq0) / units);      // group of the sequence
+    const int64_t next_group = seq0 + (in_seq + 1) * units, g0 = next_group - tiles;   // g0: its first tile
+    const int64_t tile = max(unit, g0), end = min(u1, next_group);   // the segment is [tile, end)
+    const int64_t sq = b, grp = sq * per_seq + in_seq;
+    unit = end;
+    if (unit == seq0 + units * per_seq) { seq0 = unit; ++b; }
+    if (tile >= end) continue;                            // the start of a group that the next block takes
+    const int hk = in_seq / a.qtiles, qt = in_seq - hk * a.qtiles;
+    const int64_t owner0 = work.owner(g0);
+    const int active = (int)(work.owner(g0 + tiles - 1) - owner0) + 1;   // blocks that share the group
+    const int rows = min(kQ, a.G - qt * kQ);              // live query heads
+    const int hq0 = hk * a.G + qt * kQ;
+    const int64_t k0 = sp.first + (tile - g0) * kTile, k1 = min(sp.len, sp.first + (end - g0) * kTile);
+    // this wave's quarter, in whole runs of 32 keys
+    const int64_t quarter = ((k1 - k0 + kWaves - 1) / kWaves + 31) / 32 * 32;
+    const int64_t w0 = min(k1, k0 + wave * quarter), w1 = min(k1, w0 + quarter);
+    const int groups = (int)((w1 - w0 + GK - 1) / GK);
 
-  // lane j < 32 of the wave looks after key j of each group: its page is read one group ahead of
-  // the row offset that needs it
-  auto key_of = [&](int grpi) { return w0 + 32 * (int64_t)grpi + (lane & 31); };
-  auto page_of = [&](int grpi) -> int32_t {
-    const int64_t t = key_of(grpi);
-    return t < w1 ? table[(uint32_t)t / (uint32_t)ps] : -1;
-  };
-  auto put_rows = [&](int grpi, int32_t page) {
-    const int64_t t = key_of(grpi);
-    const int off = (int)((uint32_t)t % (uint32_t)ps);
-    const bool ok = page >= 0 && page < a.kv.pages;   // a hole in the table is a masked run of keys
-    if (lane < 32) {
-      ring[wave][grpi & 1][lane] =
-          ok ? ((int64_t)page * a.kv.page_stride + (int64_t)off * a.kv.tok_stride) * EB : -1;
-      if constexpr (I8)
-        sring[wave][grpi & 1][lane] = ok ? ((int64_t)page * a.kv.heads + hk) * ps + off : 0;
-    }
-    // LDS serves a wave's accesses in order; only the compiler has to keep them so
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-  };
+    const int32_t* table = a.blocks + sq * a.blocks_per_seq;
+    const int ps = a.kv.page_size;
+    const int64_t head_off = hk * a.kv.head_stride;
+    const char* kbase = (const char*)a.kv.k + head_off * EB;
+    const char* vbase = (const char*)a.kv.v + head_off * EB;
 
-  uint32_t kr[2][KW], vr[8][VW];
-  float ksc[I8 ? 8 : 1], vsc[I8 ? 8 : 1];
-  int live = 0;                             // which of the lane's eight keys are live
-  auto load_k = [&](int grpi) {
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int64_t r = max((int64_t)0, ring[wave][grpi & 1][16 * t + n]);   // masked: any row will do
-#pragma unroll
-      for (int c = 0; c < KW / 4; ++c) {
-        const int d = I8 ? 64 * c + 16 * g : 32 * c + 8 * g;
-        if (d < D) load_dw<4>(kbase + r + d * EB, &kr[t][4 * c]);
-        else kr[t][4 * c] = kr[t][4 * c + 1] = kr[t][4 * c + 2] = kr[t][4 * c + 3] = 0;
-      }
-    }
-  };
-  auto load_v = [&](int grpi) {
-    live = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int key = 16 * (i / 4) + 4 * g + (i & 3);
-      const int64_t raw = ring[wave][grpi & 1][key];
-      const int64_t r = max((int64_t)0, raw);
-      live |= (raw >= 0 ? 1 : 0) << i;
-      if constexpr (I8) {
-        const int64_t sr = sring[wave][grpi & 1][key];
-        ksc[i] = a.kv.k_scale[sr];
-        vsc[i] = raw >= 0 ? a.kv.v_scale[sr] : 0.f;   // times a masked weight of 0
-      }
-#pragma unroll
-      for (int c = 0; c < VL; ++c) {
-        const int d = VE * n + (VE / VL) * c;
-        if (d < D) load_dw<VW / VL>(vbase + r + d * EB, &vr[i][VW / VL * c]);
-        else
-#pragma unroll
-          for (int j = 0; j < VW / VL; ++j) vr[i][VW / VL * c + j] = 0;
-      }
-    }
-  };
-
-  v4f o[VE];
-#pragma unroll
-  for (int j = 0; j < VE; ++j) o[j] = v4f{0.f, 0.f, 0.f, 0.f};
-  float m = -INFINITY, l = 0.f;
-
-  if (groups > 0) {
-    put_rows(0, page_of(0));
+    // lane j of the wave looks after key j of each group (all but j < 32 in double for GK = 32): its
+    // page is read one group ahead of the row offset that needs it
+    auto key_of = [&](int grpi) { return w0 + GK * (int64_t)grpi + (lane & (GK - 1)); };
+    auto page_of = [&](int grpi) -> int32_t {
+      const int64_t t = key_of(grpi);
+      return t < w1 ? table[(uint32_t)t / (uint32_t)ps] : -1;
+    };
+    const int32_t page0 = page_of(0);
     int32_t next = page_of(1);
-    load_k(0);
-    load_v(0);
-    for (int i = 0; i < groups; ++i) {
-      const bool more = i + 1 < groups;
-      if (more) put_rows(i + 1, next);
-      if (i + 2 < groups) next = page_of(i + 2);
-      // scores
-      v4f s[2];
+
+    // queries: operand c, lane (g, n): elements of head n (zero past the live heads and past D)
+    bf16x8 qf[QS][KC];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        s[t] = v4f{0.f, 0.f, 0.f, 0.f};
-        v4f rest = v4f{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int c = 0; c < KC; ++c) {
-          bf16x8 kf;
-          if constexpr (I8) {
-            uint32_t w[4];
-            i8x4_bf16(kr[t][2 * c], w[0], w[1]);
-            i8x4_bf16(kr[t][2 * c + 1], w[2], w[3]);
-            kf = frag(w[0], w[1], w[2], w[3]);
-          } else {
-            kf = frag(kr[t][4 * c], kr[t][4 * c + 1], kr[t][4 * c + 2], kr[t][4 * c + 3]);
-          }
-          s[t] = mfma_bf16(kf, qf[0][c], s[t]);
-#pragma unroll
-          for (int u = 1; u < QS; ++u) rest = mfma_bf16(kf, qf[u][c], rest);
-        }
-        // an infinite key times a query's zero or negative remainder would spoil its score
-        if constexpr (QF)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            s[t][r] = __builtin_isfinite(s[t][r]) ? s[t][r] + rest[r] : s[t][r];
-      }
-      if (more) load_k(i + 1);
-      const bool full = __all(live == 0xFF);
-      float x[8], mx = -INFINITY;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        x[k] = s[k / 4][k & 3] * a.scale_log2;
-        if constexpr (I8) x[k] *= ksc[k];
-        if (!full && !((live >> k) & 1)) x[k] = -INFINITY;
-        mx = fmaxf(mx, x[k]);
-      }
-      if (__any(mx > m)) {                  // a new maximum: shared by the four lanes of a query
-        mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
-        mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-        const float top = fmaxf(m, mx);
-        const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top);
-        m = top;
-        l *= f;
-#pragma unroll
-        for (int j = 0; j < VE; ++j) o[j] *= f;
-      }
-      const float base = m == -INFINITY ? 0.f : m;
-      uint32_t hi[4], lo[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float p0 = __builtin_amdgcn_exp2f(x[2 * k] - base), p1 = __builtin_amdgcn_exp2f(x[2 * k + 1] - base);
-        l += p0 + p1;
-        if constexpr (I8) { p0 *= vsc[2 * k]; p1 *= vsc[2 * k + 1]; }
-        hi[k] = pack_bf16(p0, p1);
-        lo[k] = pack_bf16(p0 - bf16_lo(hi[k]), p1 - bf16_hi(hi[k]));
-      }
-      const bf16x8 ph = frag(hi[0], hi[1], hi[2], hi[3]), pl = frag(lo[0], lo[1], lo[2], lo[3]);
-      if (!full) {                          // a masked row may hold anything: 0 * NaN is not 0
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-#pragma unroll
-          for (int w = 0; w < VW; ++w) vr[k][w] = (live >> k) & 1 ? vr[k][w] : 0u;
+    for (int c = 0; c < KC; ++c) {
+      // the int8 cache reads 16 elements per lane, so its steps come in pairs of adjacent eights
+      const int d = I8 ? 64 * (c / 2) + 16 * g + 8 * (c & 1) : 32 * c + 8 * g;
+      float v[8] = {};
+      if (n < rows && d < D) {
+        const int64_t o = sq * a.q_tok + (int64_t)(hq0 + n) * a.q_head + d;
+        load_f8<!QF>(a.q, o, v);
       }
 #pragma unroll
-      for (int j = 0; j < VE; ++j) {
+      for (int t = 0; t < QS; ++t) {
         uint32_t w[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if constexpr (I8)
-            w[k] = upper_halves(i8_f32(vr[2 * k][j / 4], j & 3), i8_f32(vr[2 * k + 1][j / 4], j & 3));
-          else
-            w[k] = __builtin_amdgcn_perm(vr[2 * k + 1][j / 2], vr[2 * k][j / 2],
-                                         j & 1 ? 0x07060302u : 0x05040100u);
+        for (int j = 0; j < 4; ++j) {
+          w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+          v[2 * j] -= bf16_lo(w[j]);
+          v[2 * j + 1] -= bf16_hi(w[j]);
         }
-        const bf16x8 vf = frag(w[0], w[1], w[2], w[3]);
-        o[j] = mfma_bf16(vf, ph, o[j]);
-        o[j] = mfma_bf16(vf, pl, o[j]);
+        qf[t][c] = frag(w[0], w[1], w[2], w[3]);
       }
-      if (more) load_v(i + 1);
     }
-  }
-  l += __shfl_xor(l, 16, 64);
-  l += __shfl_xor(l, 32, 64);
 
-  // join the waves.  Lane (g, n) holds elements VE (4g + r) + j of head n.
-  if (n < rows) {
-    if (g == 0) { sm_m[wave][n] = m; sm_l[wave][n] = l; }
+    float scl[2] = {0.f, 0.f};                // scales of the lane's key and value, on their way to LDS
+    auto put_rows = [&](int grpi, int32_t page) {
+      const int64_t t = key_of(grpi);
+      const int off = (int)((uint32_t)t % (uint32_t)ps);
+      const bool ok = page >= 0 && page < a.kv.pages;   // a hole in the table is a masked run of keys
+      ring[wave][grpi & 1][lane & (GK - 1)] =
+          ok ? ((int64_t)page * a.kv.page_stride + (int64_t)off * a.kv.tok_stride) * EB : -1;
+      if constexpr (I8) {
+        const int64_t sr = ok ? ((int64_t)page * a.kv.heads + hk) * ps + off : 0;
+        const float x = a.kv.k_scale[sr], y = a.kv.v_scale[sr];
+        scl[0] = ok ? x : 0.f;
+        scl[1] = ok ? y : 0.f;                          // times a masked weight of 0
+      }
+      // LDS serves a wave's accesses in order; only the compiler has to keep them so
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    };
+
+    // A lane whose elements lie past D reads the row's first ones instead: its key elements are
+    // cleared before use, its value elements reach only outputs past D.  A masked key reads row 0.
+    uint32_t kr[KG][2][KW], vr[KG][8][VW];
+    int live[KG];                             // which of the lane's eight keys of a run are live
+    auto load_k = [&](int grpi) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+      for (int u = 0; u < KG; ++u)
 #pragma unroll
-      for (int j = 0; j < VE; ++j) sm_o[wave][n][VE * (4 * g + r) + j] = o[j][r];
-  }
-  __syncthreads();
-  const int64_t orow = (b * a.Hq + hq0) * (int64_t)D;
-  auto finish = [&](int h, int d, float num, float den, float top) {
-    const float v = den > 0.f ? num / den : 0.f;   // NaN sums fall to 0 / 0 below
-    const float r = den == den ? v : num;
-    if constexpr (QF) ((float*)a.out)[orow + (int64_t)h * D + d] = r;
-    else ((uint16_t*)a.out)[orow + (int64_t)h * D + d] = (uint16_t)pack_bf16(r, 0.f);
-    if (d == 0 && a.lse)
-      a.lse[b * a.Hq + hq0 + h] = den > 0.f ? (top + log2f(den)) * kLn2 : den == den ? -INFINITY : den;
-  };
-  float* part = a.part + (grp * a.splits + split) * (int64_t)min(kQ, a.G) * D;
-  float* ml = a.ml + (grp * a.splits + split) * 2 * kQ;
-  for (int e = threadIdx.x; e < rows * D; e += 64 * kWaves) {
-    const int h = e / D, d = e - h * D;
-    float top = sm_m[0][h];
+        for (int t = 0; t < 2; ++t) {
+          const int64_t r = max((int64_t)0, ring[wave][grpi & 1][32 * u + 16 * t + n]);
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) top = fmaxf(top, sm_m[w][h]);
-    float num = 0.f, den = 0.f;
+          for (int c = 0; c < KW / 4; ++c) {
+            const int d = I8 ? 64 * c + 16 * g : 32 * c + 8 * g;
+            load_dw<4>(kbase + r + (d < D ? d : 0) * EB, &kr[u][t][4 * c]);
+          }
+        }
+    };
+    auto clear_k = [&](int u) {
+      if (D == DT) return;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      const float f = sm_m[w][h] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(sm_m[w][h] - top);
-      // a wave without live keys adds nothing; a NaN sum must not be hidden by f = 0
-      if (sm_m[w][h] != -INFINITY || sm_l[w][h] != 0.f) {
+      for (int c = 0; c < KW / 4; ++c) {
+        const bool in = (I8 ? 64 * c + 16 * g : 32 * c + 8 * g) < D;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) kr[u][t][4 * c + j] = in ? kr[u][t][4 * c + j] : 0u;
+      }
+    };
+    auto load_v = [&](int grpi) {
+#pragma unroll
+      for (int u = 0; u < KG; ++u) {
+        live[u] = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int64_t raw = ring[wave][grpi & 1][32 * u + 16 * (i / 4) + 4 * g + (i & 3)];
+          const int64_t r = max((int64_t)0, raw);
+          live[u] |= (raw >= 0 ? 1 : 0) << i;
+#pragma unroll
+          for (int c = 0; c < VL; ++c) {
+            const int d = VE * n + (VE / VL) * c;
+            load_dw<VW / VL>(vbase + r + (d < D ? d : 0) * EB, &vr[u][i][VW / VL * c]);
+          }
+        }
+      }
+    };
+
+    v4f o[VE];
+#pragma unroll
+    for (int j = 0; j < VE; ++j) o[j] = v4f{0.f, 0.f, 0.f, 0.f};
+    float m = -INFINITY, l = 0.f;
+
+    if (groups > 0) {
+      put_rows(0, page0);
+      load_k(0);
+      load_v(0);
+      for (int i = 0; i < groups; ++i) {
+        const bool more = i + 1 < groups;
+        if constexpr (I8) {
+          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+          sring[wave][0][lane] = scl[0];
+          sring[wave][1][lane] = scl[1];
+          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+          __builtin_amdgcn_wave_barrier();
+        }
+        // scores
+        float x[KG][8], mx = -INFINITY;
+        bool full = true;
+#pragma unroll
+        for (int u = 0; u < KG; ++u) {
+          clear_k(u);
+          full = full && __all(live[u] == 0xFF);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            v4f s = v4f{0.f, 0.f, 0.f, 0.f}, rest = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < KC; ++c) {
+              bf16x8 kf;
+              if constexpr (I8) {
+                uint32_t w[4];
+                i8x4_bf16(kr[u][t][2 * c], w[0], w[1]);
+                i8x4_bf16(kr[u][t][2 * c + 1], w[2], w[3]);
+                kf = frag(w[0], w[1], w[2], w[3]);
+              } else {
+                kf = frag(kr[u][t][4 * c], kr[u][t][4 * c + 1], kr[u][t][4 * c + 2], kr[u][t][4 * c + 3]);
+              }
+              s = mfma_bf16(kf, qf[0][c], s);
+#pragma unroll
+              for (int e = 1; e < QS; ++e) rest = mfma_bf16(kf, qf[e][c], rest);
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              float v = s[r];
+              // an infinite key times a query's zero or negative remainder would spoil its score
+              if constexpr (QF) v = __builtin_isfinite(v) ? v + rest[r] : v;
+              x[u][4 * t + r] = v * a.scale_log2;
+            }
+          }
+        }
+        if (more) {
+          put_rows(i + 1, next);
+          load_k(i + 1);
+          next = page_of(i + 2);
+        }
+#pragma unroll
+        for (int u = 0; u < KG; ++u)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            if constexpr (I8) x[u][k] *= sring[wave][0][32 * u + 16 * (k / 4) + 4 * g + (k & 3)];
+            if (!full && !((live[u] >> k) & 1)) x[u][k] = -INFINITY;
+            mx = fmaxf(mx, x[u][k]);
+          }
+        if (__any(mx > m)) {                  // a new maximum: shared by the four lanes of a query
+          mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
+          mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+          const float top = fmaxf(m, mx);
+          const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top);
+          m = top;
+          l *= f;
+#pragma unroll
+          for (int j = 0; j < VE; ++j) o[j] *= f;
+        }
+        const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int u = 0; u < KG; ++u) {
+          uint32_t pw[PS][4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float p0 = __builtin_amdgcn_exp2f(x[u][2 * k] - base);
+            float p1 = __builtin_amdgcn_exp2f(x[u][2 * k + 1] - base);
+            l += p0 + p1;
+            if constexpr (I8) {
+              const float* vs = &sring[wave][1][32 * u + 16 * (k / 2) + 4 * g + (2 * k & 3)];
+              p0 *= vs[0];
+              p1 *= vs[1];
+            }
+#pragma unroll
+            for (int e = 0; e < PS; ++e) {
+              pw[e][k] = pack_bf16(p0, p1);
+              p0 -= bf16_lo(pw[e][k]);
+              p1 -= bf16_hi(pw[e][k]);
+            }
+          }
+          bf16x8 pf[PS];
+#pragma unroll
+          for (int e = 0; e < PS; ++e) pf[e] = frag(pw[e][0], pw[e][1], pw[e][2], pw[e][3]);
+          if (!full) {                        // a masked row may hold anything: 0 * NaN is not 0
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+#pragma unroll
+              for (int w = 0; w < VW; ++w) vr[u][k][w] = (live[u] >> k) & 1 ? vr[u][k][w] : 0u;
+          }
+#pragma unroll
+          for (int j = 0; j < VE; ++j) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t* v0 = vr[u][2 * k];
+              const uint32_t* v1 = vr[u][2 * k + 1];
+              if constexpr (I8) w[k] = upper_halves(i8_f32(v0[j / 4], j & 3), i8_f32(v1[j / 4], j & 3));
+              else w[k] = __builtin_amdgcn_perm(v1[j / 2], v0[j / 2], j & 1 ? 0x07060302u : 0x05040100u);
+            }
+            const bf16x8 vf = frag(w[0], w[1], w[2], w[3]);
+#pragma unroll
+            for (int e = 0; e < PS; ++e) o[j] = mfma_bf16(vf, pf[e], o[j]);
+          }
+        }
+        if (more) load_v(i + 1);
+      }
+    }
+    l += __shfl_xor(l, 16, 64);
+    l += __shfl_xor(l, 32, 64);
+
+    // join the waves.  Lane (g, n) holds elements VE (4g + r) + j of head n.
+    if (n < rows) {
+      if (g == 0) { sm_m[wave][n] = m; sm_l[wave][n] = l; }
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int j = 0; j < VE; ++j) sm_o[wave][n][VE * (4 * g + r) + j] = o[j][r];
+    }
+    __syncthreads();
+    const int64_t orow = (sq * a.Hq + hq0) * (int64_t)D;
+    auto finish = [&](int h, int d, float num, float den, float top) {
+      const float v = den > 0.f ? num / den : 0.f;   // NaN sums fall to 0 / 0 below
+      const float r = den == den ? v : num;
+      if constexpr (QF) ((float*)a.out)[orow + (int64_t)h * D + d] = r;
+      else ((uint16_t*)a.out)[orow + (int64_t)h * D + d] = (uint16_t)pack_bf16(r, 0.f);
+      if (d == 0 && a.lse)
+        a.lse[sq * a.Hq + hq0 + h] = den > 0.f ? (top + log2f(den)) * kLn2 : den == den ? -INFINITY : den;
+    };
+    // a block's partial sums: place 0 for a group that an earlier block began, 1 for one it begins
+    const int64_t place = 2 * (int64_t)blockIdx.x + (owner0 == (int64_t)blockIdx.x);
+    float* part = a.part + place * prows * D;   // [prows][D]
+    float* ml = a.ml + place * 2 * kQ;          // [2][kQ]
+    for (int e = threadIdx.x; e < rows * D; e += 64 * kWaves) {
+      const int h = e / D, d = e - h * D;
+      float top = sm_m[0][h];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) top = fmaxf(top, sm_m[w][h]);
+      float num = 0.f, den = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const float f = weight(sm_m[w][h], sm_l[w][h], top);
         num += f * sm_o[w][h][d];
         den += f * sm_l[w][h];
       }
+      if (active == 1) {
+        finish(h, d, num, den, top);
+      } else {
+        put(part + h * D + d, num);
+        if (d == 0) { put(ml + h, top); put(ml + kQ + h, den); }
+      }
     }
-    if (active == 1) {
-      finish(h, d, num, den, top);
-    } else {
-      part[h * D + d] = num;
-      if (d == 0) { ml[h] = top; ml[kQ + h] = den; }
+    if (active > 1) {
+      // The last block of the group to arrive joins the runs.  Partial sums are stored and read by
+      // device-scope atomic accesses, which pass by the caches that the XCDs do not share, and every
+      // wave waits for its stores before the block counts as arrived; the block that arrives last
+      // reads after that.  That is the order of a device-scope release and acquire, without their
+      // write-back and invalidation of the XCD's L2 (10 us per block for the one, up to 8 us for the
+      // other while the rest of the chip streams).
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+      __builtin_amdgcn_s_waitcnt(waitcnt_imm(0));
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        last_sh = __hip_atomic_fetch_add(a.ticket + grp, 1u, __ATOMIC_RELAXED,
+                                         __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)active - 1;
+        if (last_sh)                            // ready for the next launch
+          __hip_atomic_store(a.ticket + grp, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+      __syncthreads();
+      if (last_sh) {
+        // The weights of the runs in LDS (sm_o is free), as many runs at a time as fit; then runs
+        // s = w, w + 4, ... to wave w, a lane two fours of 512 columns, the waves' sums joined in
+        // order.  The first runs' sums, maxima and columns are all asked for before any is used: a
+        // round trip to memory is most of what a join of few runs costs.
+        constexpr int kCols = 512;
+        constexpr int kRoom = kWaves * kQ * (DT + 4) - kWaves * kCols;
+        float* wt = &sm_o[0][0][0];               // [rows][at]
+        float* sums = wt + kRoom;                 // [kWaves][kCols]
+        const int at = kRoom / rows;
+        const int cols = rows * D;
+        auto run = [&](int s) { return 2 * (owner0 + s) + (s == 0); };
+        auto column = [&](int s, int e) {
+          return e < cols ? get4(a.part + run(s) * prows * D + e) : v4f{0.f, 0.f, 0.f, 0.f};
+        };
+        // thread (i, row): runs i, i + 16, ... of a row, the first kHeld of them in registers
+        constexpr int kHeld = 4, kAhead = 4;
+        const int hrow = threadIdx.x & (kQ - 1), i0 = threadIdx.x / kQ;
+        float hm[kHeld], hl[kHeld];
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k) {
+          const int s = i0 + 16 * k;
+          const bool in = hrow < rows && s < active;
+          const float* p = a.ml + run(in ? s : 0) * 2 * kQ + hrow;
+          hm[k] = in ? get(p) : -INFINITY;
+          hl[k] = in ? get(p + kQ) : 0.f;
+        }
+        v4f ahead[kAhead][2];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const int s = min(wave + kWaves * k, active - 1);
+          ahead[k][0] = column(s, 4 * lane);
+          ahead[k][1] = column(s, 256 + 4 * lane);
+        }
+        float top = -INFINITY, den = 0.f;
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k) top = fmaxf(top, hm[k]);
+        if (hrow < rows)
+          for (int s = i0 + 16 * kHeld; s < active; s += 16) top = fmaxf(top, get(a.ml + run(s) * 2 * kQ + hrow));
+        auto over_rows = [&](float v, auto op) {  // of the 16 threads of each row
+          v = op(v, __shfl_xor(v, 16, 64));
+          v = op(v, __shfl_xor(v, 32, 64));
+          __syncthreads();
+          if (lane < kQ) sums[kQ * wave + lane] = v;
+          __syncthreads();
+#pragma unroll
+          for (int w = 0; w < kWaves; ++w) v = w ? op(v, sums[kQ * w + hrow]) : sums[hrow];
+          return v;
+        };
+        top = over_rows(top, [](float x, float y) { return fmaxf(x, y); });
+#pragma unroll 1
+        for (int j = 0; j < cols; j += kCols) {
+          const int e = j + 4 * lane;
+          const int h0 = min(e / D, rows - 1), h1 = min((e + 256) / D, rows - 1);   // D % 8 == 0: one row per four
+          v4f num[2] = {v4f{0.f, 0.f, 0.f, 0.f}, v4f{0.f, 0.f, 0.f, 0.f}};
+#pragma unroll 1
+          for (int s0 = 0; s0 < active; s0 += at) {
+            const int ns = min(at, active - s0);
+            if (j == 0 || active > at) {
+              __syncthreads();
+              if (hrow < rows) {
+                auto put_weight = [&](int s, float pm, float pl) {
+                  const float f = weight(pm, pl, top);
+                  wt[hrow * at + s] = f;
+                  if (j == 0) den += f * pl;
+                };
+                int s = i0;
+                if (s0 == 0) {
+#pragma unroll
+                  for (int k = 0; k < kHeld; ++k, s += 16)
+                    if (s < ns) put_weight(s, hm[k], hl[k]);
+                }
+                for (; s < ns; s += 16) {
+                  const float* p = a.ml + run(s0 + s) * 2 * kQ + hrow;
+                  put_weight(s, get(p), get(p + kQ));
+                }
+              }
+              __syncthreads();
+            }
+            const float* w0r = wt + h0 * at;
+            const float* w1r = wt + h1 * at;
+            int s = wave;
+            if (j == 0 && s0 == 0) {
+#pragma unroll
+              for (int k = 0; k < kAhead; ++k, s += kWaves)
+                if (s < ns) { num[0] += w0r[s] * ahead[k][0]; num[1] += w1r[s] * ahead[k][1]; }
+            }
+#pragma unroll 8
+            for (; s < ns; s += kWaves) {
+              const v4f v0 = column(s0 + s, e), v1 = column(s0 + s, e + 256);
+              num[0] += w0r[s] * v0;
+              num[1] += w1r[s] * v1;
+            }
+          }
+          if (j == 0) {
+            den = over_rows(den, [](float x, float y) { return x + y; });
+            if (threadIdx.x < kQ) { sm_l[0][hrow] = den; sm_m[0][hrow] = top; }
+            __syncthreads();                      // sums is free again
+          }
+          *(v4f*)(sums + kCols * wave + 4 * lane) = num[0];
+          *(v4f*)(sums + kCols * wave + 256 + 4 * lane) = num[1];
+          __syncthreads();
+#pragma unroll
+          for (int u = 0; u < kCols; u += 64 * kWaves) {
+            const int c = j + u + threadIdx.x;
+            if (c < cols) {
+              const int h = c / D;
+              float nsum = 0.f;
+#pragma unroll
+              for (int w = 0; w < kWaves; ++w) nsum += sums[kCols * w + u + threadIdx.x];
+              finish(h, c - h * D, nsum, sm_l[0][h], sm_m[0][h]);
+            }
+          }
+          __syncthreads();
+        }
+      }
     }
-  }
-}
-
-// Joins the runs' partial sums: one block per (sequence, key head, query tile).
-template <bool QF>
-__global__ __launch_bounds__(256) void paged_attn_join_kernel(AttnArgs a) {
-  const int64_t grp = blockIdx.x;
-  const int qt = (int)(grp % a.qtiles);
-  const int64_t bh = grp / a.qtiles;
-  const int hk = (int)(bh % a.kv.heads);
-  const int64_t b = bh / a.kv.heads;
-  const int D = a.kv.head_dim, rows = min(kQ, a.G - qt * kQ), hq0 = hk * a.G + qt * kQ;
-  const int64_t cap = a.blocks_per_seq * a.kv.page_size;
-  const int64_t len = max((int64_t)0, min((int64_t)a.lens[b], cap));
-  const int64_t keys = a.window > 0 ? min(len, (int64_t)a.window) : len;
-  const int64_t per = (keys + a.splits - 1) / a.splits;
-  const int64_t chunk = max((int64_t)a.chunk, (per + 32 * kWaves - 1) / (32 * kWaves) * (32 * kWaves));
-  const int active = (int)max((int64_t)1, (keys + chunk - 1) / chunk);
-  if (active == 1) return;
-  for (int e = threadIdx.x; e < rows * D; e += 256) {
-    const int h = e / D, d = e - h * D;
-    const float* ml = a.ml + grp * a.splits * 2 * kQ;
-    const float* part = a.part + grp * a.splits * (int64_t)min(kQ, a.G) * D + h * D + d;
-    float top = -INFINITY;
-    for (int s = 0; s < active; ++s) top = fmaxf(top, ml[s * 2 * kQ + h]);
-    float num = 0.f, den = 0.f;
-    for (int s = 0; s < active; ++s) {
-      const float ms = ml[s * 2 * kQ + h], ls = ml[s * 2 * kQ + kQ + h];
-      if (ms == -INFINITY && ls == 0.f) continue;
-      const float f = ms == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ms - top);
-      num += f * part[s * (int64_t)min(kQ, a.G) * D];
-      den += f * ls;
-    }
-    const float v = den > 0.f ? num / den : 0.f;
-    const float r = den == den ? v : num;
-    const int64_t o = (b * a.Hq + hq0 + h) * (int64_t)D + d;
-    if constexpr (QF) ((float*)a.out)[o] = r;
-    else ((uint16_t*)a.out)[o] = (uint16_t)pack_bf16(r, 0.f);
-    if (d == 0 && a.lse)
-      a.lse[b * a.Hq + hq0 + h] = den > 0.f ? (top + log2f(den)) * kLn2 : den == den ? -INFINITY : den;
+    __syncthreads();                          // the next segment reuses the LDS
   }
 }
 
 template <int DT>
 hipError_t launch_attn_t(const AttnArgs& a, bool q_bf16, hipStream_t s) {
-  const int64_t groups = a.B * a.kv.heads * a.qtiles;
-  const dim3 grid((unsigned)(groups * a.splits));
+  const dim3 grid((unsigned)a.nblocks);
   const bool i8 = a.kv.dtype == BL_DTYPE_I8;
   if (q_bf16) {
     if (i8) paged_attn_kernel<DT, true, false><<<grid, 64 * kWaves, 0, s>>>(a);
@@ -405,14 +634,14 @@ hipError_t launch_attn_t(const AttnArgs& a, bool q_bf16, hipStream_t s) {
     if (i8) paged_attn_kernel<DT, true, true><<<grid, 64 * kWaves, 0, s>>>(a);
     else paged_attn_kernel<DT, false, true><<<grid, 64 * kWaves, 0, s>>>(a);
   }
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.splits == 1) return e;
-  if (q_bf16) paged_attn_join_kernel<false><<<dim3((unsigned)groups), 256, 0, s>>>(a);
-  else paged_attn_join_kernel<true><<<dim3((unsigned)groups), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 
 }  // namespace
+
+int paged_attn_blocks(int64_t head_dim) {
+  return 256 * resident(head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256);
+}
 
 hipError_t launch_paged_attn(const AttnArgs& a, bool q_bf16, hipStream_t s) {
   if (a.kv.head_dim <= 64) return launch_attn_t<64>(a, q_bf16, s);

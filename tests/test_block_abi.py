@@ -170,7 +170,7 @@ def _changed(**kw):
     (dict(lens=None), EINVAL), (dict(out=None), EINVAL), (dict(lse=P + 2), EINVAL), (dict(ws=None), EINVAL),
     (dict(ws=P + 3 * SLOT + 128), EINVAL), (dict(wsb=255), ENOSPC), (dict(out=P + 3 * SLOT), EINVAL),
     (dict(lse=P + SLOT), EINVAL), (dict(lse=P + 3 * SLOT), EINVAL), (dict(kv=_kv(heads=4)), EINVAL),
-    (dict(kv=_kv(dim=64)), EINVAL), (dict(plan=_changed(splits=99)), EINVAL), (dict(plan=_changed(chunk=64)), EINVAL),
+    (dict(kv=_kv(dim=64)), EINVAL), (dict(plan=_changed(blocks=99)), EINVAL), (dict(plan=_changed(blocks=0)), EINVAL),
     (dict(plan=_changed(B=-1)), EINVAL), (dict(plan=_changed(q_heads=21)), EINVAL)])
 def test_attention_rejects(kw, want):
     assert _attn(**kw) == want
@@ -185,9 +185,10 @@ def test_attention_plan():
     for B, hq, hk, D, n, w in [(1, 20, 5, 128, 262144, 0), (64, 32, 8, 128, 8192, 0), (1, 1, 1, 8, 1, 0),
                                (3, 500, 25, 64, 100000, 77), (1, 1, 1, 128, 2 ** 31 - 1, 0)]:
         st, p = f(B, hq, hk, D, n, w)
-        keys = min(n, w) if w else n
-        assert st == 0 and p.chunk % 128 == 0 and p.splits >= 1 and p.ws_bytes >= 256
-        assert p.splits * p.chunk >= keys and (p.splits - 1) * p.chunk < keys     # no run without keys
+        tiles = B * hk * -(-hq // hk // 16) * (-(-(min(n, w) if w else n) // 128) + 6)
+        assert st == 0 and 1 <= p.blocks <= max(1, tiles) and p.ws_bytes >= 256
+        # tickets, then two partial sums per block
+        assert p.ws_bytes >= 4 * B * hk + 2 * p.blocks * (128 + 4 * D * min(16, hq // hk))
     assert f(0, 8, 8, 64, 10, 0)[0] == 0
 
 
@@ -207,6 +208,12 @@ class Strided(FakeT):
 
     def stride(self, i=None):
         return self._s if i is None else self._s[i]
+
+    def get_device(self):
+        return self.device.index if self.is_cuda else -1
+
+    def new_empty(self, shape, dtype=None):
+        return Strided(shape, dtype or self.dtype, device=self.device)
 
 
 F32, BF, I8, I32 = torch.float32, torch.bfloat16, torch.int8, torch.int32
