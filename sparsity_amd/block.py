@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 from . import bitlinear as _B
 from .bitlinear import BL_DTYPE_BF16, BL_DTYPE_F32, _check, _ptr
@@ -43,6 +44,11 @@ class BlAttnPlan(ctypes.Structure):
                 ("ws_bytes", _SZ)]
 
 
+# The same records as bytes, which the calls below pack in one go.
+_ROPE = struct.Struct("QQ5q")
+_ROPE3 = struct.Struct("QQ5qQQ5qQQ5q")
+_KV = struct.Struct("4Q4q4i")
+
 _fns = None
 
 
@@ -51,8 +57,8 @@ def _lib():
     global _fns
     if _fns is None:
         L = _B.lib()
-        rd, kv, pl = (ctypes.POINTER(BlRopeDesc), ctypes.POINTER(BlKvCache),
-                      ctypes.POINTER(BlAttnPlan))
+        rd = kv = _VP                       # ctypes arrays, pointers or packed bytes
+        pl = ctypes.POINTER(BlAttnPlan)
         L.bitlinear_norm_quant.argtypes = [_VP, _I32, _VP, _I32, _VP, _F64, _I64, _I64, _I32, _VP,
                                            _VP, _VP, _VP, _VP]
         L.bitlinear_norm_quant_bwd_workspace_bytes.argtypes = [_I64, _I64, ctypes.POINTER(_SZ)]
@@ -112,7 +118,8 @@ def bitlinear_rope_append(qkv, T, R, interleaved, x_dtype, q_dtype, pos, seq, bl
                           blocks_per_seq, table, positions, kv, stream) -> int:
     """qkv: a ctypes array of three BlRopeDesc; kv: a BlKvCache."""
     return _lib().bitlinear_rope_append(qkv, T, R, interleaved, x_dtype, q_dtype, pos, seq, blocks,
-                                        seqs, blocks_per_seq, table, positions, kv, stream)
+                                        seqs, blocks_per_seq, table, positions,
+                                        None if kv is None else ctypes.byref(kv), stream)
 
 
 def bitlinear_paged_attn_plan(B, q_heads, kv_heads, head_dim, max_len, window):
@@ -125,7 +132,8 @@ def bitlinear_paged_attn_plan(B, q_heads, kv_heads, head_dim, max_len, window):
 
 def bitlinear_paged_attn(plan, q, q_dtype, q_tok, q_head, scale, kv, blocks, blocks_per_seq, lens,
                          out, lse, ws, ws_bytes, stream) -> int:
-    return _lib().bitlinear_paged_attn(plan, q, q_dtype, q_tok, q_head, scale, kv, blocks,
+    return _lib().bitlinear_paged_attn(plan, q, q_dtype, q_tok, q_head, scale,
+                                       None if kv is None else ctypes.byref(kv), blocks,
                                        blocks_per_seq, lens, out, lse, ws, ws_bytes, stream)
 
 
@@ -381,8 +389,8 @@ def rope(xs, pos, table, interleaved: bool = False, inverse: bool = False, dtype
             strides.append((xt, xh, yt, yh, n))
     if outs is None:
         outs = [x.new_empty(x.shape, dtype=dtype) for x in xs]
-    arr = (BlRopeDesc * len(xs))(*[(x.data_ptr(), y.data_ptr(), *s)
-                                   for x, y, s in zip(xs, outs, strides)])
+    arr = b"".join([_ROPE.pack(x.data_ptr(), y.data_ptr(), *s)
+                    for x, y, s in zip(xs, outs, strides)])
     _check(_lib().bitlinear_rope(arr, len(xs), T, D, R, interleaved, inverse, xd, yd, pos.data_ptr(),
                                  table.data_ptr(), positions, _stream(ix)), "bitlinear_rope")
     return outs
@@ -453,13 +461,13 @@ def rope_append(q, k, v, pos, table, k_cache, v_cache, blocks, seq=None, k_scale
         raise ValueError("heads or head dimension of out, k, v and the cache do not fit")
     if out is None:
         out = q.new_empty(q.shape, dtype=dtype)
-    arr = (BlRopeDesc * 3)((q.data_ptr(), out.data_ptr(), qt, qh, ot, oh, nq),
-                           (k.data_ptr(), None, kt, kh, 0, 0, nk),
-                           (v.data_ptr(), None, vt, vh, 0, 0, nv))
+    arr = _ROPE3.pack(q.data_ptr(), out.data_ptr(), qt, qh, ot, oh, nq, k.data_ptr(), 0, kt, kh, 0, 0,
+                      nk, v.data_ptr(), 0, vt, vh, 0, 0, nv)
     _check(_lib().bitlinear_rope_append(
         arr, T, R, interleaved, xd, qd, pos.data_ptr(), _ptr(seq), blocks.data_ptr(), seqs, per,
         table.data_ptr(), positions,
-        BlKvCache(k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale), _ptr(v_scale), *cache),
+        _KV.pack(k_cache.data_ptr(), v_cache.data_ptr(), 0 if k_scale is None else k_scale.data_ptr(),
+                 0 if v_scale is None else v_scale.data_ptr(), *cache),
         _stream(ix)), "bitlinear_rope_append")
     return out
 
@@ -515,7 +523,9 @@ class PagedAttn:
             out = q.new_empty(shape)
         _check(_lib().bitlinear_paged_attn(
             self.plan, q.data_ptr(), qd, qt, qh, self.scale if scale is None else scale,
-            BlKvCache(k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale), _ptr(v_scale), *cache),
+            _KV.pack(k_cache.data_ptr(), v_cache.data_ptr(),
+                     0 if k_scale is None else k_scale.data_ptr(),
+                     0 if v_scale is None else v_scale.data_ptr(), *cache),
             blocks.data_ptr(), blocks.shape[1], lens.data_ptr(), out.data_ptr(), _ptr(lse),
             ws.data_ptr(), ws.numel(), _stream(ix)), "bitlinear_paged_attn")
         return out if lse is None else (out, lse)

@@ -139,24 +139,27 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_quant_kernel(NormA
   }
 }
 
-template <bool XBF, int RES, int W>
-void launch_norm_w(const NormArgs& a, hipStream_t s) {
-  const int per = (a.K / 8 + 64 * W - 1) / (64 * W);   // pieces per lane
+template <bool XBF, int RES, int W, int P>
+void launch_norm_wp(const NormArgs& a, hipStream_t s) {
   constexpr int RPB = W == 1 ? 4 : 1;
   const dim3 grid((unsigned)((a.T + RPB - 1) / RPB)), block(W == 1 ? 256 : 64 * W);
-  const size_t lds = a.lift_M ? (size_t)RPB * a.K : 0;
-  if (per <= 1) norm_quant_kernel<XBF, RES, W, 1><<<grid, block, lds, s>>>(a);
-  else if (per <= 2) norm_quant_kernel<XBF, RES, W, 2><<<grid, block, lds, s>>>(a);
-  else if (per <= 4) norm_quant_kernel<XBF, RES, W, 4><<<grid, block, lds, s>>>(a);
-  else if constexpr (W == 1) norm_quant_kernel<XBF, RES, W, 8><<<grid, block, lds, s>>>(a);
+  norm_quant_kernel<XBF, RES, W, P><<<grid, block, a.lift_M ? (size_t)RPB * a.K : 0, s>>>(a);
 }
 
+// Waves per row.  Many rows: the fewest that leave a lane two pieces (8192 x 3200: four waves 44.6 us,
+// two 49.5, one 54.2, sixteen 62.1).  Few rows, where latency counts: one piece per lane, up to eight
+// waves (1 x 2560: eight 3.07 us, four 3.27, sixteen 3.60; 1 x 8192: eight 3.80, sixteen 4.13).
 template <bool XBF, int RES>
 hipError_t launch_norm_t(const NormArgs& a, hipStream_t s) {
-  const int pieces = a.K / 8;
-  if (pieces <= 512 && a.T >= 1024) launch_norm_w<XBF, RES, 1>(a, s);
-  else if (pieces <= 1024) launch_norm_w<XBF, RES, 4>(a, s);
-  else launch_norm_w<XBF, RES, 16>(a, s);
+  const int pieces = a.K / 8, most = a.T < 1024 ? 64 : 128;   // pieces per wave
+  if (pieces <= 64) launch_norm_wp<XBF, RES, 1, 1>(a, s);
+  else if (pieces <= most) launch_norm_wp<XBF, RES, 1, 2>(a, s);
+  else if (pieces <= 256) launch_norm_wp<XBF, RES, 4, 1>(a, s);
+  else if (pieces <= 4 * most) launch_norm_wp<XBF, RES, 4, 2>(a, s);
+  else if (pieces <= 512) launch_norm_wp<XBF, RES, 8, 1>(a, s);
+  else if (pieces <= 1024) launch_norm_wp<XBF, RES, 8, 2>(a, s);
+  else if (pieces <= 2048) launch_norm_wp<XBF, RES, 16, 2>(a, s);
+  else launch_norm_wp<XBF, RES, 16, 4>(a, s);
   return hipGetLastError();
 }
 
@@ -279,26 +282,23 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdArgs a) {
   }
 }
 
-// dw[k] = sum over blocks of part[block][k]: 16 lanes of four columns, 16 row groups, joined in LDS
+// dw[k] = sum over blocks of part[block][k]: 8 lanes of four columns, 32 row groups, joined in LDS
 __global__ __launch_bounds__(256) void norm_dw_kernel(const float* __restrict__ part, int blocks,
                                                       int K, float* __restrict__ dw) {
-  __shared__ float4 red[16][16];
-  const int c = threadIdx.x & 15, r = threadIdx.x >> 4;
-  const int k = (blockIdx.x * 16 + c) * 4;
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int C = 8, R = 32;
+  __shared__ v4f red[R][C];
+  const int c = threadIdx.x % C, r = threadIdx.x / C;
+  const int k = (blockIdx.x * C + c) * 4;
+  v4f s = v4f{0.f, 0.f, 0.f, 0.f};
   if (k < K)
-    for (int b = r; b < blocks; b += 16) {
-      const float4 v = *(const float4*)(part + (size_t)b * K + k);
-      s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
-    }
+#pragma unroll 8
+    for (int b = r; b < blocks; b += R) s += *(const v4f*)(part + (size_t)b * K + k);
   red[r][c] = s;
   __syncthreads();
   if (r == 0 && k < K) {
-    for (int i = 1; i < 16; ++i) {
-      const float4 v = red[i][c];
-      s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
-    }
-    *(float4*)(dw + k) = s;
+#pragma unroll
+    for (int i = 1; i < R; ++i) s += red[i][c];
+    *(v4f*)(dw + k) = s;
   }
 }
 
@@ -315,7 +315,7 @@ hipError_t launch_bwd_t(const NormBwdArgs& a, hipStream_t s) {
   else norm_bwd_kernel<GBF, HBF, OBF, 16, 4><<<grid, block, lds, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.dw) return e;
-  norm_dw_kernel<<<dim3((unsigned)((a.K + 63) / 64)), 256, 0, s>>>(a.part, a.blocks, a.K, a.dw);
+  norm_dw_kernel<<<dim3((unsigned)((a.K + 31) / 32)), 256, 0, s>>>(a.part, a.blocks, a.K, a.dw);
   return hipGetLastError();
 }
 

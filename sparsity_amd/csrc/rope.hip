@@ -128,6 +128,21 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
   const int64_t t = blockIdx.x;
   const bool on = 8 * i < a.D;
   const Item it = item_of(i, a.R, a.interleaved);
+  // a head's elements are asked for one head ahead, the first before the position and its cosines
+  auto tensor = [&](int hd) {
+    return APPEND ? (hd >= a.t[1].head0) + (hd >= a.t[2].head0) : tensor_of(a, hd);
+  };
+  auto fetch = [&](int hd, float (&u)[4], float (&w)[4]) {
+    if (!on || hd >= a.heads) return;
+    const RopeTensor& x = a.t[tensor(hd)];
+    const int64_t r = t * x.x_tok + (hd - x.head0) * x.x_head;
+    load4<XBF>(x.x, r + it.e0, u);
+    load4<XBF>(x.x, r + it.e1, w);
+  };
+  const int step = gridDim.y * HPB;
+  int hd = blockIdx.y * HPB + slot;
+  float u[4] = {}, w[4] = {}, un[4] = {}, wn[4] = {};
+  fetch(hd, un, wn);
   const int64_t pos = a.pos[t];
   float c[4], s[4];
   load_cs(a, pos, on ? it.pair0 : -1, c, s);
@@ -143,16 +158,13 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
       if (page >= a.kv.pages) page = -1;    // not a page of this cache: nothing is written
     }
   }
-  for (int hd = blockIdx.y * HPB + slot; hd < a.heads; hd += gridDim.y * HPB) {
-    const int m = APPEND ? (hd >= a.t[1].head0) + (hd >= a.t[2].head0) : tensor_of(a, hd);
+  for (; hd < a.heads; hd += step) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) { u[k] = un[k]; w[k] = wn[k]; }
+    fetch(hd + step, un, wn);
+    const int m = tensor(hd);
     const RopeTensor& x = a.t[m];
     const int h = hd - x.head0;
-    float u[4] = {}, w[4] = {};
-    if (on) {
-      const int64_t r = t * x.x_tok + h * x.x_head;
-      load4<XBF>(x.x, r + it.e0, u);
-      load4<XBF>(x.x, r + it.e1, w);
-    }
     if ((!APPEND || m < 2) && it.pair0 >= 0) rotate(u, w, c, s, a.interleaved);
     if (!APPEND || m == 0) {
       if (!known || pad) {

@@ -34,7 +34,8 @@ def _f32(t):
 
 
 SIZES = [(1, 8), (1, 2560), (3, 512), (5, 520), (2, 4104), (1030, 264), (1025, 3200), (2, 8200),
-         (1, 16384), (2, 32768), (7, 6912)]
+         (1, 16384), (2, 32768), (7, 6912),
+         (1029, 1000), (1026, 4104)]
 
 
 @pytest.mark.parametrize("T,K", SIZES)
