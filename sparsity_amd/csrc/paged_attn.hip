@@ -125,6 +125,14 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
   return (int64_t)((uint64_t)hi << 32 | lo);
 }
 
+// The same value, which the compiler may not compute ahead of this place: what the end of a segment
+// derives from the thread's index would otherwise sit in registers all through the loop over keys
+// (256 of them and 112 bytes of spills at D = 128, against 232 and none).
+__device__ __forceinline__ int here(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 // Live positions of a sequence: [first, len).
 struct Span {
   int64_t first, len;
@@ -230,31 +238,25 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT)) void paged_attn_kernel(A
     const int32_t page0 = page_of(0);
     int32_t next = page_of(1);
 
-    // queries: operand c, lane (g, n): elements of head n (zero past the live heads and past D)
-    bf16x8 qf[QS][KC];
+    // queries, as they lie in memory: operand c of lane (g, n), eight elements of head n (zero past the
+    // live heads and past D)
+    uint4 qraw[KC][QF ? 2 : 1];
 #pragma unroll
     for (int c = 0; c < KC; ++c) {
       // the int8 cache reads 16 elements per lane, so its steps come in pairs of adjacent eights
       const int d = I8 ? 64 * (c / 2) + 16 * g + 8 * (c & 1) : 32 * c + 8 * g;
-      float v[8] = {};
+#pragma unroll
+      for (int e = 0; e < (QF ? 2 : 1); ++e) qraw[c][e] = make_uint4(0, 0, 0, 0);
       if (n < rows && d < D) {
-        const int64_t o = sq * a.q_tok + (int64_t)(hq0 + n) * a.q_head + d;
-        load_f8<!QF>(a.q, o, v);
-      }
+        const char* p = (const char*)a.q + (sq * a.q_tok + (int64_t)(hq0 + n) * a.q_head + d) * (QF ? 4 : 2);
 #pragma unroll
-      for (int t = 0; t < QS; ++t) {
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
-          v[2 * j] -= bf16_lo(w[j]);
-          v[2 * j + 1] -= bf16_hi(w[j]);
-        }
-        qf[t][c] = frag(w[0], w[1], w[2], w[3]);
+        for (int e = 0; e < (QF ? 2 : 1); ++e) qraw[c][e] = ((const uint4*)p)[e];
       }
     }
 
-    float scl[2] = {0.f, 0.f};                // scales of the lane's key and value, on their way to LDS
+    // scales of the lane's key and value, on their way to LDS, and whether the key is live
+    float scl[2] = {0.f, 0.f};
+    bool scl_ok = false;
     auto put_rows = [&](int grpi, int32_t page) {
       const int64_t t = key_of(grpi);
       const int off = (int)((uint32_t)t % (uint32_t)ps);
@@ -263,9 +265,9 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT)) void paged_attn_kernel(A
           ok ? ((int64_t)page * a.kv.page_stride + (int64_t)off * a.kv.tok_stride) * EB : -1;
       if constexpr (I8) {
         const int64_t sr = ok ? ((int64_t)page * a.kv.heads + hk) * ps + off : 0;
-        const float x = a.kv.k_scale[sr], y = a.kv.v_scale[sr];
-        scl[0] = ok ? x : 0.f;
-        scl[1] = ok ? y : 0.f;                          // times a masked weight of 0
+        scl[0] = a.kv.k_scale[sr];
+        scl[1] = a.kv.v_scale[sr];
+        scl_ok = ok;
       }
       // LDS serves a wave's accesses in order; only the compiler has to keep them so
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -327,12 +329,39 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT)) void paged_attn_kernel(A
       put_rows(0, page0);
       load_k(0);
       load_v(0);
+    }
+    // the queries as bf16 terms, each what the ones before leave
+    bf16x8 qf[QS][KC];
+#pragma unroll
+    for (int c = 0; c < KC; ++c) {
+      if constexpr (QF) {
+        float v[8];
+        const uint4 lo = qraw[c][0], hi = qraw[c][1];
+        const uint32_t bits[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(bits[j]);
+#pragma unroll
+        for (int t = 0; t < QS; ++t) {
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+            v[2 * j] -= bf16_lo(w[j]);
+            v[2 * j + 1] -= bf16_hi(w[j]);
+          }
+          qf[t][c] = frag(w[0], w[1], w[2], w[3]);
+        }
+      } else {
+        qf[0][c] = __builtin_bit_cast(bf16x8, qraw[c][0]);
+      }
+    }
+    if (groups > 0) {
       for (int i = 0; i < groups; ++i) {
         const bool more = i + 1 < groups;
         if constexpr (I8) {
           __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
           sring[wave][0][lane] = scl[0];
-          sring[wave][1][lane] = scl[1];
+          sring[wave][1][lane] = scl_ok ? scl[1] : 0.f;   // times a masked weight of 0
           __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
           __builtin_amdgcn_wave_barrier();
         }
@@ -444,6 +473,7 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT)) void paged_attn_kernel(A
     l += __shfl_xor(l, 16, 64);
     l += __shfl_xor(l, 32, 64);
 
+    const int tid = here(threadIdx.x), tl = tid & 63, tw = tid >> 6;
     // join the waves.  Lane (g, n) holds elements VE (4g + r) + j of head n.
     if (n < rows) {
       if (g == 0) { sm_m[wave][n] = m; sm_l[wave][n] = l; }
@@ -466,7 +496,7 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT)) void paged_attn_kernel(A
     const int64_t place = 2 * (int64_t)blockIdx.x + (owner0 == (int64_t)blockIdx.x);
     float* part = a.part + place * prows * D;   // [prows][D]
     float* ml = a.ml + place * 2 * kQ;          // [2][kQ]
-    for (int e = threadIdx.x; e < rows * D; e += 64 * kWaves) {
+    for (int e = tid; e < rows * D; e += 64 * kWaves) {
       const int h = e / D, d = e - h * D;
       float top = sm_m[0][h];
 #pragma unroll
@@ -495,7 +525,7 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT)) void paged_attn_kernel(A
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
       __builtin_amdgcn_s_waitcnt(waitcnt_imm(0));
       __syncthreads();
-      if (threadIdx.x == 0) {
+      if (tid == 0) {
         last_sh = __hip_atomic_fetch_add(a.ticket + grp, 1u, __ATOMIC_RELAXED,
                                          __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)active - 1;
         if (last_sh)                            // ready for the next launch
@@ -519,7 +549,7 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT)) void paged_attn_kernel(A
         };
         // thread (i, row): runs i, i + 16, ... of a row, the first kHeld of them in registers
         constexpr int kHeld = 4, kAhead = 4;
-        const int hrow = threadIdx.x & (kQ - 1), i0 = threadIdx.x / kQ;
+        const int hrow = tid & (kQ - 1), i0 = tid / kQ;
         float hm[kHeld], hl[kHeld];
 #pragma unroll
         for (int k = 0; k < kHeld; ++k) {
@@ -532,9 +562,9 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT)) void paged_attn_kernel(A
         v4f ahead[kAhead][2];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-          const int s = min(wave + kWaves * k, active - 1);
-          ahead[k][0] = column(s, 4 * lane);
-          ahead[k][1] = column(s, 256 + 4 * lane);
+          const int s = min(tw + kWaves * k, active - 1);
+          ahead[k][0] = column(s, 4 * tl);
+          ahead[k][1] = column(s, 256 + 4 * tl);
         }
         float top = -INFINITY, den = 0.f;
 #pragma unroll
@@ -545,7 +575,7 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT)) void paged_attn_kernel(A
           v = op(v, __shfl_xor(v, 16, 64));
           v = op(v, __shfl_xor(v, 32, 64));
           __syncthreads();
-          if (lane < kQ) sums[kQ * wave + lane] = v;
+          if (tl < kQ) sums[kQ * tw + tl] = v;
           __syncthreads();
 #pragma unroll
           for (int w = 0; w < kWaves; ++w) v = w ? op(v, sums[kQ * w + hrow]) : sums[hrow];
@@ -554,7 +584,7 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT)) void paged_attn_kernel(A
         top = over_rows(top, [](float x, float y) { return fmaxf(x, y); });
 #pragma unroll 1
         for (int j = 0; j < cols; j += kCols) {
-          const int e = j + 4 * lane;
+          const int e = j + 4 * tl;
           const int h0 = min(e / D, rows - 1), h1 = min((e + 256) / D, rows - 1);   // D % 8 == 0: one row per four
           v4f num[2] = {v4f{0.f, 0.f, 0.f, 0.f}, v4f{0.f, 0.f, 0.f, 0.f}};
 #pragma unroll 1
@@ -583,13 +613,13 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT)) void paged_attn_kernel(A
             }
             const float* w0r = wt + h0 * at;
             const float* w1r = wt + h1 * at;
-            int s = wave;
+            int s = tw;
             if (j == 0 && s0 == 0) {
 #pragma unroll
               for (int k = 0; k < kAhead; ++k, s += kWaves)
                 if (s < ns) { num[0] += w0r[s] * ahead[k][0]; num[1] += w1r[s] * ahead[k][1]; }
             }
-#pragma unroll 8
+#pragma unroll 4
             for (; s < ns; s += kWaves) {
               const v4f v0 = column(s0 + s, e), v1 = column(s0 + s, e + 256);
               num[0] += w0r[s] * v0;
@@ -598,20 +628,20 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT)) void paged_attn_kernel(A
           }
           if (j == 0) {
             den = over_rows(den, [](float x, float y) { return x + y; });
-            if (threadIdx.x < kQ) { sm_l[0][hrow] = den; sm_m[0][hrow] = top; }
+            if (tid < kQ) { sm_l[0][hrow] = den; sm_m[0][hrow] = top; }
             __syncthreads();                      // sums is free again
           }
-          *(v4f*)(sums + kCols * wave + 4 * lane) = num[0];
-          *(v4f*)(sums + kCols * wave + 256 + 4 * lane) = num[1];
+          *(v4f*)(sums + kCols * tw + 4 * tl) = num[0];
+          *(v4f*)(sums + kCols * tw + 256 + 4 * tl) = num[1];
           __syncthreads();
 #pragma unroll
           for (int u = 0; u < kCols; u += 64 * kWaves) {
-            const int c = j + u + threadIdx.x;
+            const int c = j + u + tid;
             if (c < cols) {
               const int h = c / D;
               float nsum = 0.f;
 #pragma unroll
-              for (int w = 0; w < kWaves; ++w) nsum += sums[kCols * w + u + threadIdx.x];
+              for (int w = 0; w < kWaves; ++w) nsum += sums[kCols * w + u + tid];
               finish(h, c - h * D, nsum, sm_l[0][h], sm_m[0][h]);
             }
           }
