@@ -530,6 +530,8 @@ int bitlinear_bwd_group(const void* table, const bl_bwd_group_plan* plan, void* 
  * in front of a projection (BitNet b1.58 page, "The mechanism": a norm precedes every activation
  * quantization), rotary positions, a paged key-value cache and the decode attention over it.
  *
+ * T < 2^22 tokens in each of these calls.
+ *
  * bitlinear_norm_quant, per token t:
  *   h    = x + res rounded once to res_dtype (res NULL: h is x, and the h argument must be NULL)
  *   rstd = fl32(1 / sqrt(sum(h^2) / K + eps)): squares in fp32, their sum and the root in fp64
@@ -649,7 +651,8 @@ int bitlinear_paged_attn_plan(int64_t B, int64_t q_heads, int64_t kv_heads, int6
 
 /* q is q_dtype (F32 or BF16): head h of sequence b at b * q_tok + h * q_head (16-byte aligned,
  * strides multiples of 8); out is q_dtype [B][q_heads][head_dim], lse_opt fp32 [B][q_heads] or
- * NULL. */
+ * NULL.  out, lse_opt and ws may overlap no input and not each other (BL_EINVAL; a strided q counts
+ * from its first to its last row). */
 int bitlinear_paged_attn(const bl_attn_plan* plan, const void* q, int q_dtype, int64_t q_tok,
                          int64_t q_head, float scale, const bl_kv_cache* kv, const int32_t* blocks,
                          int64_t blocks_per_seq, const int32_t* lens, void* out, float* lse_opt,

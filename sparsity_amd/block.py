@@ -209,7 +209,7 @@ def norm_quant(x, weight=None, residual=None, eps: float = 1e-6, lift_M: int = 0
         _buf(weight, torch.float32, K, ix, "weight")
     ke = K // lift_M * (2 * lift_M - 4) if lift_M else K
     if out is None:
-        xq = x.new_empty((T, ke), dtype=torch.int8)
+        xq = x.new_empty((T, ke), dtype=torch.int8) if lift_M else torch.empty_like(x, dtype=torch.int8)
         scale = x.new_empty(T, dtype=torch.float32)
         if residual is not None:
             h = torch.empty_like(residual)
@@ -257,7 +257,7 @@ def norm_quant_bwd(dn, h, rstd, weight=None, dres=None, dtype=None, want_dw: boo
     if dres is not None:
         _rows(dres, shape, ix, "dres", dtype)
     if out is None:
-        dh = dn.new_empty(shape, dtype=dtype)
+        dh = torch.empty_like(dn, dtype=dtype)
         dw = dn.new_empty(K, dtype=torch.float32) if want_dw else None
     else:
         dh, dw = out
@@ -347,6 +347,12 @@ def _heads(t, T: int, D: int, index: int, name: str, dtype):
     return s[0], s[1], shape[1]
 
 
+def _like(t, dtype):
+    """A new contiguous tensor of t's shape."""
+    import torch
+    return torch.empty_like(t, dtype=dtype) if t.is_contiguous() else t.new_empty(t.shape, dtype=dtype)
+
+
 def _table(table, index: int):
     import torch
     shape = table.shape
@@ -388,7 +394,7 @@ def rope(xs, pos, table, interleaved: bool = False, inverse: bool = False, dtype
                 raise ValueError("outs: heads differ from xs")
             strides.append((xt, xh, yt, yh, n))
     if outs is None:
-        outs = [x.new_empty(x.shape, dtype=dtype) for x in xs]
+        outs = [_like(x, dtype) for x in xs]
     arr = b"".join([_ROPE.pack(x.data_ptr(), y.data_ptr(), *s)
                     for x, y, s in zip(xs, outs, strides)])
     _check(_lib().bitlinear_rope(arr, len(xs), T, D, R, interleaved, inverse, xd, yd, pos.data_ptr(),
@@ -460,7 +466,7 @@ def rope_append(q, k, v, pos, table, k_cache, v_cache, blocks, seq=None, k_scale
     if no != nq or nk != heads or nv != heads or D != cache[6]:
         raise ValueError("heads or head dimension of out, k, v and the cache do not fit")
     if out is None:
-        out = q.new_empty(q.shape, dtype=dtype)
+        out = _like(q, dtype)
     arr = _ROPE3.pack(q.data_ptr(), out.data_ptr(), qt, qh, ot, oh, nq, k.data_ptr(), 0, kt, kh, 0, 0,
                       nk, v.data_ptr(), 0, vt, vh, 0, 0, nv)
     _check(_lib().bitlinear_rope_append(
@@ -477,7 +483,8 @@ class PagedAttn:
     sizes the launch and holds its workspace; calling it attends one query token per sequence.
 
     max_len bounds the sequences' lengths (longer ones only run on too few workgroups); window > 0
-    attends the last ``window`` positions only.  Calls of one object are ordered on one stream.
+    attends the last ``window`` positions only.  Calls of one object are ordered on one stream.  Build
+    it outside any graph capture (it waits for its workspace).
     """
 
     def __init__(self, B: int, q_heads: int, heads: int, D: int, page_size: int, max_len: int,
@@ -489,6 +496,8 @@ class PagedAttn:
         self.shape = torch.Size((B, q_heads, D))
         self.scale = D ** -0.5
         self.ws = torch.zeros(self.plan.ws_bytes, dtype=torch.uint8, device=device)
+        if self.ws.is_cuda:                 # zeroed before a call on any stream
+            torch.cuda.current_stream(self.ws.device).synchronize()
 
     def __call__(self, q, k_cache, v_cache, blocks, lens, scale=None, k_scale=None, v_scale=None,
                  out=None, want_lse: bool = False, lse=None):
@@ -520,7 +529,7 @@ class PagedAttn:
         elif want_lse:
             lse = q.new_empty((B, heads), dtype=torch.float32)
         if out is None:
-            out = q.new_empty(shape)
+            out = _like(q, dtype)
         _check(_lib().bitlinear_paged_attn(
             self.plan, q.data_ptr(), qd, qt, qh, self.scale if scale is None else scale,
             _KV.pack(k_cache.data_ptr(), v_cache.data_ptr(),

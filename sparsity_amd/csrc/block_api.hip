@@ -27,8 +27,9 @@ bool overlap(const Span& a, const Span& b) {
   return x < y + b.bytes && y < x + a.bytes;
 }
 
-// [T][K] sizes whose element count stays addressable and whose rows fit a grid.
-bool rows_ok(int64_t T, int64_t K) { return T >= 0 && T <= INT32_MAX && K >= 8 && K % 8 == 0; }
+// A launch holds fewer than 2^32 threads, and a row takes up to 1024 of them.
+constexpr int64_t kMaxTokens = ((int64_t)1 << 22) - 1;
+bool rows_ok(int64_t T, int64_t K) { return T >= 0 && T <= kMaxTokens && K >= 8 && K % 8 == 0; }
 
 }  // namespace
 
@@ -109,7 +110,7 @@ int bitlinear_norm_quant_bwd(const void* dn, int dn_dtype, const void* h, int h_
 
 int bitlinear_rope_table(const double* freq, int64_t half, int64_t positions, double mscale,
                          float* table, void* stream) {
-  if (half < 1 || half > 128 || positions < 0 || positions > INT32_MAX) return BL_EINVAL;
+  if (half < 1 || half > 128 || positions < 0 || positions > ((int64_t)1 << 31) / half) return BL_EINVAL;
   if (!isfinite(mscale)) return BL_EINVAL;
   if (positions == 0) return BL_OK;
   if (!aligned(freq, 8) || !aligned(table, 16)) return BL_EINVAL;
@@ -175,7 +176,8 @@ int rope_tensors(const bl_rope_desc* d, int64_t count, int64_t T, int64_t D, int
   return BL_OK;
 }
 
-int check_cache(const bl_kv_cache* kv, bool scales) {
+// Checks a cache; *extent: elements from the start of k (and of v) to the end of its last row.
+int check_cache(const bl_kv_cache* kv, int64_t* extent) {
   if (!kv) return BL_EINVAL;
   if (kv->dtype != BL_DTYPE_BF16 && kv->dtype != BL_DTYPE_I8) return BL_ENOTSUP;
   const int64_t q = kv->dtype == BL_DTYPE_I8 ? 16 : 8;
@@ -197,8 +199,8 @@ int check_cache(const bl_kv_cache* kv, bool scales) {
     span += (x.count - 1) * x.stride;
   }
   if (!aligned(kv->k, 16) || !aligned(kv->v, 16)) return BL_EINVAL;
-  if (scales && kv->dtype == BL_DTYPE_I8 && (!aligned(kv->k_scale, 4) || !aligned(kv->v_scale, 4)))
-    return BL_EINVAL;
+  if (kv->dtype == BL_DTYPE_I8 && (!aligned(kv->k_scale, 4) || !aligned(kv->v_scale, 4))) return BL_EINVAL;
+  *extent = span;
   return BL_OK;
 }
 
@@ -211,7 +213,7 @@ int bitlinear_rope(const bl_rope_desc* descs, int64_t count, int64_t T, int64_t 
                    const float* table, int64_t positions, void* stream) {
   if (!float_dtype(x_dtype) || !float_dtype(y_dtype)) return BL_ENOTSUP;
   if (!descs || count < 1 || count > bl::kRopeMax) return BL_EINVAL;
-  if (T < 0 || T > INT32_MAX || D < 1 || D > 256 || R < 2 || R > D || R % 2 || positions < 0 ||
+  if (T < 0 || T > kMaxTokens || D < 1 || D > 256 || R < 2 || R > D || R % 2 || positions < 0 ||
       positions > INT32_MAX)
     return BL_EINVAL;
   bl::RopeArgs a = {};
@@ -232,10 +234,11 @@ int bitlinear_rope_append(const bl_rope_desc* qkv, int64_t T, int64_t R, int int
                           const float* table, int64_t positions, const bl_kv_cache* kv,
                           void* stream) {
   if (!float_dtype(x_dtype) || !float_dtype(q_dtype)) return BL_ENOTSUP;
-  const int cs = check_cache(kv, true);
+  int64_t extent = 0;
+  const int cs = check_cache(kv, &extent);
   if (cs != BL_OK) return cs;
   const int64_t D = kv->head_dim;
-  if (!qkv || T < 0 || T > INT32_MAX || R < 8 || R > D || R % 8 || positions < 0 ||
+  if (!qkv || T < 0 || T > kMaxTokens || R < 8 || R > D || R % 8 || positions < 0 ||
       positions > INT32_MAX || seqs < 1 || blocks_per_seq < 1 || seqs > INT32_MAX ||
       blocks_per_seq > INT32_MAX)
     return BL_EINVAL;
@@ -310,7 +313,8 @@ int bitlinear_paged_attn(const bl_attn_plan* plan, const void* q, int q_dtype, i
                                            plan->max_len, plan->window, &p);
   if (st != BL_OK) return st;
   if (p.blocks != plan->blocks) return BL_EINVAL;   // not this build's plan
-  const int cs = check_cache(kv, true);
+  int64_t extent = 0;
+  const int cs = check_cache(kv, &extent);
   if (cs != BL_OK) return cs;
   if (kv->heads != p.kv_heads || kv->head_dim != p.head_dim) return BL_EINVAL;
   if (!isfinite(scale) || blocks_per_seq < 0 || blocks_per_seq > INT32_MAX) return BL_EINVAL;
@@ -326,6 +330,13 @@ int bitlinear_paged_attn(const bl_attn_plan* plan, const void* q, int q_dtype, i
   const Span o = {out, (uint64_t)(rows * p.head_dim * esize(q_dtype))}, l = {lse_opt, (uint64_t)rows * 4},
              s = {ws, p.ws_bytes};
   if (overlap(o, l) || overlap(o, s) || overlap(l, s)) return BL_EINVAL;
+  const uint64_t kvb = (uint64_t)extent * esize(kv->dtype);
+  const uint64_t scb = kv->dtype == BL_DTYPE_I8 ? (uint64_t)kv->pages * kv->heads * kv->page_size * 4 : 0;
+  const Span in[7] = {{q, (uint64_t)((p.B - 1) * q_tok + (p.q_heads - 1) * q_head + p.head_dim) * esize(q_dtype)},
+                      {kv->k, kvb}, {kv->v, kvb}, {kv->k_scale, scb}, {kv->v_scale, scb},
+                      {blocks, (uint64_t)p.B * blocks_per_seq * 4}, {lens, (uint64_t)p.B * 4}};
+  for (const Span& i : in)
+    if (overlap(i, o) || overlap(i, l) || overlap(i, s)) return BL_EINVAL;
   bl::AttnArgs a = {};
   a.kv = *kv;
   a.q = q;

@@ -27,7 +27,8 @@ def _norm(**kw):
 
 @pytest.mark.parametrize("kw,want", [
     (dict(xd=2), ENOTSUP), (dict(rd=7), ENOTSUP), (dict(K=252), EINVAL), (dict(K=0), EINVAL),
-    (dict(K=32776), ENOTSUP), (dict(T=-1), EINVAL), (dict(T=1 << 31), EINVAL), (dict(eps=0.0), EINVAL),
+    (dict(K=32776), ENOTSUP), (dict(T=-1), EINVAL), (dict(T=1 << 31), EINVAL), (dict(T=1 << 22), EINVAL),
+    (dict(eps=0.0), EINVAL),
     (dict(eps=-1.0), EINVAL), (dict(eps=math.nan), EINVAL), (dict(eps=math.inf), EINVAL),
     (dict(lift=4), EINVAL), (dict(lift=7), EINVAL), (dict(lift=6, K=256), EINVAL), (dict(lift=18), EINVAL),
     (dict(x=None), EINVAL), (dict(x=P + 8), EINVAL), (dict(xq=None), EINVAL), (dict(xq=P + 4 * SLOT + 4), EINVAL),
@@ -85,7 +86,7 @@ def _rope(descs=None, **kw):
 
 @pytest.mark.parametrize("kw,want", [
     (dict(xd=2), ENOTSUP), (dict(yd=3), ENOTSUP), (dict(D=0), EINVAL), (dict(D=257), EINVAL), (dict(R=3), EINVAL),
-    (dict(R=0), EINVAL), (dict(R=130), EINVAL), (dict(T=-1), EINVAL), (dict(n=-1), EINVAL), (dict(pos=None), EINVAL),
+    (dict(R=0), EINVAL), (dict(R=130), EINVAL), (dict(T=-1), EINVAL), (dict(T=1 << 22), EINVAL), (dict(n=-1), EINVAL), (dict(pos=None), EINVAL),
     (dict(pos=P + 2), EINVAL), (dict(table=None), EINVAL), (dict(table=P + 8), EINVAL),
     (dict(descs=[]), EINVAL), (dict(descs=[_desc(i) for i in range(5)]), EINVAL),
     (dict(descs=[_desc(heads=0)]), EINVAL), (dict(descs=[_desc(x=None)]), EINVAL), (dict(descs=[_desc(y=None)]), EINVAL),
@@ -103,6 +104,7 @@ def test_rope_table_rejects():
     f = lambda freq=P, half=32, n=8, m=1.0, t=P + SLOT: K.bitlinear_rope_table(freq, half, n, m, t, None)
     assert f(half=0) == f(half=129) == f(n=-1) == f(m=math.nan) == f(freq=None) == f(t=None) == EINVAL
     assert f(freq=P + 4) == f(t=P + SLOT + 8) == f(t=P) == EINVAL
+    assert f(n=(1 << 26) + 1) == EINVAL          # 2^31 entries and more
     assert f(n=0) == 0
 
 
@@ -169,7 +171,8 @@ def _changed(**kw):
     (dict(q_head=-128), EINVAL), (dict(scale=math.inf), EINVAL), (dict(per=-1), EINVAL), (dict(blocks=None), EINVAL),
     (dict(lens=None), EINVAL), (dict(out=None), EINVAL), (dict(lse=P + 2), EINVAL), (dict(ws=None), EINVAL),
     (dict(ws=P + 3 * SLOT + 128), EINVAL), (dict(wsb=255), ENOSPC), (dict(out=P + 3 * SLOT), EINVAL),
-    (dict(lse=P + SLOT), EINVAL), (dict(lse=P + 3 * SLOT), EINVAL), (dict(kv=_kv(heads=4)), EINVAL),
+    (dict(lse=P + SLOT), EINVAL), (dict(lse=P + 3 * SLOT), EINVAL),
+    (dict(out=P), EINVAL), (dict(lse=P + 8), EINVAL), (dict(out=P + 30 * SLOT), EINVAL), (dict(ws=P + 40 * SLOT), EINVAL), (dict(kv=_kv(heads=4)), EINVAL),
     (dict(kv=_kv(dim=64)), EINVAL), (dict(plan=_changed(blocks=99)), EINVAL), (dict(plan=_changed(blocks=0)), EINVAL),
     (dict(plan=_changed(B=-1)), EINVAL), (dict(plan=_changed(q_heads=21)), EINVAL)])
 def test_attention_rejects(kw, want):
