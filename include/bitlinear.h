@@ -554,7 +554,7 @@ int bitlinear_norm_quant(const void* x, int x_dtype, const void* res, int res_dt
  * Sums are fp32 in a fixed order: results do not vary from run to run.  dh may be dres itself, or
  * dn where the types agree.  ws: bitlinear_norm_quant_bwd_workspace_bytes of device scratch (16-byte
  * aligned; contents on entry irrelevant), not needed (NULL, 0) without dw.  T == 0 writes dw = 0.
- * One launch, and a second one for dw. */
+ * One launch, and a second one for dw unless the rows are few. */
 int bitlinear_norm_quant_bwd_workspace_bytes(int64_t T, int64_t K, size_t* ws_bytes);
 int bitlinear_norm_quant_bwd(const void* dn, int dn_dtype, const void* h, int h_dtype,
                              const float* rstd, const float* w, const void* dres, void* dh,
@@ -614,8 +614,7 @@ typedef struct bl_kv_cache {
  * the value rounded once; I8 caches what act_quant_i8 writes for them per token and head.  Nothing
  * is written for a token whose position is below 0 or has no table entry, whose sequence or block
  * is out of range, or whose page is not in [0, pages); its query row is as bitlinear_rope's.  Two
- * tokens of one call must not name the same slot.  R % 8 == 0; input and query rows aligned to four
- * elements. */
+ * tokens of one call must not name the same slot. */
 int bitlinear_rope_append(const bl_rope_desc* qkv, int64_t T, int64_t R, int interleaved,
                           int x_dtype, int q_dtype, const int32_t* pos, const int32_t* seq,
                           const int32_t* blocks, int64_t seqs, int64_t blocks_per_seq,

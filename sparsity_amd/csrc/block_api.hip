@@ -238,7 +238,7 @@ int bitlinear_rope_append(const bl_rope_desc* qkv, int64_t T, int64_t R, int int
   const int cs = check_cache(kv, &extent);
   if (cs != BL_OK) return cs;
   const int64_t D = kv->head_dim;
-  if (!qkv || T < 0 || T > kMaxTokens || R < 8 || R > D || R % 8 || positions < 0 ||
+  if (!qkv || T < 0 || T > kMaxTokens || R < 2 || R > D || R % 2 || positions < 0 ||
       positions > INT32_MAX || seqs < 1 || blocks_per_seq < 1 || seqs > INT32_MAX ||
       blocks_per_seq > INT32_MAX)
     return BL_EINVAL;
@@ -248,14 +248,14 @@ int bitlinear_rope_append(const bl_rope_desc* qkv, int64_t T, int64_t R, int int
   const int st = rope_tensors(qkv, 3, T, D, R, x_dtype, q_dtype, pos, table, positions, 1, &a, &vec);
   if (st != BL_OK) return st;
   if (T == 0) return BL_OK;
-  if (!vec || !aligned(blocks, 4) || (seq && !aligned(seq, 4))) return BL_EINVAL;
+  if (!aligned(blocks, 4) || (seq && !aligned(seq, 4))) return BL_EINVAL;
   a.interleaved = interleaved != 0;
   a.kv = *kv;
   a.blocks = blocks;
   a.seq = seq;
   a.seqs = seqs;
   a.blocks_per_seq = blocks_per_seq;
-  return status_of(bl::launch_rope_append(a, x_dtype == BL_DTYPE_BF16, q_dtype == BL_DTYPE_BF16,
+  return status_of(bl::launch_rope_append(a, x_dtype == BL_DTYPE_BF16, q_dtype == BL_DTYPE_BF16, vec,
                                           (hipStream_t)stream));
 }
 

@@ -102,7 +102,7 @@ struct RopeArgs {
   int64_t seqs, blocks_per_seq;
 };
 hipError_t launch_rope(const RopeArgs& a, bool x_bf16, bool y_bf16, bool vec, hipStream_t s);
-hipError_t launch_rope_append(const RopeArgs& a, bool x_bf16, bool y_bf16, hipStream_t s);
+hipError_t launch_rope_append(const RopeArgs& a, bool x_bf16, bool y_bf16, bool vec, hipStream_t s);
 hipError_t launch_rope_table(const double* freq, int64_t half, int64_t positions, double mscale,
                              float* table, hipStream_t s);
 

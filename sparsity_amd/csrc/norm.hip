@@ -314,7 +314,7 @@ hipError_t launch_bwd_t(const NormBwdArgs& a, hipStream_t s) {
   else if (pieces <= 2048) norm_bwd_kernel<GBF, HBF, OBF, 16, 2><<<grid, block, lds, s>>>(a);
   else norm_bwd_kernel<GBF, HBF, OBF, 16, 4><<<grid, block, lds, s>>>(a);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !a.dw) return e;
+  if (e != hipSuccess || !a.dw || a.blocks == 1) return e;
   norm_dw_kernel<<<dim3((unsigned)((a.K + 31) / 32)), 256, 0, s>>>(a.part, a.blocks, a.K, a.dw);
   return hipGetLastError();
 }
@@ -324,11 +324,14 @@ hipError_t launch_bwd_t(const NormBwdArgs& a, hipStream_t s) {
 int norm_bwd_blocks(int64_t T, int64_t K) {
   const int64_t pieces = K / 8;
   const int64_t rows = pieces <= 64 ? 16 : pieces <= 512 ? 4 : 1;   // rows a block takes at a time
-  return (int)std::max<int64_t>(1, std::min<int64_t>(512, (T + rows - 1) / rows));
+  if (T <= 2 * rows) return 1;   // two rounds of rows cost less than a second launch
+  return (int)std::min<int64_t>(512, (T + rows - 1) / rows);
 }
 
-hipError_t launch_norm_bwd(const NormBwdArgs& a, bool dn_bf16, bool h_bf16, bool grad_bf16,
+hipError_t launch_norm_bwd(const NormBwdArgs& in, bool dn_bf16, bool h_bf16, bool grad_bf16,
                            hipStream_t s) {
+  NormBwdArgs a = in;
+  if (a.blocks == 1) a.part = a.dw;         // one block's sums are the sums
   if (dn_bf16) {
     if (h_bf16) return grad_bf16 ? launch_bwd_t<true, true, true>(a, s) : launch_bwd_t<true, true, false>(a, s);
     return grad_bf16 ? launch_bwd_t<true, false, true>(a, s) : launch_bwd_t<true, false, false>(a, s);

@@ -118,16 +118,17 @@ __device__ __forceinline__ int tensor_of(const RopeArgs& a, int head) {
   return m;
 }
 
-// Vector form: D and R multiples of 8, rows aligned to four elements.  LPH lanes per head (the
-// power of two not below D / 8), 256 / LPH heads at a time.  APPEND: tensors 1 and 2 go to the
-// cache.
-template <bool XBF, bool YBF, bool APPEND, int LPH>
+// LPH lanes per head (the power of two not below D / 8), 256 / LPH heads at a time, a lane eight
+// elements.  APPEND: tensors 1 and 2 go to the cache.  VEC: D and R multiples of 8, rows aligned to
+// four elements.  Otherwise (APPEND only, D a multiple of 8) a lane takes elements 8 i .. 8 i + 7 of
+// any alignment and reads the other half of each pair itself.
+template <bool XBF, bool YBF, bool APPEND, bool VEC, int LPH>
 __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
   constexpr int HPB = 256 / LPH;
   const int i = threadIdx.x & (LPH - 1), slot = threadIdx.x / LPH;
   const int64_t t = blockIdx.x;
   const bool on = 8 * i < a.D;
-  const Item it = item_of(i, a.R, a.interleaved);
+  const Item it = VEC ? item_of(i, a.R, a.interleaved) : Item{8 * i, 8 * i + 4, -1};
   // a head's elements are asked for one head ahead, the first before the position and its cosines
   auto tensor = [&](int hd) {
     return APPEND ? (hd >= a.t[1].head0) + (hd >= a.t[2].head0) : tensor_of(a, hd);
@@ -136,8 +137,16 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
     if (!on || hd >= a.heads) return;
     const RopeTensor& x = a.t[tensor(hd)];
     const int64_t r = t * x.x_tok + (hd - x.head0) * x.x_head;
-    load4<XBF>(x.x, r + it.e0, u);
-    load4<XBF>(x.x, r + it.e1, w);
+    if constexpr (VEC) {
+      load4<XBF>(x.x, r + it.e0, u);
+      load4<XBF>(x.x, r + it.e1, w);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        u[k] = load1<XBF>(x.x, r + it.e0 + k);
+        w[k] = load1<XBF>(x.x, r + it.e1 + k);
+      }
+    }
   };
   const int step = gridDim.y * HPB;
   int hd = blockIdx.y * HPB + slot;
@@ -146,6 +155,25 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
   const int64_t pos = a.pos[t];
   float c[4], s[4];
   load_cs(a, pos, on ? it.pair0 : -1, c, s);
+  // element by element: its cosine, its sine with the sign it has there, the other half of its pair
+  float ec[8], es[8];
+  int other[8];
+  if constexpr (!VEC) {
+    const int half = a.R / 2;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int e = 8 * i + k;
+      ec[k] = 1.f;
+      es[k] = 0.f;
+      other[k] = -1;
+      if (!on || e >= a.R || pos < 0 || pos >= a.positions) continue;
+      const bool first = a.interleaved ? !(e & 1) : e < half;
+      const float* p = a.table + (pos * half + (a.interleaved ? e / 2 : first ? e : e - half)) * 2;
+      ec[k] = p[0];
+      es[k] = first != (a.inverse != 0) ? -p[1] : p[1];
+      other[k] = a.interleaved ? e ^ 1 : first ? e + half : e - half;
+    }
+  }
   const bool known = pos < a.positions, pad = pos < 0;
   int64_t page = -1;
   int off = 0;
@@ -165,7 +193,17 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
     const int m = tensor(hd);
     const RopeTensor& x = a.t[m];
     const int h = hd - x.head0;
-    if ((!APPEND || m < 2) && it.pair0 >= 0) rotate(u, w, c, s, a.interleaved);
+    if constexpr (VEC) {
+      if ((!APPEND || m < 2) && it.pair0 >= 0) rotate(u, w, c, s, a.interleaved);
+    } else if (m < 2) {
+      const int64_t r = t * x.x_tok + h * x.x_head;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (other[k] >= 0) {
+          float& v = k < 4 ? u[k] : w[k - 4];
+          v = v * ec[k] + load1<XBF>(x.x, r + other[k]) * es[k];
+        }
+    }
     if (!APPEND || m == 0) {
       if (!known || pad) {
         const float v = pad ? 0.f : __builtin_nanf("");
@@ -174,8 +212,16 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
       }
       if (on) {
         const int64_t r = t * x.y_tok + h * x.y_head;
-        store4<YBF>(x.y, r + it.e0, u);
-        store4<YBF>(x.y, r + it.e1, w);
+        if constexpr (VEC) {
+          store4<YBF>(x.y, r + it.e0, u);
+          store4<YBF>(x.y, r + it.e1, w);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            store1<YBF>(x.y, r + it.e0 + k, u[k]);
+            store1<YBF>(x.y, r + it.e1 + k, w[k]);
+          }
+        }
       }
       continue;
     }
@@ -251,7 +297,7 @@ __global__ __launch_bounds__(256) void rope_table_kernel(const double* __restric
   *(float2*)(table + 2 * i) = make_float2((float)(cs * mscale), (float)(sn * mscale));
 }
 
-template <bool XBF, bool YBF, bool APPEND>
+template <bool XBF, bool YBF, bool APPEND, bool VEC>
 hipError_t launch_rope_t(const RopeArgs& a, hipStream_t s) {
   const int lanes = a.D / 8;
   auto go = [&](auto lph) {
@@ -259,7 +305,7 @@ hipError_t launch_rope_t(const RopeArgs& a, hipStream_t s) {
     const int hpb = 256 / LPH, rounds = (a.heads + hpb - 1) / hpb;
     // few tokens: a block per round of heads, so the heads of a token run side by side
     const int y = (int)std::min<int64_t>(rounds, std::max<int64_t>(1, 1024 / a.T));
-    rope_kernel<XBF, YBF, APPEND, LPH><<<dim3((unsigned)a.T, (unsigned)y), 256, 0, s>>>(a);
+    rope_kernel<XBF, YBF, APPEND, VEC, LPH><<<dim3((unsigned)a.T, (unsigned)y), 256, 0, s>>>(a);
   };
   if (lanes <= 8) go(std::integral_constant<int, 8>{});
   else if (lanes <= 16) go(std::integral_constant<int, 16>{});
@@ -269,25 +315,27 @@ hipError_t launch_rope_t(const RopeArgs& a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_rope(const RopeArgs& a, bool x_bf16, bool y_bf16, bool vec, hipStream_t s) {
-  if (!vec) {
-    const dim3 grid((unsigned)a.T);
-    if (x_bf16) {
-      if (y_bf16) rope_scalar_kernel<true, true><<<grid, 256, 0, s>>>(a);
-      else rope_scalar_kernel<true, false><<<grid, 256, 0, s>>>(a);
-    } else {
-      if (y_bf16) rope_scalar_kernel<false, true><<<grid, 256, 0, s>>>(a);
-      else rope_scalar_kernel<false, false><<<grid, 256, 0, s>>>(a);
-    }
-    return hipGetLastError();
-  }
-  if (x_bf16) return y_bf16 ? launch_rope_t<true, true, false>(a, s) : launch_rope_t<true, false, false>(a, s);
-  return y_bf16 ? launch_rope_t<false, true, false>(a, s) : launch_rope_t<false, false, false>(a, s);
+// Calls f with the two input types as compile-time booleans.
+template <class F>
+static hipError_t with_types(bool x, bool y, F&& f) {
+  if (x) return y ? f(std::true_type{}, std::true_type{}) : f(std::true_type{}, std::false_type{});
+  return y ? f(std::false_type{}, std::true_type{}) : f(std::false_type{}, std::false_type{});
 }
 
-hipError_t launch_rope_append(const RopeArgs& a, bool x_bf16, bool y_bf16, hipStream_t s) {
-  if (x_bf16) return y_bf16 ? launch_rope_t<true, true, true>(a, s) : launch_rope_t<true, false, true>(a, s);
-  return y_bf16 ? launch_rope_t<false, true, true>(a, s) : launch_rope_t<false, false, true>(a, s);
+hipError_t launch_rope(const RopeArgs& a, bool x_bf16, bool y_bf16, bool vec, hipStream_t s) {
+  return with_types(x_bf16, y_bf16, [&](auto x, auto y) {
+    constexpr bool X = decltype(x)::value, Y = decltype(y)::value;
+    if (vec) return launch_rope_t<X, Y, false, true>(a, s);
+    rope_scalar_kernel<X, Y><<<dim3((unsigned)a.T), 256, 0, s>>>(a);
+    return hipGetLastError();
+  });
+}
+
+hipError_t launch_rope_append(const RopeArgs& a, bool x_bf16, bool y_bf16, bool vec, hipStream_t s) {
+  return with_types(x_bf16, y_bf16, [&](auto x, auto y) {
+    constexpr bool X = decltype(x)::value, Y = decltype(y)::value;
+    return vec ? launch_rope_t<X, Y, true, true>(a, s) : launch_rope_t<X, Y, true, false>(a, s);
+  });
 }
 
 hipError_t launch_rope_table(const double* freq, int64_t half, int64_t positions, double mscale,

@@ -139,12 +139,11 @@ def _append(q=None, k=None, v=None, **kw):
 
 
 @pytest.mark.parametrize("kw,want", [
-    (dict(xd=2), ENOTSUP), (dict(qd=2), ENOTSUP), (dict(R=4), EINVAL), (dict(R=20), EINVAL), (dict(R=136), EINVAL),
+    (dict(xd=2), ENOTSUP), (dict(qd=2), ENOTSUP), (dict(R=0), EINVAL), (dict(R=21), EINVAL), (dict(R=136), EINVAL),
     (dict(T=-1), EINVAL), (dict(seqs=0), EINVAL), (dict(per=0), EINVAL), (dict(blocks=None), EINVAL),
     (dict(blocks=P + 2), EINVAL), (dict(seq=P + 1), EINVAL), (dict(pos=None), EINVAL), (dict(table=P + 4), EINVAL),
     (dict(kv=None), EINVAL), (dict(k=_desc(1, heads=4)), EINVAL), (dict(v=_desc(2, heads=6)), EINVAL),
-    (dict(q=_desc(0, heads=20, x_tok=2562, y_tok=2560)), EINVAL),     # rows not aligned to four elements
-    (dict(k=_desc(1, heads=5, x=P + SLOT + 4)), EINVAL), (dict(q=_desc(0, heads=20, x_tok=2560, y_tok=640)), EINVAL)])
+    (dict(k=_desc(1, heads=5, x=P + SLOT + 2)), EINVAL), (dict(q=_desc(0, heads=20, x_tok=2560, y_tok=640)), EINVAL)])
 def test_append_rejects(kw, want):
     assert _append(**kw) == want
 

@@ -116,7 +116,11 @@ def test_rope_gradient_against_differences():
                                                     (80, 32, 4, 1, 7, "bf16", True),
                                                     (64, 64, 3, 3, 1, "f32", True),
                                                     (256, 128, 4, 2, 64, "bf16", False),
-                                                    (96, 48, 25, 25, 24, "f32", False)])
+                                                    (96, 48, 25, 25, 24, "f32", False),
+                                                    (80, 20, 4, 2, 16, "bf16", False),   # pairs that
+                                                    (64, 22, 3, 1, 16, "f32", False),    # no vector holds
+                                                    (48, 30, 2, 2, 8, "f32", True),
+                                                    (16, 2, 1, 1, 4, "bf16", False)])
 @pytest.mark.parametrize("T", [1, 13, 260])
 def test_append(kv, D, Rt, Hq, Hk, ps, xd, inter, T):
     import torch
@@ -190,3 +194,30 @@ def test_append_decode_step_without_sequence_list_and_token_major_cache():
         got_k[pg, off] = 0
         got_v[pg, off] = 0
     assert not got_k.any() and not got_v.any()
+
+
+@pytest.mark.parametrize("xd", ["f32", "bf16"])
+def test_append_from_rows_of_any_alignment(xd):
+    """Queries, keys and values one element off alignment, with odd strides; queries in place."""
+    import torch
+    g = rng(31)
+    T, Hq, Hk, D, ps = 7, 4, 2, 32, 8
+    W = Hq * D + 2 * Hk * D + 3
+    table = R.rope_table(S.rope_frequencies(16)[0], 30)
+    x, _ = _t(g, (T, W), xd)
+    buf = torch.empty(T * W + 1, dtype=torch.float32 if xd == "f32" else torch.bfloat16, device="cuda")[1:]
+    buf.copy_(dev(x.reshape(-1)))
+    rows = buf.view(T, W)
+    cut = lambda a, h: rows[:, a:a + h * D].unflatten(1, (h, D))
+    q, k, v = cut(1, Hq), cut(1 + Hq * D, Hk), cut(2 + (Hq + Hk) * D, Hk)
+    pos = g.integers(0, 30, T).astype(np.int32)
+    blocks = np.arange(T * 4, dtype=np.int32).reshape(T, 4)
+    kc, vc = (torch.zeros(T * 4, Hk, ps, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    want_q = R.rope(x[:, 1:1 + Hq * D].reshape(T, Hq, D), pos, table)
+    want_k = R.bf16_round(R.rope(x[:, 1 + Hq * D:1 + (Hq + Hk) * D].reshape(T, Hk, D), pos, table))
+    want_v = R.bf16_round(x[:, 2 + (Hq + Hk) * D:2 + (Hq + 2 * Hk) * D].reshape(T, Hk, D))
+    out = S.rope_append(q, k, v, dev(pos), dev(table), kc, vc, dev(blocks), out=q)
+    assert _same(_f32(out), want_q if xd == "f32" else R.bf16_round(want_q))
+    for t in range(T):
+        pg, off = blocks[t, pos[t] // ps], pos[t] % ps
+        assert _same(_f32(kc)[pg, :, off], want_k[t]) and _same(_f32(vc)[pg, :, off], want_v[t])
