@@ -268,13 +268,13 @@ def norm_quant_bwd(dn, h, rstd, weight=None, dres=None, dtype=None, want_dw: boo
     if dw is not None:
         st, wsb = bitlinear_norm_quant_bwd_workspace_bytes(T, K)
         _check(st, "bitlinear_norm_quant_bwd_workspace_bytes")
-        if ws is None:
-            ws = dn.new_empty(wsb, dtype=torch.uint8)
-        else:
-            _buf(ws, torch.uint8, wsb, ix, "ws")
-            wsb = ws.numel()
-    else:
+    if wsb == 0:
         ws = None
+    elif ws is None:
+        ws = dn.new_empty(wsb, dtype=torch.uint8)
+    else:
+        _buf(ws, torch.uint8, wsb, ix, "ws")
+        wsb = ws.numel()
     _check(_lib().bitlinear_norm_quant_bwd(dn.data_ptr(), gd, h.data_ptr(), hd, rstd.data_ptr(),
                                            _ptr(weight), _ptr(dres), dh.data_ptr(), od, _ptr(dw), T,
                                            K, _ptr(ws), wsb, _stream(ix)),

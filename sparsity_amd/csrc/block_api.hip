@@ -71,7 +71,8 @@ int bitlinear_norm_quant(const void* x, int x_dtype, const void* res, int res_dt
 int bitlinear_norm_quant_bwd_workspace_bytes(int64_t T, int64_t K, size_t* ws_bytes) {
   if (!rows_ok(T, K) || !ws_bytes) return BL_EINVAL;
   if (K > bl::kNormMaxK) return BL_ENOTSUP;
-  *ws_bytes = (size_t)bl::norm_bwd_blocks(T, K) * (size_t)K * 4;
+  const int blocks = bl::norm_bwd_blocks(T, K);
+  *ws_bytes = blocks > 1 ? (size_t)blocks * (size_t)K * 4 : 0;   // one block writes dw itself
   return BL_OK;
 }
 
@@ -87,9 +88,10 @@ int bitlinear_norm_quant_bwd(const void* dn, int dn_dtype, const void* h, int h_
   if (T > 0 && (!aligned(dn, 16) || !aligned(h, 16) || !aligned(rstd, 4) || !aligned(dh, 16)))
     return BL_EINVAL;
   if ((w && !aligned(w, 16)) || (dres && !aligned(dres, 16)) || (dw && !aligned(dw, 16))) return BL_EINVAL;
-  if (dw && !aligned(ws, 16)) return BL_EINVAL;
-  if (dw && ws_bytes < need) return BL_ENOSPC;
-  if (!dw) { ws = nullptr; need = 0; }
+  if (!dw) need = 0;
+  if (need && !aligned(ws, 16)) return BL_EINVAL;
+  if (ws_bytes < need) return BL_ENOSPC;
+  if (!need) ws = nullptr;
   const uint64_t n = (uint64_t)T * (uint64_t)K;
   const Span in[5] = {{dn, n * esize(dn_dtype)}, {dres, n * esize(grad_dtype)}, {h, n * esize(h_dtype)},
                       {rstd, (uint64_t)T * 4}, {w, (uint64_t)K * 4}};

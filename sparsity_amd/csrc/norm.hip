@@ -14,6 +14,10 @@
 //
 // A row belongs to W waves; a lane holds pieces of eight elements, p = lane, lane + 64 W, ..., in
 // registers from the first load to the int8 store, so every input byte is read once.
+//
+// Measured (kernel time): 8192 x 3200, fp32 onto a bf16 stream with rstd: 40 us, 5.9 TB/s of the 236 MB
+// it has to move (a large device copy reaches 5.2 TB/s of reads and writes); 2048 x 4096 bf16 onto an
+// fp32 stream with 6:8 rows: 19 us; one token of 2560: 3.0 us, the round trips of a single load.
 #include <algorithm>
 
 #include "block_ops.hpp"
@@ -180,6 +184,10 @@ hipError_t launch_norm_quant(const NormArgs& a, bool x_bf16, bool res_bf16, hipS
 // (rounding and clipping of the quantizer pass the gradient through unchanged).  dh is the gradient
 // of both addends of h.  Each block walks rows and keeps its columns' dw sums in registers; the
 // blocks' sums are added in a second launch in a fixed order, so dw does not vary from run to run.
+// Teams of W waves take a row each; 16 waves and 512 blocks keep the blocks' sums (6.5 MB at K = 3200)
+// small beside the rows.  Asking for a row ahead spilled registers and more than doubled the time.
+//
+// Measured: 8192 x 3200, fp32 dn, bf16 h, dres and dh: 50 us for the rows, 5.4 TB/s, 4.8 us for dw.
 // ---------------------------------------------------------------------------------------------
 namespace {
 

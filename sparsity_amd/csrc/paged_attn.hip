@@ -24,9 +24,18 @@
 // of it): two where the output is bf16, good to 2^-17, three for fp32 queries and output; an fp32
 // query's three terms hold it exactly.  The matrix cores are idle enough that this costs nothing.
 //
-// The four waves of a block take quarters of the block's run of keys and join in LDS; a run's
-// partial sums go to the workspace and the last block of a (sequence, head group) to finish joins
-// them, in the order of the runs, so the result does not depend on which block that is.
+// The launch is one block per resident place of the chip (two per CU: a wave then has 16 KB of keys and
+// values in flight while the matrix cores work on the last 16; three waves per SIMD spill, one leaves
+// int8 caches at half the rate).  The blocks share all keys of all sequences evenly (see Work), the
+// four waves of a block take quarters of its run and join in LDS; a run that is not its group's whole
+// goes to the workspace as partial sums, and the last block of the group to finish joins the runs, in
+// their order, so the result does not depend on which block that is.
+//
+// Measured: 64 x 8192 tokens, 8 key heads, 32 query heads of 128, bf16: 363 us, 5.9 TB/s; the same in
+// int8 210 us, 5.3 TB/s; one sequence of 262144 tokens, 5 key heads: 132 us, 5.1 TB/s; 48 ragged
+// sequences up to 6001 tokens, int8: 70 us, 4.3 TB/s; 700 tokens: 12 us, ten dependent round trips to
+// memory.  What is lost: 7 us to the first keys (lengths, then pages, then rows), blocks that end up to
+// 12% apart under equal shares (memory serves the CUs unevenly), about 3 us for a join.
 #include <algorithm>
 
 #include "block_ops.hpp"

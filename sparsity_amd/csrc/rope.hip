@@ -11,6 +11,10 @@
 //
 // One pass over the data, bound by memory: a block takes a token, a group of lanes a head at a
 // time, and a lane the same pairs of every head it visits, so cos and sin are read once per lane.
+// Measured (kernel time): 8192 tokens of 50 heads of 128, fp32 to bf16: 60.5 us, 5.3 TB/s (a large
+// device copy: 5.2); asking for one head ahead is worth 9%, two or four heads at a time lose 2 to 8%.
+// 1021 tokens of 40 bf16 heads of 80: 7.0 us, of which 2.6 us would be the bytes.  Append of 4096
+// tokens (48 heads of 128) to an int8 cache: 27 us, 5.4 TB/s; of 16 tokens: 4.2 us of latency.
 //
 // The int8 cache holds act_quant_i8's expressions per token and head (absmax / 127, round half to
 // even) on the rotated key and on the value.
