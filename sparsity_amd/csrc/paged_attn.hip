@@ -8,8 +8,8 @@
 // key head), so the kernel is bound by memory: the work is to keep loads in flight and to spend
 // little on each byte.
 //
-// A wave takes 32 keys at a time (64 of an int8 cache) for up to 16 query heads of one key head, the running maximum and
-// sum of the softmax in registers:
+// A wave takes 32 keys at a time (64 of an int8 cache) for up to 16 query heads of one key head, the
+// running maximum and sum of the softmax in registers:
 //   S^T = K Q^T   16x16x32 MFMAs with 16 keys as rows.  A lane's operand is 16 contiguous bytes of
 //                 its key's row, straight from memory.  Lane (g, n) (g = lane / 16, n = lane % 16)
 //                 receives the scores of query n and keys 4g..4g+3 of each 16-key tile.
