@@ -71,8 +71,7 @@ int bitlinear_norm_quant(const void* x, int x_dtype, const void* res, int res_dt
 int bitlinear_norm_quant_bwd_workspace_bytes(int64_t T, int64_t K, size_t* ws_bytes) {
   if (!rows_ok(T, K) || !ws_bytes) return BL_EINVAL;
   if (K > bl::kNormMaxK) return BL_ENOTSUP;
-  const int blocks = bl::norm_bwd_blocks(T, K);
-  *ws_bytes = blocks > 1 ? (size_t)blocks * (size_t)K * 4 : 0;   // one block writes dw itself
+  *ws_bytes = bl::norm_bwd_columns(T, K) ? 0 : (size_t)bl::norm_bwd_blocks(T, K) * (size_t)K * 4;
   return BL_OK;
 }
 

@@ -71,10 +71,11 @@ struct NormBwdArgs {
   const void* dres;
   void* dh;
   float* dw;             // nullptr: not wanted
-  float* part;           // [blocks][K] column sums of each block
+  float* part;           // [blocks][K] column sums of each block; nullptr: dw by columns
   int32_t T, K, blocks;
 };
-int norm_bwd_blocks(int64_t T, int64_t K);
+int norm_bwd_blocks(int64_t T, int64_t K);      // blocks of the rows
+bool norm_bwd_columns(int64_t T, int64_t K);    // whether dw is summed by columns, without a workspace
 hipError_t launch_norm_bwd(const NormBwdArgs& a, bool dn_bf16, bool h_bf16, bool grad_bf16,
                            hipStream_t s);
 

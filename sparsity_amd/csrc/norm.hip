@@ -182,8 +182,10 @@ hipError_t launch_norm_quant(const NormArgs& a, bool x_bf16, bool res_bf16, hipS
 // Gradient.  With nh = h * rstd and gw = dn * w:
 //   dh = rstd * (gw - nh * mean(gw * nh)) (+ dres)        dw = sum over tokens of dn * nh
 // (rounding and clipping of the quantizer pass the gradient through unchanged).  dh is the gradient
-// of both addends of h.  Each block walks rows and keeps its columns' dw sums in registers; the
-// blocks' sums are added in a second launch in a fixed order, so dw does not vary from run to run.
+// of both addends of h.  dw is summed in a fixed order, so it does not vary from run to run, in one of
+// two ways.  Many rows: each block walks rows and keeps its columns' sums in registers, and a second
+// launch adds the blocks'.  Few rows: blocks of their own read dn and h once more, from the caches, and
+// sum 64 columns each over all rows, in the same launch and without a workspace.
 // Teams of W waves take a row each; 16 waves and 512 blocks keep the blocks' sums (6.5 MB at K = 3200)
 // small beside the rows.  Asking for a row ahead spilled registers and more than doubled the time.
 //
@@ -191,11 +193,52 @@ hipError_t launch_norm_quant(const NormArgs& a, bool x_bf16, bool res_bf16, hipS
 // ---------------------------------------------------------------------------------------------
 namespace {
 
+// dw of 64 columns: eight lanes of eight columns, 128 rows at a time, the 128 joined in LDS.
+constexpr int kColumns = 64;
+constexpr size_t kColumnLds = (128 + 16) * kColumns * sizeof(float);
+
+template <bool GBF, bool HBF>
+__device__ __forceinline__ void dw_columns(const NormBwdArgs& a, int block, float* lds) {
+  const int c = threadIdx.x & 7, r = threadIdx.x >> 3;
+  const int k = block * kColumns + 8 * c;
+  float s[8] = {};
+  if (k < a.K) {
+#pragma unroll 4
+    for (int64_t t = r; t < a.T; t += 128) {
+      float g[8], h[8];
+      const float rstd = a.rstd[t];
+      load_f8<GBF>(a.dn, (size_t)t * a.K + k, g);
+      load_f8<HBF>(a.h, (size_t)t * a.K + k, h);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j] += g[j] * (h[j] * rstd);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) lds[r * kColumns + 8 * c + j] = s[j];
+  __syncthreads();
+  const int col = threadIdx.x % kColumns, part = threadIdx.x / kColumns;   // 16 parts of eight rows
+  float v = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v += lds[(8 * part + i) * kColumns + col];
+  float* join = lds + 128 * kColumns;
+  join[part * kColumns + col] = v;
+  __syncthreads();
+  if (part == 0 && block * kColumns + col < a.K) {
+#pragma unroll
+    for (int i = 1; i < 16; ++i) v += join[i * kColumns + col];
+    a.dw[block * kColumns + col] = v;
+  }
+}
+
 template <bool GBF, bool HBF, bool OBF, int W, int P>
 __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdArgs a) {
   constexpr int RPB = 16 / W;               // row teams of W waves
   __shared__ float red[2][16];
-  extern __shared__ __attribute__((aligned(16))) float sm_dw[];   // [K]
+  extern __shared__ __attribute__((aligned(16))) float sm_dw[];   // [K], or dw_columns' sums
+  if ((int)blockIdx.x >= a.blocks) {        // the blocks behind those of the rows
+    dw_columns<GBF, HBF>(a, blockIdx.x - a.blocks, sm_dw);
+    return;
+  }
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int team = wave / W;
   const int K = a.K, pieces = K / 8;
@@ -270,7 +313,7 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdArgs a) {
       store_f8<OBF>(a.dh, row + 8 * p, o);
     }
   }
-  if (!a.dw) return;
+  if (!a.part) return;
   // the teams' sums one after another into LDS, in team order
   for (int k = 0; k < RPB; ++k) {
     if (team == k) {
@@ -311,18 +354,34 @@ __global__ __launch_bounds__(256) void norm_dw_kernel(const float* __restrict__ 
 }
 
 template <bool GBF, bool HBF, bool OBF>
-hipError_t launch_bwd_t(const NormBwdArgs& a, hipStream_t s) {
+hipError_t launch_rows(const NormBwdArgs& a, int columns, hipStream_t s) {
   const int pieces = a.K / 8;
-  const dim3 grid((unsigned)a.blocks), block(1024);
-  const size_t lds = a.dw && pieces <= 512 ? (size_t)a.K * 4 : 0;   // one team: no sums to join
+  const dim3 grid((unsigned)(a.blocks + columns)), block(1024);
+  if (grid.x == 0) return hipSuccess;
+  // more than 512 pieces: one team, no sums to join
+  const size_t lds = columns ? kColumnLds : a.part && pieces <= 512 ? (size_t)a.K * 4 : 0;
   if (pieces <= 64) norm_bwd_kernel<GBF, HBF, OBF, 1, 1><<<grid, block, lds, s>>>(a);
   else if (pieces <= 256) norm_bwd_kernel<GBF, HBF, OBF, 4, 1><<<grid, block, lds, s>>>(a);
   else if (pieces <= 512) norm_bwd_kernel<GBF, HBF, OBF, 4, 2><<<grid, block, lds, s>>>(a);
   else if (pieces <= 1024) norm_bwd_kernel<GBF, HBF, OBF, 16, 1><<<grid, block, lds, s>>>(a);
   else if (pieces <= 2048) norm_bwd_kernel<GBF, HBF, OBF, 16, 2><<<grid, block, lds, s>>>(a);
   else norm_bwd_kernel<GBF, HBF, OBF, 16, 4><<<grid, block, lds, s>>>(a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !a.dw || a.blocks == 1) return e;
+  return hipGetLastError();
+}
+
+template <bool GBF, bool HBF, bool OBF>
+hipError_t launch_bwd_t(NormBwdArgs a, hipStream_t s) {
+  if (a.dw && !a.part) {
+    const int columns = (a.K + kColumns - 1) / kColumns, rows = a.blocks;
+    if (a.dh != a.dn) return launch_rows<GBF, HBF, OBF>(a, columns, s);
+    // in place over dn: the columns have to be read before
+    a.blocks = 0;
+    const hipError_t e = launch_rows<GBF, HBF, OBF>(a, columns, s);
+    a.blocks = rows;
+    return e != hipSuccess ? e : launch_rows<GBF, HBF, OBF>(a, 0, s);
+  }
+  const hipError_t e = launch_rows<GBF, HBF, OBF>(a, 0, s);
+  if (e != hipSuccess || !a.dw) return e;
   norm_dw_kernel<<<dim3((unsigned)((a.K + 31) / 32)), 256, 0, s>>>(a.part, a.blocks, a.K, a.dw);
   return hipGetLastError();
 }
@@ -332,14 +391,17 @@ hipError_t launch_bwd_t(const NormBwdArgs& a, hipStream_t s) {
 int norm_bwd_blocks(int64_t T, int64_t K) {
   const int64_t pieces = K / 8;
   const int64_t rows = pieces <= 64 ? 16 : pieces <= 512 ? 4 : 1;   // rows a block takes at a time
-  if (T <= 2 * rows) return 1;   // two rounds of rows cost less than a second launch
   return (int)std::min<int64_t>(512, (T + rows - 1) / rows);
 }
 
-hipError_t launch_norm_bwd(const NormBwdArgs& in, bool dn_bf16, bool h_bf16, bool grad_bf16,
+// By columns while a block's walk over the rows is short and the second reading comes from the caches.
+// One launch against two, graph replays (calls one after another): 64 x 2560 4.3 us against 7.5 (10.9
+// against 15.2), 512 x 2560 6.6 against 10.1, 512 x 8192 13.9 against 18.8; 1024 x 2560 13.2 against
+// 11.9, 2048 x 512 13.3 against 8.5, 2048 x 8192 46 against 41.
+bool norm_bwd_columns(int64_t T, int64_t K) { return T <= 768 && T * K <= (int64_t)1 << 22; }
+
+hipError_t launch_norm_bwd(const NormBwdArgs& a, bool dn_bf16, bool h_bf16, bool grad_bf16,
                            hipStream_t s) {
-  NormBwdArgs a = in;
-  if (a.blocks == 1) a.part = a.dw;         // one block's sums are the sums
   if (dn_bf16) {
     if (h_bf16) return grad_bf16 ? launch_bwd_t<true, true, true>(a, s) : launch_bwd_t<true, true, false>(a, s);
     return grad_bf16 ? launch_bwd_t<true, false, true>(a, s) : launch_bwd_t<true, false, false>(a, s);

@@ -117,7 +117,8 @@ def _grad_bound(dn, h, rstd, w, dres, out, grad):
 
 
 @pytest.mark.parametrize("T,K", [(1, 8), (3, 512), (17, 520), (130, 2048), (1031, 264), (5, 4096),
-                                 (6, 4104), (3, 8192), (2, 16384), (2, 32768), (700, 3200)])
+                                 (6, 4104), (3, 8192), (2, 16384), (2, 32768), (700, 3200),
+                                 (2100, 2048), (20000, 256), (530, 8200), (300, 16384), (140, 32768)])
 @pytest.mark.parametrize("dd,hd,gd,withres", [("f32", "bf16", "bf16", True), ("bf16", "f32", "f32", False),
                                               ("f32", "f32", "f32", True), ("bf16", "bf16", "bf16", False),
                                               ("f32", "bf16", "f32", True)])
@@ -162,6 +163,20 @@ def test_norm_grad_against_differences():
         u = rng(60 + s).standard_normal(K)
         d = (f(h, w + e * u) - f(h, w - e * u)) / (2 * e)
         assert abs(d - float((host(dw).astype(np.float64) * u).sum())) <= 1e-6 * np.abs(host(dw) * u).sum()
+
+
+@pytest.mark.parametrize("T,K", [(20, 512), (300, 1032), (4200, 1032)])
+def test_norm_grad_in_place_of_its_input(T, K):
+    """dh over dn: dw still sums the gradient that came in."""
+    g = rng(T)
+    dn, dnt = _rows(g, T, K, "f32")
+    h, ht = _rows(g, T, K, "bf16")
+    rstd = dev((1 / np.sqrt((h.astype(np.float64) ** 2).mean(-1) + 1e-6)).astype(np.float32))
+    want, dw = S.norm_quant_bwd(dnt, ht, rstd)
+    keep = f32_bits(host(want)).copy()
+    got, dw1 = S.norm_quant_bwd(dnt, ht, rstd, out=(dnt, dw.clone()))
+    assert got is dnt and np.array_equal(f32_bits(host(dnt)), keep)
+    assert np.array_equal(f32_bits(host(dw)), f32_bits(host(dw1)))
 
 
 def test_norm_grad_in_place_and_no_tokens():
