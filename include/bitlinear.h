@@ -641,7 +641,7 @@ typedef struct bl_attn_plan {
   int64_t B, max_len;
   int32_t q_heads, kv_heads, head_dim, window;
   int32_t blocks;                    /* workgroups, which share the keys of all sequences evenly */
-  int32_t reserved;
+  int32_t q_rows;                    /* query heads of one key head that a workgroup takes */
   size_t ws_bytes;
 } bl_attn_plan;
 

@@ -40,7 +40,7 @@ class BlAttnPlan(ctypes.Structure):
     """bl_attn_plan: the split of a decode attention and its workspace."""
     _fields_ = [("B", _I64), ("max_len", _I64), ("q_heads", ctypes.c_int32),
                 ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
-                ("window", ctypes.c_int32), ("blocks", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("blocks", ctypes.c_int32), ("q_rows", ctypes.c_int32),
                 ("ws_bytes", _SZ)]
 
 

@@ -264,19 +264,18 @@ int bitlinear_rope_append(const bl_rope_desc* qkv, int64_t T, int64_t R, int int
 
 namespace {
 
-constexpr int64_t kQRows = 16;             // query heads per block
 constexpr int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 
 struct AttnWs {
   int64_t ticket, ml, part, total;
 };
 AttnWs attn_ws(const bl_attn_plan& p) {
-  const int64_t G = p.q_heads / p.kv_heads, qt = (G + kQRows - 1) / kQRows;
+  const int64_t G = p.q_heads / p.kv_heads, rows = p.q_rows, qt = (G + rows - 1) / rows;
   AttnWs w;
   w.ticket = 0;
   w.ml = up256(p.B * p.kv_heads * qt * 4);
-  w.part = w.ml + up256((int64_t)p.blocks * 2 * 2 * kQRows * 4);
-  w.total = w.part + up256((int64_t)p.blocks * 2 * std::min(G, kQRows) * p.head_dim * 4);
+  w.part = w.ml + up256((int64_t)p.blocks * 2 * 2 * rows * 4);
+  w.total = w.part + up256((int64_t)p.blocks * 2 * std::min(G, rows) * p.head_dim * 4);
   return w;
 }
 
@@ -290,15 +289,10 @@ int bitlinear_paged_attn_plan(int64_t B, int64_t q_heads, int64_t kv_heads, int6
       q_heads > (1 << 20) || q_heads % kv_heads || head_dim < 8 || head_dim > 256 || head_dim % 8 ||
       max_len < 1 || max_len > INT32_MAX || window < 0 || window > INT32_MAX)
     return BL_EINVAL;
-  const int64_t G = q_heads / kv_heads, qt = (G + kQRows - 1) / kQRows;
-  const int64_t groups = B * kv_heads * qt;
-  if (groups > ((int64_t)1 << 22)) return BL_EINVAL;
-  // a block per resident place of the chip, fewer where there is less work: tiles of 128 keys, and
-  // the start of a group as so many more (at most six: see paged_attn.hip)
-  const int64_t keys = window ? std::min(window, max_len) : max_len;
-  const int64_t blocks = std::min<int64_t>(bl::paged_attn_blocks(head_dim), groups * ((keys + 127) / 128 + 6));
-  *plan = {B, max_len, (int32_t)q_heads, (int32_t)kv_heads, (int32_t)head_dim, (int32_t)window,
-           (int32_t)std::max<int64_t>(1, blocks), 0, 0};
+  const int64_t G = q_heads / kv_heads;
+  if (B * kv_heads * ((G + 15) / 16) > ((int64_t)1 << 22)) return BL_EINVAL;
+  *plan = {B, max_len, (int32_t)q_heads, (int32_t)kv_heads, (int32_t)head_dim, (int32_t)window, 0, 0, 0};
+  bl::paged_attn_split(*plan);
   plan->ws_bytes = (size_t)std::max<int64_t>(256, attn_ws(*plan).total);
   return BL_OK;
 }
@@ -313,7 +307,7 @@ int bitlinear_paged_attn(const bl_attn_plan* plan, const void* q, int q_dtype, i
   const int st = bitlinear_paged_attn_plan(plan->B, plan->q_heads, plan->kv_heads, plan->head_dim,
                                            plan->max_len, plan->window, &p);
   if (st != BL_OK) return st;
-  if (p.blocks != plan->blocks) return BL_EINVAL;   // not this build's plan
+  if (p.blocks != plan->blocks || p.q_rows != plan->q_rows) return BL_EINVAL;   // not this build's plan
   int64_t extent = 0;
   const int cs = check_cache(kv, &extent);
   if (cs != BL_OK) return cs;
@@ -355,7 +349,8 @@ int bitlinear_paged_attn(const bl_attn_plan* plan, const void* q, int q_dtype, i
   a.B = p.B;
   a.Hq = p.q_heads;
   a.G = p.q_heads / p.kv_heads;
-  a.qtiles = (int32_t)((a.G + kQRows - 1) / kQRows);
+  a.q_rows = p.q_rows;
+  a.qtiles = (a.G + a.q_rows - 1) / a.q_rows;
   a.nblocks = p.blocks;
   a.window = p.window;
   return status_of(bl::launch_paged_attn(a, q_dtype == BL_DTYPE_BF16, (hipStream_t)stream));

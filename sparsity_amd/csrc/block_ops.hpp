@@ -118,13 +118,14 @@ struct AttnArgs {
   int64_t blocks_per_seq;
   void* out;             // [B][Hq][D]
   float* lse;            // [B][Hq] or nullptr
-  float* part;           // [2 * nblocks][min(G, 16)][D] sums of runs of keys
-  float* ml;             // [2 * nblocks][2][16] their running maximum and sum
+  float* part;           // [2 * nblocks][min(G, q_rows)][D] sums of runs of keys
+  float* ml;             // [2 * nblocks][2][q_rows] their running maximum and sum
   uint32_t* ticket;      // [B * key heads * qtiles] arrivals, zero between launches
   int64_t B;
-  int32_t Hq, G, qtiles, nblocks, window;
+  int32_t Hq, G, q_rows, qtiles, nblocks, window;
 };
-int paged_attn_blocks(int64_t head_dim);   // blocks that fill the chip
+// Fills q_rows and blocks of a plan whose other sizes are set.
+void paged_attn_split(bl_attn_plan& p);
 hipError_t launch_paged_attn(const AttnArgs& a, bool q_bf16, hipStream_t s);
 
 }  // namespace bl

@@ -8,8 +8,8 @@
 // key head), so the kernel is bound by memory: the work is to keep loads in flight and to spend
 // little on each byte.
 //
-// A wave takes 32 keys at a time (64 of an int8 cache) for up to 16 query heads of one key head, the
-// running maximum and sum of the softmax in registers:
+// A wave takes 32 keys at a time (64 of an int8 cache) for up to 16 query heads of one key head (32 in
+// two tiles, see paged_attn_split), the running maximum and sum of the softmax in registers:
 //   S^T = K Q^T   16x16x32 MFMAs with 16 keys as rows.  A lane's operand is 16 contiguous bytes of
 //                 its key's row, straight from memory.  Lane (g, n) (g = lane / 16, n = lane % 16)
 //                 receives the scores of query n and keys 4g..4g+3 of each 16-key tile.
@@ -24,7 +24,7 @@
 // of it): two where the output is bf16, good to 2^-17, three for fp32 queries and output; an fp32
 // query's three terms hold it exactly.  The matrix cores are idle enough that this costs nothing.
 //
-// The launch is one block per resident place of the chip (two per CU: a wave then has 16 KB of keys and
+// The launch is one block per resident place of the chip (two per CU, one where registers ask for it: a wave then has 16 KB of keys and
 // values in flight while the matrix cores work on the last 16; three waves per SIMD spill, one leaves
 // int8 caches at half the rate).  The blocks share all keys of all sequences evenly (see Work), the
 // four waves of a block take quarters of its run and join in LDS; a run that is not its group's whole
@@ -46,7 +46,7 @@ namespace bl {
 namespace {
 
 constexpr int kWaves = 4;
-constexpr int kQ = 16;                      // query heads of a block
+constexpr int kQ = 16;                      // query heads of an MFMA
 constexpr int64_t kTile = 32 * kWaves;      // keys of a tile: one group of 32 per wave
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -108,7 +108,7 @@ __device__ __forceinline__ void load_dw(const void* p, uint32_t* r) {
 
 // Resident blocks per CU (one wave of each per SIMD) that the registers allow without spilling (but for
 // 168 bytes of fp32 queries over an int8 cache at D = 256).
-constexpr int resident(int DT) { return DT <= 128 ? 2 : 1; }
+constexpr int resident(int DT, int QT) { return DT * QT <= 128 ? 2 : 1; }
 
 // The work of a launch as one run of units: sequence after sequence, group (key head and query tile)
 // after group, each the cost of starting and ending a group, kStart units, and then its tiles of
@@ -156,9 +156,10 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, int64_t b) {
   return s;
 }
 
-// DT: 64, 128 or 256, the head dimension's room.  I8: int8 cache.  QF: fp32 queries.
-template <int DT, bool I8, bool QF>
-__global__ __launch_bounds__(64 * kWaves, resident(DT)) void paged_attn_kernel(AttnArgs a) {
+// DT: 64, 128 or 256, the head dimension's room.  I8: int8 cache.  QF: fp32 queries.  QT: query tiles.
+template <int DT, bool I8, bool QF, int QT>
+__global__ __launch_bounds__(64 * kWaves, resident(DT, QT)) void paged_attn_kernel(AttnArgs a) {
+  constexpr int R = kQ * QT;                // query heads of a block
   constexpr int EB = I8 ? 1 : 2;            // bytes per cache element
   constexpr int VE = DT / 16;               // value elements per lane and key
   constexpr int VW = VE * EB / 4;           // their dwords
@@ -170,8 +171,8 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT)) void paged_attn_kernel(A
   constexpr int KG = I8 ? 2 : 1;            // runs of 32 keys a wave takes at a time: 16 KB at D = 128
   constexpr int GK = 32 * KG;
 
-  __shared__ __attribute__((aligned(16))) float sm_o[kWaves][kQ][DT + 4];   // the waves' sums
-  __shared__ float sm_m[kWaves][kQ], sm_l[kWaves][kQ];
+  __shared__ __attribute__((aligned(16))) float sm_o[kWaves][R][DT + 4];   // the waves' sums
+  __shared__ float sm_m[kWaves][R], sm_l[kWaves][R];
   // per-wave rings of two groups of keys: byte offsets of the keys' rows (-1: masked), scales
   __shared__ __attribute__((aligned(16))) int64_t ring[kWaves][2][GK];
   __shared__ __attribute__((aligned(16))) float sring[I8 ? kWaves : 1][2][I8 ? GK : 1];
@@ -181,7 +182,7 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT)) void paged_attn_kernel(A
   const int g = lane >> 4, n = lane & 15;
   const int D = a.kv.head_dim;
   const int per_seq = a.kv.heads * a.qtiles;   // groups per sequence
-  const int prows = min(kQ, a.G);              // rows of a partial sum
+  const int prows = min(R, a.G);               // rows of a partial sum
 
   // this block's units [u0, u1), and the sequence of the first: sums over the lengths, 64 at a time
   constexpr int64_t kStart = start_units(DT, EB);
@@ -224,8 +225,8 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT)) void paged_attn_kernel(A
     const int hk = in_seq / a.qtiles, qt = in_seq - hk * a.qtiles;
     const int64_t owner0 = work.owner(g0);
     const int active = (int)(work.owner(g0 + tiles - 1) - owner0) + 1;   // blocks that share the group
-    const int rows = min(kQ, a.G - qt * kQ);              // live query heads
-    const int hq0 = hk * a.G + qt * kQ;
+    const int rows = min(R, a.G - qt * R);                // live query heads
+    const int hq0 = hk * a.G + qt * R;
     const int64_t k0 = sp.first + (tile - g0) * kTile, k1 = min(sp.len, sp.first + (end - g0) * kTile);
     // this wave's quarter, in whole runs of 32 keys
     const int64_t quarter = ((k1 - k0 + kWaves - 1) / kWaves + 31) / 32 * 32;
@@ -248,21 +249,22 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT)) void paged_attn_kernel(A
     const int32_t page0 = page_of(0);
     int32_t next = page_of(1);
 
-    // queries, as they lie in memory: operand c of lane (g, n), eight elements of head n (zero past the
-    // live heads and past D)
-    uint4 qraw[KC][QF ? 2 : 1];
+    // queries, as they lie in memory: operand c of lane (g, n), eight elements of head 16 f + n (zero past
+    // the live heads and past D)
+    constexpr int QL = QF ? 2 : 1;            // 16-byte loads
+    uint4 qraw[QT][KC][QL];
 #pragma unroll
-    for (int c = 0; c < KC; ++c) {
-      // the int8 cache reads 16 elements per lane, so its steps come in pairs of adjacent eights
-      const int d = I8 ? 64 * (c / 2) + 16 * g + 8 * (c & 1) : 32 * c + 8 * g;
+    for (int f = 0; f < QT; ++f)
 #pragma unroll
-      for (int e = 0; e < (QF ? 2 : 1); ++e) qraw[c][e] = make_uint4(0, 0, 0, 0);
-      if (n < rows && d < D) {
-        const char* p = (const char*)a.q + (sq * a.q_tok + (int64_t)(hq0 + n) * a.q_head + d) * (QF ? 4 : 2);
+      for (int c = 0; c < KC; ++c) {
+        // the int8 cache reads 16 elements per lane, so its steps come in pairs of adjacent eights
+        const int d = I8 ? 64 * (c / 2) + 16 * g + 8 * (c & 1) : 32 * c + 8 * g;
+        const int h = kQ * f + n;
+        const char* p = (const char*)a.q + (sq * a.q_tok + (int64_t)(hq0 + h) * a.q_head + d) * (QF ? 4 : 2);
 #pragma unroll
-        for (int e = 0; e < (QF ? 2 : 1); ++e) qraw[c][e] = ((const uint4*)p)[e];
+        for (int e = 0; e < QL; ++e)
+          qraw[f][c][e] = h < rows && d < D ? ((const uint4*)p)[e] : make_uint4(0, 0, 0, 0);
       }
-    }
 
     // scales of the lane's key and value, on their way to LDS, and whether the key is live
     float scl[2] = {0.f, 0.f};
@@ -330,10 +332,15 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT)) void paged_attn_kernel(A
       }
     };
 
-    v4f o[VE];
+    v4f o[QT][VE];
+    float m[QT], l[QT];
 #pragma unroll
-    for (int j = 0; j < VE; ++j) o[j] = v4f{0.f, 0.f, 0.f, 0.f};
-    float m = -INFINITY, l = 0.f;
+    for (int f = 0; f < QT; ++f) {
+      m[f] = -INFINITY;
+      l[f] = 0.f;
+#pragma unroll
+      for (int j = 0; j < VE; ++j) o[f][j] = v4f{0.f, 0.f, 0.f, 0.f};
+    }
 
     if (groups > 0) {
       put_rows(0, page0);
@@ -341,30 +348,32 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT)) void paged_attn_kernel(A
       load_v(0);
     }
     // the queries as bf16 terms, each what the ones before leave
-    bf16x8 qf[QS][KC];
+    bf16x8 qf[QT][QS][KC];
 #pragma unroll
-    for (int c = 0; c < KC; ++c) {
-      if constexpr (QF) {
-        float v[8];
-        const uint4 lo = qraw[c][0], hi = qraw[c][1];
-        const uint32_t bits[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    for (int f = 0; f < QT; ++f)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(bits[j]);
+      for (int c = 0; c < KC; ++c) {
+        if constexpr (QF) {
+          float v[8];
+          const uint4 lo = qraw[f][c][0], hi = qraw[f][c][1];
+          const uint32_t bits[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-        for (int t = 0; t < QS; ++t) {
-          uint32_t w[4];
+          for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(bits[j]);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
-            v[2 * j] -= bf16_lo(w[j]);
-            v[2 * j + 1] -= bf16_hi(w[j]);
+          for (int t = 0; t < QS; ++t) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+              v[2 * j] -= bf16_lo(w[j]);
+              v[2 * j + 1] -= bf16_hi(w[j]);
+            }
+            qf[f][t][c] = frag(w[0], w[1], w[2], w[3]);
           }
-          qf[t][c] = frag(w[0], w[1], w[2], w[3]);
+        } else {
+          qf[f][0][c] = __builtin_bit_cast(bf16x8, qraw[f][c][0]);
         }
-      } else {
-        qf[0][c] = __builtin_bit_cast(bf16x8, qraw[c][0]);
       }
-    }
     if (groups > 0) {
       for (int i = 0; i < groups; ++i) {
         const bool more = i + 1 < groups;
@@ -376,7 +385,7 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT)) void paged_attn_kernel(A
           __builtin_amdgcn_wave_barrier();
         }
         // scores
-        float x[KG][8], mx = -INFINITY;
+        float x[QT][KG][8];
         bool full = true;
 #pragma unroll
         for (int u = 0; u < KG; ++u) {
@@ -384,7 +393,9 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT)) void paged_attn_kernel(A
           full = full && __all(live[u] == 0xFF);
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            v4f s = v4f{0.f, 0.f, 0.f, 0.f}, rest = v4f{0.f, 0.f, 0.f, 0.f};
+            v4f s[QT], rest[QT];
+#pragma unroll
+            for (int f = 0; f < QT; ++f) s[f] = rest[f] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int c = 0; c < KC; ++c) {
               bf16x8 kf;
@@ -396,17 +407,22 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT)) void paged_attn_kernel(A
               } else {
                 kf = frag(kr[u][t][4 * c], kr[u][t][4 * c + 1], kr[u][t][4 * c + 2], kr[u][t][4 * c + 3]);
               }
-              s = mfma_bf16(kf, qf[0][c], s);
 #pragma unroll
-              for (int e = 1; e < QS; ++e) rest = mfma_bf16(kf, qf[e][c], rest);
+              for (int f = 0; f < QT; ++f) {
+                s[f] = mfma_bf16(kf, qf[f][0][c], s[f]);
+#pragma unroll
+                for (int e = 1; e < QS; ++e) rest[f] = mfma_bf16(kf, qf[f][e][c], rest[f]);
+              }
             }
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              float v = s[r];
-              // an infinite key times a query's zero or negative remainder would spoil its score
-              if constexpr (QF) v = __builtin_isfinite(v) ? v + rest[r] : v;
-              x[u][4 * t + r] = v * a.scale_log2;
-            }
+            for (int f = 0; f < QT; ++f)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                float v = s[f][r];
+                // an infinite key times a query's zero or negative remainder would spoil its score
+                if constexpr (QF) v = __builtin_isfinite(v) ? v + rest[f][r] : v;
+                x[f][u][4 * t + r] = v * a.scale_log2;
+              }
           }
         }
         if (more) {
@@ -414,48 +430,61 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT)) void paged_attn_kernel(A
           load_k(i + 1);
           next = page_of(i + 2);
         }
+        float mx[QT];
+        bool rise = false;
 #pragma unroll
-        for (int u = 0; u < KG; ++u)
+        for (int f = 0; f < QT; ++f) {
+          mx[f] = -INFINITY;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            if constexpr (I8) x[u][k] *= sring[wave][0][32 * u + 16 * (k / 4) + 4 * g + (k & 3)];
-            if (!full && !((live[u] >> k) & 1)) x[u][k] = -INFINITY;
-            mx = fmaxf(mx, x[u][k]);
-          }
-        if (__any(mx > m)) {                  // a new maximum: shared by the four lanes of a query
-          mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
-          mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-          const float top = fmaxf(m, mx);
-          const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top);
-          m = top;
-          l *= f;
+          for (int u = 0; u < KG; ++u)
 #pragma unroll
-          for (int j = 0; j < VE; ++j) o[j] *= f;
+            for (int k = 0; k < 8; ++k) {
+              float& v = x[f][u][k];
+              if constexpr (I8) v *= sring[wave][0][32 * u + 16 * (k / 4) + 4 * g + (k & 3)];
+              if (!full && !((live[u] >> k) & 1)) v = -INFINITY;
+              mx[f] = fmaxf(mx[f], v);
+            }
+          rise = rise || mx[f] > m[f];
         }
-        const float base = m == -INFINITY ? 0.f : m;
+        if (__any(rise)) {                    // a new maximum: shared by the four lanes of a query
+#pragma unroll
+          for (int f = 0; f < QT; ++f) {
+            float top = fmaxf(mx[f], __shfl_xor(mx[f], 16, 64));
+            top = fmaxf(m[f], fmaxf(top, __shfl_xor(top, 32, 64)));
+            const float fall = m[f] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[f] - top);
+            m[f] = top;
+            l[f] *= fall;
+#pragma unroll
+            for (int j = 0; j < VE; ++j) o[f][j] *= fall;
+          }
+        }
 #pragma unroll
         for (int u = 0; u < KG; ++u) {
-          uint32_t pw[PS][4];
+          bf16x8 pf[QT][PS];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float p0 = __builtin_amdgcn_exp2f(x[u][2 * k] - base);
-            float p1 = __builtin_amdgcn_exp2f(x[u][2 * k + 1] - base);
-            l += p0 + p1;
-            if constexpr (I8) {
-              const float* vs = &sring[wave][1][32 * u + 16 * (k / 2) + 4 * g + (2 * k & 3)];
-              p0 *= vs[0];
-              p1 *= vs[1];
+          for (int f = 0; f < QT; ++f) {
+            const float base = m[f] == -INFINITY ? 0.f : m[f];
+            uint32_t pw[PS][4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float p0 = __builtin_amdgcn_exp2f(x[f][u][2 * k] - base);
+              float p1 = __builtin_amdgcn_exp2f(x[f][u][2 * k + 1] - base);
+              l[f] += p0 + p1;
+              if constexpr (I8) {
+                const float* vs = &sring[wave][1][32 * u + 16 * (k / 2) + 4 * g + (2 * k & 3)];
+                p0 *= vs[0];
+                p1 *= vs[1];
+              }
+#pragma unroll
+              for (int e = 0; e < PS; ++e) {
+                pw[e][k] = pack_bf16(p0, p1);
+                p0 -= bf16_lo(pw[e][k]);
+                p1 -= bf16_hi(pw[e][k]);
+              }
             }
 #pragma unroll
-            for (int e = 0; e < PS; ++e) {
-              pw[e][k] = pack_bf16(p0, p1);
-              p0 -= bf16_lo(pw[e][k]);
-              p1 -= bf16_hi(pw[e][k]);
-            }
+            for (int e = 0; e < PS; ++e) pf[f][e] = frag(pw[e][0], pw[e][1], pw[e][2], pw[e][3]);
           }
-          bf16x8 pf[PS];
-#pragma unroll
-          for (int e = 0; e < PS; ++e) pf[e] = frag(pw[e][0], pw[e][1], pw[e][2], pw[e][3]);
           if (!full) {                        // a masked row may hold anything: 0 * NaN is not 0
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -474,23 +503,27 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT)) void paged_attn_kernel(A
             }
             const bf16x8 vf = frag(w[0], w[1], w[2], w[3]);
 #pragma unroll
-            for (int e = 0; e < PS; ++e) o[j] = mfma_bf16(vf, pf[e], o[j]);
+            for (int f = 0; f < QT; ++f)
+#pragma unroll
+              for (int e = 0; e < PS; ++e) o[f][j] = mfma_bf16(vf, pf[f][e], o[f][j]);
           }
         }
         if (more) load_v(i + 1);
       }
     }
-    l += __shfl_xor(l, 16, 64);
-    l += __shfl_xor(l, 32, 64);
-
     const int tid = here(threadIdx.x), tl = tid & 63, tw = tid >> 6;
-    // join the waves.  Lane (g, n) holds elements VE (4g + r) + j of head n.
-    if (n < rows) {
-      if (g == 0) { sm_m[wave][n] = m; sm_l[wave][n] = l; }
+    // join the waves.  Lane (g, n) holds elements VE (4g + r) + j of head 16 f + n.
+#pragma unroll
+    for (int f = 0; f < QT; ++f) {
+      const int h = kQ * f + n;
+      l[f] += __shfl_xor(l[f], 16, 64);
+      l[f] += __shfl_xor(l[f], 32, 64);
+      if (h >= rows) continue;
+      if (g == 0) { sm_m[wave][h] = m[f]; sm_l[wave][h] = l[f]; }
 #pragma unroll
       for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int j = 0; j < VE; ++j) sm_o[wave][n][VE * (4 * g + r) + j] = o[j][r];
+        for (int j = 0; j < VE; ++j) sm_o[wave][h][VE * (4 * g + r) + j] = o[f][j][r];
     }
     __syncthreads();
     const int64_t orow = (sq * a.Hq + hq0) * (int64_t)D;
@@ -505,7 +538,7 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT)) void paged_attn_kernel(A
     // a block's partial sums: place 0 for a group that an earlier block began, 1 for one it begins
     const int64_t place = 2 * (int64_t)blockIdx.x + (owner0 == (int64_t)blockIdx.x);
     float* part = a.part + place * prows * D;   // [prows][D]
-    float* ml = a.ml + place * 2 * kQ;          // [2][kQ]
+    float* ml = a.ml + place * 2 * R;           // [2][R]
     for (int e = tid; e < rows * D; e += 64 * kWaves) {
       const int h = e / D, d = e - h * D;
       float top = sm_m[0][h];
@@ -522,7 +555,7 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT)) void paged_attn_kernel(A
         finish(h, d, num, den, top);
       } else {
         put(part + h * D + d, num);
-        if (d == 0) { put(ml + h, top); put(ml + kQ + h, den); }
+        if (d == 0) { put(ml + h, top); put(ml + R + h, den); }
       }
     }
     if (active > 1) {
@@ -548,7 +581,7 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT)) void paged_attn_kernel(A
         // order.  The first runs' sums, maxima and columns are all asked for before any is used: a
         // round trip to memory is most of what a join of few runs costs.
         constexpr int kCols = 512;
-        constexpr int kRoom = kWaves * kQ * (DT + 4) - kWaves * kCols;
+        constexpr int kRoom = kWaves * R * (DT + 4) - kWaves * kCols;
         float* wt = &sm_o[0][0][0];               // [rows][at]
         float* sums = wt + kRoom;                 // [kWaves][kCols]
         const int at = kRoom / rows;
@@ -557,17 +590,17 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT)) void paged_attn_kernel(A
         auto column = [&](int s, int e) {
           return e < cols ? get4(a.part + run(s) * prows * D + e) : v4f{0.f, 0.f, 0.f, 0.f};
         };
-        // thread (i, row): runs i, i + 16, ... of a row, the first kHeld of them in registers
-        constexpr int kHeld = 4, kAhead = 4;
-        const int hrow = tid & (kQ - 1), i0 = tid / kQ;
+        // thread (i, row): runs i, i + kSlots, ... of a row, the first kHeld of them in registers
+        constexpr int kHeld = 4, kAhead = 4, kSlots = 64 * kWaves / R;
+        const int hrow = tid & (R - 1), i0 = tid / R;
         float hm[kHeld], hl[kHeld];
 #pragma unroll
         for (int k = 0; k < kHeld; ++k) {
-          const int s = i0 + 16 * k;
+          const int s = i0 + kSlots * k;
           const bool in = hrow < rows && s < active;
-          const float* p = a.ml + run(in ? s : 0) * 2 * kQ + hrow;
+          const float* p = a.ml + run(in ? s : 0) * 2 * R + hrow;
           hm[k] = in ? get(p) : -INFINITY;
-          hl[k] = in ? get(p + kQ) : 0.f;
+          hl[k] = in ? get(p + R) : 0.f;
         }
         v4f ahead[kAhead][2];
 #pragma unroll
@@ -580,15 +613,16 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT)) void paged_attn_kernel(A
 #pragma unroll
         for (int k = 0; k < kHeld; ++k) top = fmaxf(top, hm[k]);
         if (hrow < rows)
-          for (int s = i0 + 16 * kHeld; s < active; s += 16) top = fmaxf(top, get(a.ml + run(s) * 2 * kQ + hrow));
-        auto over_rows = [&](float v, auto op) {  // of the 16 threads of each row
-          v = op(v, __shfl_xor(v, 16, 64));
+          for (int s = i0 + kSlots * kHeld; s < active; s += kSlots)
+            top = fmaxf(top, get(a.ml + run(s) * 2 * R + hrow));
+        auto over_rows = [&](float v, auto op) {  // of the kSlots threads of each row
+          if constexpr (QT == 1) v = op(v, __shfl_xor(v, 16, 64));
           v = op(v, __shfl_xor(v, 32, 64));
           __syncthreads();
-          if (tl < kQ) sums[kQ * tw + tl] = v;
+          if (tl < R) sums[R * tw + tl] = v;
           __syncthreads();
 #pragma unroll
-          for (int w = 0; w < kWaves; ++w) v = w ? op(v, sums[kQ * w + hrow]) : sums[hrow];
+          for (int w = 0; w < kWaves; ++w) v = w ? op(v, sums[R * w + hrow]) : sums[hrow];
           return v;
         };
         top = over_rows(top, [](float x, float y) { return fmaxf(x, y); });
@@ -611,12 +645,12 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT)) void paged_attn_kernel(A
                 int s = i0;
                 if (s0 == 0) {
 #pragma unroll
-                  for (int k = 0; k < kHeld; ++k, s += 16)
+                  for (int k = 0; k < kHeld; ++k, s += kSlots)
                     if (s < ns) put_weight(s, hm[k], hl[k]);
                 }
-                for (; s < ns; s += 16) {
-                  const float* p = a.ml + run(s0 + s) * 2 * kQ + hrow;
-                  put_weight(s, get(p), get(p + kQ));
+                for (; s < ns; s += kSlots) {
+                  const float* p = a.ml + run(s0 + s) * 2 * R + hrow;
+                  put_weight(s, get(p), get(p + R));
                 }
               }
               __syncthreads();
@@ -638,7 +672,7 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT)) void paged_attn_kernel(A
           }
           if (j == 0) {
             den = over_rows(den, [](float x, float y) { return x + y; });
-            if (tid < kQ) { sm_l[0][hrow] = den; sm_m[0][hrow] = top; }
+            if (tid < R) { sm_l[0][hrow] = den; sm_m[0][hrow] = top; }
             __syncthreads();                      // sums is free again
           }
           *(v4f*)(sums + kCols * tw + 4 * tl) = num[0];
@@ -663,30 +697,49 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT)) void paged_attn_kernel(A
   }
 }
 
-template <int DT>
+template <int DT, int QT>
 hipError_t launch_attn_t(const AttnArgs& a, bool q_bf16, hipStream_t s) {
-  const dim3 grid((unsigned)a.nblocks);
+  const dim3 grid((unsigned)a.nblocks), block(64 * kWaves);
   const bool i8 = a.kv.dtype == BL_DTYPE_I8;
   if (q_bf16) {
-    if (i8) paged_attn_kernel<DT, true, false><<<grid, 64 * kWaves, 0, s>>>(a);
-    else paged_attn_kernel<DT, false, false><<<grid, 64 * kWaves, 0, s>>>(a);
+    if (i8) paged_attn_kernel<DT, true, false, QT><<<grid, block, 0, s>>>(a);
+    else paged_attn_kernel<DT, false, false, QT><<<grid, block, 0, s>>>(a);
   } else {
-    if (i8) paged_attn_kernel<DT, true, true><<<grid, 64 * kWaves, 0, s>>>(a);
-    else paged_attn_kernel<DT, false, true><<<grid, 64 * kWaves, 0, s>>>(a);
+    if (i8) paged_attn_kernel<DT, true, true, QT><<<grid, block, 0, s>>>(a);
+    else paged_attn_kernel<DT, false, true, QT><<<grid, block, 0, s>>>(a);
   }
   return hipGetLastError();
 }
 
 }  // namespace
 
-int paged_attn_blocks(int64_t head_dim) {
-  return 256 * resident(head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256);
+// A block takes two query tiles where a key head has more than 16 query heads: its keys and values are
+// then read once for 32 of them (D > 128 has no registers for it).  It also doubles what is joined, by
+// half the blocks, so a small batch of few groups stays at one tile.  24 query heads over one key head,
+// one tile against two, us at head dimensions 64 and 128: 64 sequences of 64000 tokens 299 : 209 and
+// 590 : 388, 64 of 4000 33 : 30 and 56 : 49, 16 of 16000 28 : 35 and 50 : 50, 64 of 1000 19 : 23 and 29 : 29,
+// 2 of 64000 44 : 94 and 60 : 83.
+void paged_attn_split(bl_attn_plan& p) {
+  const int64_t G = p.q_heads / p.kv_heads, D = p.head_dim;
+  const int64_t keys = p.window ? std::min<int64_t>(p.window, p.max_len) : p.max_len;
+  const int64_t tiles = (keys + kTile - 1) / kTile, pairs = p.B * p.kv_heads;
+  const int64_t many = std::min<int64_t>(pairs, 256);
+  const bool two = G > kQ && D <= 128 && pairs * tiles >= 1024 && many * many * tiles >= 1 << 16;
+  p.q_rows = two ? 2 * kQ : kQ;
+  // a block per resident place of the chip, fewer where there is less work: tiles of keys, and the
+  // start of a group as so many more (at most six: start_units)
+  const int64_t groups = pairs * ((G + p.q_rows - 1) / p.q_rows);
+  const int64_t places = 256 * resident(D <= 64 ? 64 : D <= 128 ? 128 : 256, two ? 2 : 1);
+  p.blocks = (int32_t)std::max<int64_t>(1, std::min(places, groups * (tiles + 6)));
 }
 
 hipError_t launch_paged_attn(const AttnArgs& a, bool q_bf16, hipStream_t s) {
-  if (a.kv.head_dim <= 64) return launch_attn_t<64>(a, q_bf16, s);
-  if (a.kv.head_dim <= 128) return launch_attn_t<128>(a, q_bf16, s);
-  return launch_attn_t<256>(a, q_bf16, s);
+  const int D = a.kv.head_dim;
+  if (a.q_rows == 2 * kQ)
+    return D <= 64 ? launch_attn_t<64, 2>(a, q_bf16, s) : launch_attn_t<128, 2>(a, q_bf16, s);
+  if (D <= 64) return launch_attn_t<64, 1>(a, q_bf16, s);
+  if (D <= 128) return launch_attn_t<128, 1>(a, q_bf16, s);
+  return launch_attn_t<256, 1>(a, q_bf16, s);
 }
 
 }  // namespace bl

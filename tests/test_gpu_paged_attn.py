@@ -239,3 +239,43 @@ def test_order_of_blocks_does_not_matter_and_graph_replays():
         gr.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, first) and torch.equal(lo, lse)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "i8"])
+@pytest.mark.parametrize("qd", ["bf16", "f32"])
+@pytest.mark.parametrize("B,Hq,Hk,D,ps,top", [(3, 17, 1, 128, 16, 1200), (2, 96, 3, 64, 20, 700),
+                                              (4, 33, 1, 40, 8, 129), (1, 71, 1, 96, 64, 3000),
+                                              (2, 40, 2, 128, 12, 64)])
+def test_two_query_tiles_per_block(kv, qd, B, Hq, Hk, D, ps, top):
+    """More than 16 query heads on a key head under a bound of lengths that calls for one reading of the
+    keys by 32 of them: within the bound, dead slots may hold anything, and a batch split at its own,
+    short bound (one query tile per block) agrees."""
+    D = -(-D // 16) * 16 if kv == "i8" else D   # rows of 16 bytes
+    g = rng(B * 17 + Hq + top)
+    per = -(-top // ps) + 1
+    pages = B * per + 1                        # page 0 is masked from the start
+    c = Cache(g, pages, Hk, ps, D, kv)
+    blocks = 1 + g.permutation(pages - 1)[:B * per].reshape(B, per).astype(np.int32)
+    lens = g.integers(0, top + 1, B).astype(np.int32)
+    lens[0] = top
+    blocks[0, 0] = -1                          # a hole: its keys are dead as well
+    dead = np.ones((pages, ps), bool)
+    for b in range(B):
+        for t in range(int(lens[b])):
+            if blocks[b, t // ps] >= 0:
+                dead[blocks[b, t // ps], t % ps] = False
+    sel = dev(np.broadcast_to(dead[:, None], (pages, Hk, ps)).copy())
+    for t in ((c.kt, c.vt) if kv == "bf16" else (c.kst, c.vst)):
+        t[sel] = float("nan")
+    if qd == "bf16":
+        q, qt = _bf16(g.standard_normal((B, Hq, D)))
+    else:
+        q = g.standard_normal((B, Hq, D)).astype(np.float32)
+        qt = dev(q)
+    bound = 128 * (1 << 16) // (B * Hk) ** 2 + 1024 * 128
+    wide, near = S.PagedAttn(B, Hq, Hk, D, ps, bound), S.PagedAttn(B, Hq, Hk, D, ps, top)
+    assert (wide.plan.q_rows, near.plan.q_rows) == (32, 16)
+    print(kv, qd, B, Hq, Hk, D, ps, top, wide.plan.blocks, flush=True)
+    for plan in (wide, near, wide):
+        out, lse = plan(qt, c.kt, c.vt, dev(blocks), dev(lens), k_scale=c.kst, v_scale=c.vst, want_lse=True)
+        _check(out, lse, q, c, blocks, lens, bf16=qd == "bf16")
