@@ -553,7 +553,8 @@ int bitlinear_norm_quant(const void* x, int x_dtype, const void* res, int res_dt
  *   dw = sum_t dn * h*rstd   (fp32 [K]; NULL: not computed)
  * Sums are fp32 in a fixed order: results do not vary from run to run.  dh may be dres itself, or
  * dn where the types agree.  ws: bitlinear_norm_quant_bwd_workspace_bytes of device scratch (16-byte
- * aligned; contents on entry irrelevant), not needed (NULL, 0) without dw or where that is 0.  T == 0 writes dw = 0.
+ * aligned; contents on entry irrelevant), not needed (NULL, 0) without dw or where that is 0.  T == 0
+ * writes dw = 0.
  * One launch, and a second one for dw unless the rows are few. */
 int bitlinear_norm_quant_bwd_workspace_bytes(int64_t T, int64_t K, size_t* ws_bytes);
 int bitlinear_norm_quant_bwd(const void* dn, int dn_dtype, const void* h, int h_dtype,

@@ -151,13 +151,14 @@ void launch_norm_wp(const NormArgs& a, hipStream_t s) {
 }
 
 // Waves per row.  Many rows: the fewest that leave a lane two pieces (8192 x 3200: four waves 44.6 us,
-// two 49.5, one 54.2, sixteen 62.1).  Few rows, where latency counts: one piece per lane, up to eight
+// two 49.5, one 54.2, sixteen 62.1; 10922 x 1536: two 21.9, four 24.0).  Few rows, where latency counts: one piece per lane, up to eight
 // waves (1 x 2560: eight 3.07 us, four 3.27, sixteen 3.60; 1 x 8192: eight 3.80, sixteen 4.13).
 template <bool XBF, int RES>
 hipError_t launch_norm_t(const NormArgs& a, hipStream_t s) {
   const int pieces = a.K / 8, most = a.T < 1024 ? 64 : 128;   // pieces per wave
   if (pieces <= 64) launch_norm_wp<XBF, RES, 1, 1>(a, s);
   else if (pieces <= most) launch_norm_wp<XBF, RES, 1, 2>(a, s);
+  else if (pieces <= 256 && a.T >= 1024) launch_norm_wp<XBF, RES, 2, 2>(a, s);
   else if (pieces <= 256) launch_norm_wp<XBF, RES, 4, 1>(a, s);
   else if (pieces <= 4 * most) launch_norm_wp<XBF, RES, 4, 2>(a, s);
   else if (pieces <= 512) launch_norm_wp<XBF, RES, 8, 1>(a, s);
@@ -186,10 +187,11 @@ hipError_t launch_norm_quant(const NormArgs& a, bool x_bf16, bool res_bf16, hipS
 // two ways.  Many rows: each block walks rows and keeps its columns' sums in registers, and a second
 // launch adds the blocks'.  Few rows: blocks of their own read dn and h once more, from the caches, and
 // sum 64 columns each over all rows, in the same launch and without a workspace.
-// Teams of W waves take a row each; 16 waves and 512 blocks keep the blocks' sums (6.5 MB at K = 3200)
-// small beside the rows.  Asking for a row ahead spilled registers and more than doubled the time.
+// Teams of W waves take a row each, 16 waves a block, one block per CU: two per CU read no faster and
+// double the sums (6553 x 2560: 41.8 us against 39.8, 1638 x 2560: 17.7 against 14.4).  Two rows per team
+// at a time gain nothing (39.6), a row asked for ahead spills and more than doubles the time.
 //
-// Measured: 8192 x 3200, fp32 dn, bf16 h, dres and dh: 50 us for the rows, 5.4 TB/s, 4.8 us for dw.
+// Measured: 8192 x 3200, fp32 dn, bf16 h, dres and dh: 48 us for the rows, 5.5 TB/s, 4.8 us for dw.
 // ---------------------------------------------------------------------------------------------
 namespace {
 
@@ -353,17 +355,20 @@ __global__ __launch_bounds__(256) void norm_dw_kernel(const float* __restrict__ 
   }
 }
 
+// As many waves per row as leave few lanes without a piece, up to two pieces each (4088 x 4104: 16 waves of
+// one piece 47 us, eight of two 39; 31775 x 528: four waves 69 us, two 47).
 template <bool GBF, bool HBF, bool OBF>
 hipError_t launch_rows(const NormBwdArgs& a, int columns, hipStream_t s) {
   const int pieces = a.K / 8;
   const dim3 grid((unsigned)(a.blocks + columns)), block(1024);
   if (grid.x == 0) return hipSuccess;
-  // more than 512 pieces: one team, no sums to join
-  const size_t lds = columns ? kColumnLds : a.part && pieces <= 512 ? (size_t)a.K * 4 : 0;
+  // more than 1024 pieces: one team, no sums to join
+  const size_t lds = columns ? kColumnLds : a.part && pieces <= 1024 ? (size_t)a.K * 4 : 0;
   if (pieces <= 64) norm_bwd_kernel<GBF, HBF, OBF, 1, 1><<<grid, block, lds, s>>>(a);
+  else if (pieces <= 128) norm_bwd_kernel<GBF, HBF, OBF, 2, 1><<<grid, block, lds, s>>>(a);
   else if (pieces <= 256) norm_bwd_kernel<GBF, HBF, OBF, 4, 1><<<grid, block, lds, s>>>(a);
   else if (pieces <= 512) norm_bwd_kernel<GBF, HBF, OBF, 4, 2><<<grid, block, lds, s>>>(a);
-  else if (pieces <= 1024) norm_bwd_kernel<GBF, HBF, OBF, 16, 1><<<grid, block, lds, s>>>(a);
+  else if (pieces <= 1024) norm_bwd_kernel<GBF, HBF, OBF, 8, 2><<<grid, block, lds, s>>>(a);
   else if (pieces <= 2048) norm_bwd_kernel<GBF, HBF, OBF, 16, 2><<<grid, block, lds, s>>>(a);
   else norm_bwd_kernel<GBF, HBF, OBF, 16, 4><<<grid, block, lds, s>>>(a);
   return hipGetLastError();
@@ -390,14 +395,15 @@ hipError_t launch_bwd_t(NormBwdArgs a, hipStream_t s) {
 
 int norm_bwd_blocks(int64_t T, int64_t K) {
   const int64_t pieces = K / 8;
-  const int64_t rows = pieces <= 64 ? 16 : pieces <= 512 ? 4 : 1;   // rows a block takes at a time
-  return (int)std::min<int64_t>(512, (T + rows - 1) / rows);
+  // rows a block takes at a time
+  const int64_t rows = pieces <= 64 ? 16 : pieces <= 128 ? 8 : pieces <= 512 ? 4 : pieces <= 1024 ? 2 : 1;
+  return (int)std::min<int64_t>(256, (T + rows - 1) / rows);
 }
 
 // By columns while a block's walk over the rows is short and the second reading comes from the caches.
-// One launch against two, graph replays (calls one after another): 64 x 2560 4.3 us against 7.5 (10.9
-// against 15.2), 512 x 2560 6.6 against 10.1, 512 x 8192 13.9 against 18.8; 1024 x 2560 13.2 against
-// 11.9, 2048 x 512 13.3 against 8.5, 2048 x 8192 46 against 41.
+// One launch against two, graph replays (calls one after another): 64 x 2560 4.3 us against 7.5 (10.8
+// against 15.1), 512 x 2560 6.6 against 10.0, 512 x 8192 13.6 against 15.2; 1024 x 2560 13.2 against
+// 12.0, 2048 x 512 13.3 against 8.6, 2048 x 8192 45 against 38.
 bool norm_bwd_columns(int64_t T, int64_t K) { return T <= 768 && T * K <= (int64_t)1 << 22; }
 
 hipError_t launch_norm_bwd(const NormBwdArgs& a, bool dn_bf16, bool h_bf16, bool grad_bf16,

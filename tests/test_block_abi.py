@@ -53,7 +53,7 @@ def _bwd(**kw):
     (dict(dd=2), ENOTSUP), (dict(hd=-1), ENOTSUP), (dict(gd=2), ENOTSUP), (dict(K=12), EINVAL),
     (dict(K=1 << 16), ENOTSUP), (dict(T=-2), EINVAL), (dict(dn=None), EINVAL), (dict(h=P + 2), EINVAL),
     (dict(rstd=None), EINVAL), (dict(dh=None), EINVAL), (dict(dres=P + 6), EINVAL), (dict(w=P + 4), EINVAL),
-    (dict(dw=P + 8), EINVAL), (dict(ws=None), EINVAL), (dict(wsb=512 * 256 * 4 - 1), ENOSPC), (dict(wsb=0), ENOSPC),
+    (dict(dw=P + 8), EINVAL), (dict(ws=None), EINVAL), (dict(wsb=256 * 256 * 4 - 1), ENOSPC), (dict(wsb=0), ENOSPC),
     (dict(dh=P), EINVAL), (dict(dh=P + 4 * SLOT + 16), EINVAL), (dict(dh=P + SLOT), EINVAL),
     (dict(dw=P + 3 * SLOT), EINVAL), (dict(ws=P + 6 * SLOT), EINVAL), (dict(dw=P + 5 * SLOT), EINVAL),
     (dict(T=0, dw=None, dn=None, h=None), 0)])
@@ -65,7 +65,7 @@ def test_norm_grad_workspace():
     for T in (0, 1, 700):                                  # few rows: dw is summed by columns
         assert K.bitlinear_norm_quant_bwd_workspace_bytes(T, 3200) == (0, 0)
     st, most = K.bitlinear_norm_quant_bwd_workspace_bytes(1 << 20, 3200)
-    assert st == 0 and most == 512 * 3200 * 4
+    assert st == 0 and most == 256 * 3200 * 4
     assert K.bitlinear_norm_quant_bwd_workspace_bytes(1, 100)[0] == EINVAL
     assert K.bitlinear_norm_quant_bwd_workspace_bytes(1, 32776)[0] == ENOTSUP
 

@@ -34,7 +34,7 @@ def _f32(t):
 
 
 SIZES = [(1, 8), (1, 2560), (3, 512), (5, 520), (2, 4104), (1030, 264), (1025, 3200), (2, 8200),
-         (1, 16384), (2, 32768), (7, 6912),
+         (1027, 1032), (1100, 2040), (1, 16384), (2, 32768), (7, 6912),
          (1029, 1000), (1026, 4104)]
 
 
@@ -118,7 +118,8 @@ def _grad_bound(dn, h, rstd, w, dres, out, grad):
 
 @pytest.mark.parametrize("T,K", [(1, 8), (3, 512), (17, 520), (130, 2048), (1031, 264), (5, 4096),
                                  (6, 4104), (3, 8192), (2, 16384), (2, 32768), (700, 3200),
-                                 (2100, 2048), (20000, 256), (530, 8200), (300, 16384), (140, 32768)])
+                                 (2100, 2048), (20000, 256), (530, 8200), (300, 16384), (140, 32768),
+                                 (900, 1000), (1500, 1928), (801, 5008)])
 @pytest.mark.parametrize("dd,hd,gd,withres", [("f32", "bf16", "bf16", True), ("bf16", "f32", "f32", False),
                                               ("f32", "f32", "f32", True), ("bf16", "bf16", "bf16", False),
                                               ("f32", "bf16", "f32", True)])
