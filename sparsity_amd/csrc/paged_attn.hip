@@ -106,8 +106,7 @@ __device__ __forceinline__ void load_dw(const void* p, uint32_t* r) {
   }
 }
 
-// Resident blocks per CU (one wave of each per SIMD) that the registers allow without spilling (but for
-// 168 bytes of fp32 queries over an int8 cache at D = 256).
+// Resident blocks per CU (one wave of each per SIMD) that the registers allow without spilling.
 constexpr int resident(int DT, int QT) { return DT * QT <= 128 ? 2 : 1; }
 
 // The work of a launch as one run of units: sequence after sequence, group (key head and query tile)
@@ -168,7 +167,9 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT, QT)) void paged_attn_kern
   constexpr int KW = DT * EB / 16;          // key dwords per lane and key tile
   constexpr int QS = QF ? 3 : 1;            // bf16 terms of a query element
   constexpr int PS = QF ? 3 : 2;            // and of a probability
-  constexpr int KG = I8 ? 2 : 1;            // runs of 32 keys a wave takes at a time: 16 KB at D = 128
+  // runs of 32 keys a wave takes at a time: 16 KB at D = 128 (fp32 queries at D = 256 leave no registers
+  // for two: 64 x 8000 tokens 589 us with spills, 424 with one)
+  constexpr int KG = I8 && !(DT > 128 && QF) ? 2 : 1;
   constexpr int GK = 32 * KG;
 
   __shared__ __attribute__((aligned(16))) float sm_o[kWaves][R][DT + 4];   // the waves' sums
@@ -379,8 +380,8 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT, QT)) void paged_attn_kern
         const bool more = i + 1 < groups;
         if constexpr (I8) {
           __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-          sring[wave][0][lane] = scl[0];
-          sring[wave][1][lane] = scl_ok ? scl[1] : 0.f;   // times a masked weight of 0
+          sring[wave][0][lane & (GK - 1)] = scl[0];
+          sring[wave][1][lane & (GK - 1)] = scl_ok ? scl[1] : 0.f;   // times a masked weight of 0
           __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
           __builtin_amdgcn_wave_barrier();
         }
