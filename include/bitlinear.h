@@ -635,9 +635,9 @@ int bitlinear_rope_append(const bl_rope_desc* qkv, int64_t T, int64_t R, int int
  * it finds on the device; runs of one sequence in several workgroups are joined in the same launch.
  * max_len only keeps the launch of short sequences small (longer ones are computed as well).  ws is the plan's ws_bytes of device scratch
  * (256-byte aligned), zeroed by the caller once before its first use; launches that share it must
- * be ordered on one stream.  Scores and sums are fp32; probabilities enter the product with the
- * values as two bf16 terms (three for fp32 queries, which enter theirs as three).  The result does not depend on the order in which
- * blocks run. */
+ * be ordered on one stream.  Scores and sums are fp32; probabilities, and fp32 queries, enter their
+ * products as three bf16 terms, which hold their 24 bits.  The result does not depend on the order in
+ * which blocks run. */
 typedef struct bl_attn_plan {
   int64_t B, max_len;
   int32_t q_heads, kv_heads, head_dim, window;

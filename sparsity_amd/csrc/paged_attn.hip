@@ -20,9 +20,11 @@
 //                 whole row), and one byte permute per two elements turns eight row pieces into
 //                 VE operands (operand j: element VE n + j of the eight keys).  No LDS, no shuffle.
 // A lane's accumulators all belong to query n, so a new maximum rescales them by one lane-local
-// factor.  Probabilities enter the product as bf16 terms (the value, and what the terms so far leave
-// of it): two where the output is bf16, good to 2^-17, three for fp32 queries and output; an fp32
-// query's three terms hold it exactly.  The matrix cores are idle enough that this costs nothing.
+// factor.  Probabilities enter the product as three bf16 terms (the value, and what the terms so far
+// leave of it), an fp32 query as three as well: both keep their 24 bits.  (Two terms of a probability,
+// good to 2^-17, would be 2 to 3e-6 off before a bf16 output's rounding, ten times the error of 32-bit
+// operations; the third costs nothing over a bf16 cache, 1 to 2% over an int8 one at D = 128 and up to
+// 5% at D = 64: 16 x 8000 tokens 39.7 -> 41.6 us.)
 //
 // The launch is one block per resident place of the chip (two per CU, one where registers ask for it: a wave then has 16 KB of keys and
 // values in flight while the matrix cores work on the last 16; three waves per SIMD spill, one leaves
@@ -166,7 +168,7 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT, QT)) void paged_attn_kern
   constexpr int KC = DT / 32;               // 32-element steps of the q . k contraction
   constexpr int KW = DT * EB / 16;          // key dwords per lane and key tile
   constexpr int QS = QF ? 3 : 1;            // bf16 terms of a query element
-  constexpr int PS = QF ? 3 : 2;            // and of a probability
+  constexpr int PS = 3;                     // and of a probability
   // runs of 32 keys a wave takes at a time: 16 KB at D = 128 (fp32 queries at D = 256 leave no registers
   // for two: 64 x 8000 tokens 589 us with spills, 424 with one)
   constexpr int KG = I8 && !(DT > 128 && QF) ? 2 : 1;

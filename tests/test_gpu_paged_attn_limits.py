@@ -1,0 +1,77 @@
+"""Decode attention at the limits of its arithmetic, its workspace and its launch, against the formula
+in 64 bits.  u = 2^-24 is half a unit in the last place of a 24-bit float at 1."""
+import numpy as np
+import pytest
+
+import oracle.block_ref as R
+from parity_util import bf16_dev, dev, host
+from synth import rng, to_bf16
+
+pytestmark = pytest.mark.gpu
+
+S = pytest.importorskip("sparsity_amd")
+U = 2.0 ** -24
+
+
+def _f32(t):
+    return host(t.float())
+
+
+def _bf16(x):
+    v, bits = to_bf16(np.asarray(x, np.float32))
+    return v, bf16_dev(bits)
+
+
+def _query(x, qd):
+    return _bf16(x) if qd == "bf16" else (np.asarray(x, np.float32), dev(np.asarray(x, np.float32)))
+
+
+def _terms(p):
+    """The leading two bf16 terms of fp32 values."""
+    hi = R.bf16_round(p)
+    return hi, R.bf16_round(p - hi)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "i8"])
+@pytest.mark.parametrize("qd", ["bf16", "f32"])
+def test_weights_enter_the_product_with_24_bits(kv, qd):
+    """Three keys with weights 1, 1 and p, values -hi, -mid and 1, where hi + mid are the two leading bf16
+    terms of p: what is left, under 64 u p, is lost if the weight enters the product as two terms.
+
+    With scores 0, 0, -x, 0 < x <= 1: x carries three roundings (u x each in p's exponent, p x <= 0.37),
+    the exponential 2 u, the sum of six products at most 6 u; divided by 2 + p >= 2.  The bf16 output rounds
+    a result below 32 u by 2^-9 of it.
+    """
+    B, Hq, D, ps = 64, 3, 16, 4
+    g = rng(41)
+    x = (g.integers(1, 128, B) / 128).astype(np.float32)          # bf16 holds it
+    kc, vc = np.zeros((B, 1, ps, D), np.float32), np.zeros((B, 1, ps, D), np.float32)
+    ks = vs = kst = vst = None
+    if kv == "bf16":
+        p = np.exp(-x.astype(np.float64)).astype(np.float32)
+        hi, mid = _terms(p)
+        kc[:, 0, 2, 0] = -x
+        for j, v in enumerate((-hi, -mid, np.ones(B))):
+            vc[:, 0, j] = np.asarray(v, np.float32)[:, None]
+        kt, vt = _bf16(kc)[1], _bf16(vc)[1]
+    else:                                     # the same keys and values as a whole number and a scale
+        ks, vs = np.ones((B, 1, ps), np.float32), np.ones((B, 1, ps), np.float32)
+        ks[:, 0, 2] = x / np.float32(100)
+        p = np.exp(-100 * ks[:, 0, 2].astype(np.float64)).astype(np.float32)
+        hi, mid = _terms(p)
+        kc[:, 0, 2, 0] = -100
+        vs[:, 0, 0], vs[:, 0, 1] = hi, np.abs(mid)
+        vc[:, 0, 0] = -1
+        vc[:, 0, 1] = -np.sign(mid)[:, None]
+        vc[:, 0, 2] = 1
+        kc, vc = kc.astype(np.int8), vc.astype(np.int8)
+        kt, vt, kst, vst = (dev(a) for a in (kc, vc, ks, vs))
+    q = np.zeros((B, Hq, D), np.float32)
+    q[..., 0] = 1
+    q, qt = _query(q, qd)
+    blocks, lens = np.arange(B, dtype=np.int32)[:, None], np.full(B, 3, np.int32)
+    want, _, _, _ = R.paged_attn(q, kc, vc, blocks, lens, 1.0, 0, ks, vs)
+    assert np.abs(want).max() > 10 * U        # a loss of the third term would be seen
+    out = S.PagedAttn(B, Hq, 1, D, ps, 3)(qt, kt, vt, dev(blocks), dev(lens), 1.0, kst, vst)
+    bound = (3 * 0.37 + 2 + 6) / 2 * U + 2.0 ** -9 * np.abs(want)
+    assert np.all(np.abs(_f32(out) - want) <= bound), np.max(np.abs(_f32(out) - want)) / U
