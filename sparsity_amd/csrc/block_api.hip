@@ -266,14 +266,16 @@ namespace {
 
 constexpr int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 
+// The arrival counts first, as many for every plan: no plan's partial sums lie where another one's counts
+// have to be zero, so plans can take turns on a workspace.
 struct AttnWs {
   int64_t ticket, ml, part, total;
 };
 AttnWs attn_ws(const bl_attn_plan& p) {
-  const int64_t G = p.q_heads / p.kv_heads, rows = p.q_rows, qt = (G + rows - 1) / rows;
+  const int64_t G = p.q_heads / p.kv_heads, rows = p.q_rows;
   AttnWs w;
   w.ticket = 0;
-  w.ml = up256(p.B * p.kv_heads * qt * 4);
+  w.ml = up256(bl::kAttnBlocks * 4);
   w.part = w.ml + up256((int64_t)p.blocks * 2 * 2 * rows * 4);
   w.total = w.part + up256((int64_t)p.blocks * 2 * std::min(G, rows) * p.head_dim * 4);
   return w;
@@ -293,7 +295,7 @@ int bitlinear_paged_attn_plan(int64_t B, int64_t q_heads, int64_t kv_heads, int6
   if (B * kv_heads * ((G + 15) / 16) > ((int64_t)1 << 22)) return BL_EINVAL;
   *plan = {B, max_len, (int32_t)q_heads, (int32_t)kv_heads, (int32_t)head_dim, (int32_t)window, 0, 0, 0};
   bl::paged_attn_split(*plan);
-  plan->ws_bytes = (size_t)std::max<int64_t>(256, attn_ws(*plan).total);
+  plan->ws_bytes = (size_t)attn_ws(*plan).total;
   return BL_OK;
 }
 

@@ -108,6 +108,8 @@ hipError_t launch_rope_table(const double* freq, int64_t half, int64_t positions
                              float* table, hipStream_t s);
 
 // ---- decode attention over the paged cache ----
+constexpr int kAttnBlocks = 512;       // blocks of a launch at most: two per CU
+
 struct AttnArgs {
   bl_kv_cache kv;
   const void* q;
@@ -120,7 +122,7 @@ struct AttnArgs {
   float* lse;            // [B][Hq] or nullptr
   float* part;           // [2 * nblocks][min(G, q_rows)][D] sums of runs of keys
   float* ml;             // [2 * nblocks][2][q_rows] their running maximum and sum
-  uint32_t* ticket;      // [B * key heads * qtiles] arrivals, zero between launches
+  uint32_t* ticket;      // [kAttnBlocks] arrivals, zero between launches
   int64_t B;
   int32_t Hq, G, q_rows, qtiles, nblocks, window;
 };

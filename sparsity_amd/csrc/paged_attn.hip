@@ -221,7 +221,7 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT, QT)) void paged_attn_kern
     const int in_seq = (int)((unit - seq0) / units);      // group of the sequence
     const int64_t next_group = seq0 + (in_seq + 1) * units, g0 = next_group - tiles;   // g0: its first tile
     const int64_t tile = max(unit, g0), end = min(u1, next_group);   // the segment is [tile, end)
-    const int64_t sq = b, grp = sq * per_seq + in_seq;
+    const int64_t sq = b;
     unit = end;
     if (unit == seq0 + units * per_seq) { seq0 = unit; ++b; }
     if (tile >= end) continue;                            // the start of a group that the next block takes
@@ -567,15 +567,16 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT, QT)) void paged_attn_kern
       // wave waits for its stores before the block counts as arrived; the block that arrives last
       // reads after that.  That is the order of a device-scope release and acquire, without their
       // write-back and invalidation of the XCD's L2 (10 us per block for the one, up to 8 us for the
-      // other while the rest of the chip streams).
+      // other while the rest of the chip streams).  Arrivals are counted at the block that begins the
+      // group: a block begins at most one group that goes on in the next, so no two share a count.
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
       __builtin_amdgcn_s_waitcnt(waitcnt_imm(0));
       __syncthreads();
       if (tid == 0) {
-        last_sh = __hip_atomic_fetch_add(a.ticket + grp, 1u, __ATOMIC_RELAXED,
+        last_sh = __hip_atomic_fetch_add(a.ticket + owner0, 1u, __ATOMIC_RELAXED,
                                          __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)active - 1;
         if (last_sh)                            // ready for the next launch
-          __hip_atomic_store(a.ticket + grp, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          __hip_atomic_store(a.ticket + owner0, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
       __syncthreads();
       if (last_sh) {
@@ -732,7 +733,7 @@ void paged_attn_split(bl_attn_plan& p) {
   // a block per resident place of the chip, fewer where there is less work: tiles of keys, and the
   // start of a group as so many more (at most six: start_units)
   const int64_t groups = pairs * ((G + p.q_rows - 1) / p.q_rows);
-  const int64_t places = 256 * resident(D <= 64 ? 64 : D <= 128 ? 128 : 256, two ? 2 : 1);
+  const int64_t places = kAttnBlocks / 2 * resident(D <= 64 ? 64 : D <= 128 ? 128 : 256, two ? 2 : 1);
   p.blocks = (int32_t)std::max<int64_t>(1, std::min(places, groups * (tiles + 6)));
 }
 

@@ -75,3 +75,27 @@ def test_weights_enter_the_product_with_24_bits(kv, qd):
     out = S.PagedAttn(B, Hq, 1, D, ps, 3)(qt, kt, vt, dev(blocks), dev(lens), 1.0, kst, vst)
     bound = (3 * 0.37 + 2 + 6) / 2 * U + 2.0 ** -9 * np.abs(want)
     assert np.all(np.abs(_f32(out) - want) <= bound), np.max(np.abs(_f32(out) - want)) / U
+
+
+def test_one_workspace_for_several_plans():
+    """Launches of different plans take turns on one workspace that was zeroed once."""
+    import torch
+    g = rng(43)
+    Hq, Hk, D, ps, per = 16, 8, 64, 16, 40
+    pages = 64 * per
+    kt, vt = (_bf16(g.standard_normal((pages, Hk, ps, D)))[1] for _ in range(2))
+    blocks = dev(g.permutation(pages).reshape(64, per).astype(np.int32))
+    lens = dev(g.integers(1, per * ps + 1, 64).astype(np.int32))
+    q = dev(g.standard_normal((64, Hq, D)).astype(np.float32))
+    sizes = [(64, 16), (1, 16), (64, 8), (7, 16), (3, 8)]
+    plans = [S.PagedAttn(B, hq, Hk, D, ps, per * ps) for B, hq in sizes]
+    call = lambda p, B, hq: p(q[:B, :hq], kt, vt, blocks[:B], lens[:B], want_lse=True)
+    alone = [[t.clone() for t in call(p, *s)] for p, s in zip(plans, sizes)]
+    shared = torch.zeros(max(p.plan.ws_bytes for p in plans), dtype=torch.uint8, device="cuda")
+    for p in plans:
+        p.ws = shared
+    for i in [0, 1, 0, 2, 3, 0, 4, 2, 1, 3, 0, 4]:
+        B, hq = sizes[i]
+        out, lse = torch.full((B, hq, D), 7.0, device="cuda"), torch.full((B, hq), 7.0, device="cuda")
+        plans[i](q[:B, :hq], kt, vt, blocks[:B], lens[:B], out=out, lse=lse)
+        assert torch.equal(out, alone[i][0]) and torch.equal(lse, alone[i][1]), i
