@@ -627,9 +627,11 @@ int bitlinear_rope_append(const bl_rope_desc* qkv, int64_t T, int64_t R, int int
  *   s_j = scale * (q . k_j),  out = sum_j softmax(s)_j v_j,  lse = log sum_j exp(s_j)
  * over the sequence's positions j < lens[b] (the last `window` of them if window > 0) whose page
  * blocks[b][j / page_size] lies in [0, pages): a page outside is a hole, and its keys are masked.
- * What masked slots hold (NaN included) never reaches a result; a live key or value that is not
- * finite makes its heads' results not finite, except that keys whose score is -inf weigh nothing.  A
- * sequence without live keys, or of such keys alone, gives out = 0 and lse = -inf.  lens is int32 [B]; lengths past blocks_per_seq * page_size are cut there.
+ * What masked slots hold (NaN included) never reaches a result.  A live key that is not finite makes its
+ * heads' results NaN, except that keys whose score is -inf weigh nothing; a live value that is not finite
+ * makes its element of the output infinite or NaN, as the formula does.  A sequence without live keys, or
+ * of keys of score -inf alone, gives out = 0 and lse = -inf.  lens is int32 [B]; lengths past
+ * blocks_per_seq * page_size are cut there.
  *
  * The launch shares the live keys of all sequences evenly among the plan's workgroups, by the lengths
  * it finds on the device; runs of one sequence in several workgroups are joined in the same launch.

@@ -337,13 +337,16 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT, QT)) void paged_attn_kern
 
     v4f o[QT][VE];
     float m[QT], l[QT];
+    auto clear_sums = [&]() {
 #pragma unroll
-    for (int f = 0; f < QT; ++f) {
-      m[f] = -INFINITY;
-      l[f] = 0.f;
+      for (int f = 0; f < QT; ++f) {
+        m[f] = -INFINITY;
+        l[f] = 0.f;
 #pragma unroll
-      for (int j = 0; j < VE; ++j) o[f][j] = v4f{0.f, 0.f, 0.f, 0.f};
-    }
+        for (int j = 0; j < VE; ++j) o[f][j] = v4f{0.f, 0.f, 0.f, 0.f};
+      }
+    };
+    clear_sums();
 
     if (groups > 0) {
       put_rows(0, page0);
@@ -377,7 +380,11 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT, QT)) void paged_attn_kern
           qf[f][0][c] = __builtin_bit_cast(bf16x8, qraw[f][c][0]);
         }
       }
-    if (groups > 0) {
+    // An infinite value times a term of its weight that is zero would be NaN.  A wave whose sums hold a NaN
+    // takes its keys again with the leading term in the place of all three: that is infinite, or NaN, where
+    // the formula is, and stands for the NaNs alone.  Looking for them costs 0 to 1 us of a launch.
+    uint32_t taken = 0xFFFF0000u;             // of a weight's bits, what a term takes from those after it
+    for (;;) {
       for (int i = 0; i < groups; ++i) {
         const bool more = i + 1 < groups;
         if constexpr (I8) {
@@ -479,10 +486,11 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT, QT)) void paged_attn_kern
                 p1 *= vs[1];
               }
 #pragma unroll
-              for (int e = 0; e < PS; ++e) {
-                pw[e][k] = pack_bf16(p0, p1);
-                p0 -= bf16_lo(pw[e][k]);
-                p1 -= bf16_hi(pw[e][k]);
+              for (int e = 0; e < PS; ++e) {    // by truncation: the terms have the weight's sign
+                const uint32_t b0 = __float_as_uint(p0), b1 = __float_as_uint(p1);
+                pw[e][k] = upper_halves(b0, b1);
+                p0 -= __uint_as_float(b0 & taken);
+                p1 -= __uint_as_float(b1 & taken);
               }
             }
 #pragma unroll
@@ -513,21 +521,47 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT, QT)) void paged_attn_kern
         }
         if (more) load_v(i + 1);
       }
+      // the wave's sums, to be joined.  Lane (g, n) holds elements VE (4g + r) + j of head 16 f + n.
+      const int wl = here(threadIdx.x) & 63, wn = wl & 15;
+      auto place = [&](int f, int r, int j) -> float& {
+        return sm_o[wave][kQ * f + wn][VE * (4 * (wl >> 4) + r) + j];
+      };
+      if (__builtin_expect(!taken, 0)) {      // only the NaNs of the first time give way
+#pragma unroll
+        for (int f = 0; f < QT; ++f)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int j = 0; j < VE; ++j) {
+              const float v = place(f, r, j);
+              o[f][j][r] = v == v ? v : o[f][j][r];
+            }
+      }
+      v4f all = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int f = 0; f < QT; ++f) {
+        l[f] += __shfl_xor(l[f], 16, 64);
+        l[f] += __shfl_xor(l[f], 32, 64);
+#pragma unroll
+        for (int j = 0; j < VE; ++j) all += o[f][j];
+        const int h = kQ * f + wn;
+        if (h >= rows) continue;
+        if (wl < kQ) { sm_m[wave][h] = m[f]; sm_l[wave][h] = l[f]; }
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int j = 0; j < VE; ++j) place(f, r, j) = o[f][j][r];
+      }
+      const float sum = (all[0] + all[1]) + (all[2] + all[3]);   // NaN if any of them is
+      if (__builtin_expect(!taken || !__any(sum != sum), 1)) break;
+      taken = 0u;
+      clear_sums();
+      put_rows(0, page_of(0));
+      load_k(0);
+      load_v(0);
+      next = page_of(1);
     }
     const int tid = here(threadIdx.x), tl = tid & 63, tw = tid >> 6;
-    // join the waves.  Lane (g, n) holds elements VE (4g + r) + j of head 16 f + n.
-#pragma unroll
-    for (int f = 0; f < QT; ++f) {
-      const int h = kQ * f + n;
-      l[f] += __shfl_xor(l[f], 16, 64);
-      l[f] += __shfl_xor(l[f], 32, 64);
-      if (h >= rows) continue;
-      if (g == 0) { sm_m[wave][h] = m[f]; sm_l[wave][h] = l[f]; }
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int j = 0; j < VE; ++j) sm_o[wave][h][VE * (4 * g + r) + j] = o[f][j][r];
-    }
     __syncthreads();
     const int64_t orow = (sq * a.Hq + hq0) * (int64_t)D;
     auto finish = [&](int h, int d, float num, float den, float top) {

@@ -99,3 +99,52 @@ def test_one_workspace_for_several_plans():
         out, lse = torch.full((B, hq, D), 7.0, device="cuda"), torch.full((B, hq), 7.0, device="cuda")
         plans[i](q[:B, :hq], kt, vt, blocks[:B], lens[:B], out=out, lse=lse)
         assert torch.equal(out, alone[i][0]) and torch.equal(lse, alone[i][1]), i
+
+
+@pytest.mark.parametrize("kv", ["bf16", "i8"])
+@pytest.mark.parametrize("qd", ["bf16", "f32"])
+@pytest.mark.parametrize("Hq,n,top", [(4, 1, 1), (4, 70, 70), (16, 700, 700), (40, 300, 1 << 20)])
+def test_infinite_values_reach_their_elements_as_in_the_formula(kv, qd, Hq, n, top):
+    """A live infinite value makes its element of the output infinite, infinities of both signs (int8: an
+    infinite scale of a zero) make it NaN, and every other element is what it is without them."""
+    g = rng(47 + n)
+    B, D, ps = 3, 32, 16
+    per = -(-n // ps)
+    pages = B * per
+    q, qt = _query(g.standard_normal((B, Hq, D)), qd)
+    k = g.standard_normal((pages, 1, ps, D))
+    ks = vs = kst = vst = None
+    blocks, lens = np.arange(pages, dtype=np.int32).reshape(B, per), np.full(B, n, np.int32)
+    at = [(t // ps, t % ps) for t in sorted({0, n // 2, n - 1})]      # of sequence 0
+    if kv == "bf16":
+        k, kt = _bf16(k)
+        v, vt = _bf16(g.standard_normal(k.shape))
+        clean, cleant = v, vt
+        v = v.copy()
+        for i, (p, o) in enumerate(at):
+            v[p, 0, o, 3 + i], v[p, 0, o, 9 + i] = np.inf, -np.inf
+        p, o = at[-1]
+        v[p, 0, o, 20], v[at[0][0], 0, at[0][1], 20] = -np.inf, np.inf
+        vt = _bf16(v)[1]
+        clean_vs = cleanst = None
+    else:
+        k, v = (g.integers(-127, 128, k.shape).astype(np.int8) for _ in range(2))
+        p, o = at[0]
+        v[p, 0, o, :4] = 0, 1, -1, 127
+        ks, vs = ((0.01 + 0.01 * g.random(k.shape[:3])).astype(np.float32) for _ in range(2))
+        clean, clean_vs = v, vs
+        vs = vs.copy()
+        vs[p, 0, o] = np.inf
+        kt, vt, kst, vst, cleanst = (dev(a) for a in (k, v, ks, vs, clean_vs))
+        cleant = vt
+    plan = S.PagedAttn(B, Hq, 1, D, ps, top)
+    with np.errstate(invalid="ignore"):
+        want, wl, _, _ = R.paged_attn(q, k, v, blocks, lens, D ** -0.5, 0, ks, vs)
+    call = lambda vt, vst: [host(t.float()) for t in plan(qt, kt, vt, dev(blocks), dev(lens), k_scale=kst,
+                                                           v_scale=vst, want_lse=True)]
+    got, lse = call(vt, vst)
+    base, base_lse = call(cleant, cleanst)
+    odd = ~np.isfinite(want)
+    assert odd[0].any() and not odd[1:].any()
+    assert np.array_equal(got[odd], want[odd], equal_nan=True)
+    assert np.array_equal(got[~odd], base[~odd]) and np.array_equal(lse, base_lse)
