@@ -365,12 +365,15 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT, QT)) void paged_attn_kern
           const uint32_t bits[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
           for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(bits[j]);
+          // cut off, not rounded: a rounding makes the largest infinite (a canonical NaN survives the cut)
 #pragma unroll
           for (int t = 0; t < QS; ++t) {
             uint32_t w[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+              const float x = t ? v[2 * j] : __builtin_canonicalizef(v[2 * j]);
+              const float y = t ? v[2 * j + 1] : __builtin_canonicalizef(v[2 * j + 1]);
+              w[j] = upper_halves(__float_as_uint(x), __float_as_uint(y));
               v[2 * j] -= bf16_lo(w[j]);
               v[2 * j + 1] -= bf16_hi(w[j]);
             }

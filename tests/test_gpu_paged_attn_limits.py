@@ -148,3 +148,85 @@ def test_infinite_values_reach_their_elements_as_in_the_formula(kv, qd, Hq, n, t
     assert odd[0].any() and not odd[1:].any()
     assert np.array_equal(got[odd], want[odd], equal_nan=True)
     assert np.array_equal(got[~odd], base[~odd]) and np.array_equal(lse, base_lse)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "i8"])
+def test_queries_enter_the_product_with_24_bits(kv):
+    """fp32 queries (a, hi, mid) against keys 2^14 (1, -1, -1), where hi + mid are the two leading bf16
+    terms of a: the score is 2^14 of what is left of a, exact in every step but the last roundings, and the
+    score of a query held as two terms would be 0.  One key, so lse is the score."""
+    B, Hq, D, ps = 8, 16, 16, 1
+    g = rng(53)
+    a = (1 + g.random((B, Hq))).astype(np.float32)
+    hi, mid = _terms(a)
+    q = np.zeros((B, Hq, D), np.float32)
+    q[..., 0], q[..., 1], q[..., 2] = a, hi, mid
+    c = 2.0 ** 14
+    kc = np.zeros((B, 1, ps, D), np.float32)
+    kc[..., 0], kc[..., 1:3] = 1, -1
+    ks = kst = vst = None
+    if kv == "bf16":
+        kt, vt = _bf16(kc * c)[1], _bf16(np.ones_like(kc))[1]
+    else:
+        kt, vt = dev(kc.astype(np.int8)), dev(np.ones(kc.shape, np.int8))
+        kst, vst = dev(np.full((B, 1, ps), c, np.float32)), dev(np.ones((B, 1, ps), np.float32))
+    blocks, lens = np.arange(B, dtype=np.int32)[:, None], np.ones(B, np.int32)
+    want = c * (a.astype(np.float64) - hi - mid)
+    assert np.abs(want).max() > 0.02
+    out, lse = S.PagedAttn(B, Hq, 1, D, ps, 1)(dev(q), kt, vt, dev(blocks), dev(lens), 1.0, kst, vst, want_lse=True)
+    # sums of mid and lo parts: three of at most 2^14 * 2^-8, rounded; then three roundings to and from log2
+    assert np.all(np.abs(host(lse) - want) <= 3 * U * 2.0 ** 6 + 6 * U * np.abs(want))
+    assert np.array_equal(_f32(out), np.ones_like(q))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "i8"])
+def test_queries_at_the_end_of_the_fp32_range(kv):
+    """Queries that a rounding to bf16 would carry to infinity, against keys that bring the score back:
+    one key of score q k and one of score 0."""
+    B, D, ps = 1, 16, 4
+    big = np.array([3.4028235e38, -3.4028235e38, 3.399e38, 3.39e38, -3.3962e38, 1.0], np.float32)
+    Hq = len(big)
+    q = np.zeros((B, Hq, D), np.float32)
+    q[0, :, 5] = big
+    tiny = 2.0 ** -125
+    kc, vc = np.zeros((1, 1, ps, D), np.float32), np.zeros((1, 1, ps, D), np.float32)
+    ks = vs = kst = vst = None
+    if kv == "bf16":
+        kc[0, 0, 1, 5] = tiny
+        vc[0, 0, 1] = 1
+        kt, vt = _bf16(kc)[1], _bf16(vc)[1]
+        scale = 0.5
+    else:
+        kc[0, 0, 1, 5] = vc[0, 0, 1, 0] = 1
+        ks, vs = (np.full((1, 1, ps), s, np.float32) for s in (tiny, 1.0))
+        kc, vc = kc.astype(np.int8), vc.astype(np.int8)
+        kt, vt, kst, vst = (dev(a) for a in (kc, vc, ks, vs))
+        scale = 0.5
+    blocks, lens = np.zeros((1, 1), np.int32), np.full(1, 2, np.int32)
+    want, wl, mag, smag = R.paged_attn(q, kc, vc, blocks, lens, scale, 0, ks, vs)
+    out, lse = S.PagedAttn(B, Hq, 1, D, ps, 2)(dev(q), kt, vt, dev(blocks), dev(lens), scale, kst, vst, want_lse=True)
+    e = (8 * U * smag + 8 * U)[..., None]     # a score's few roundings, the exponential's and the sums'
+    assert np.all(np.abs(_f32(out) - want) <= 2 * e * mag + 1e-30)
+    assert np.all(np.abs(host(lse) - wl) <= e[..., 0] + 4 * U * np.abs(wl))
+
+
+def test_values_at_the_end_of_the_fp32_range():
+    """An int8 value times a scale that a rounding to bf16 would carry to infinity."""
+    B, Hq, D, ps = 1, 2, 16, 4
+    vs = np.full((1, 1, ps), 3.4028235e38, np.float32)
+    kt, vt = dev(np.zeros((1, 1, ps, D), np.int8)), dev(np.ones((1, 1, ps, D), np.int8))
+    out = S.PagedAttn(B, Hq, 1, D, ps, 1)(dev(np.ones((B, Hq, D), np.float32)), kt, vt,
+                                          dev(np.zeros((1, 1), np.int32)), dev(np.ones(1, np.int32)),
+                                          k_scale=dev(np.ones((1, 1, ps), np.float32)), v_scale=dev(vs))
+    assert np.array_equal(_f32(out), np.full((B, Hq, D), vs[0, 0, 0]))
+
+
+def test_a_query_that_is_nan_in_its_last_bits():
+    B, Hq, D, ps = 1, 4, 16, 4
+    q = np.ones((B, Hq, D), np.float32)
+    q[0, 1:, 3].view(np.uint32)[:] = [0x7F800001, 0xFF800001, 0x7FC00000]
+    kt, vt = _bf16(np.full((1, 1, ps, D), -1.0))[1], _bf16(np.ones((1, 1, ps, D)))[1]
+    out, lse = S.PagedAttn(B, Hq, 1, D, ps, 3)(dev(q), kt, vt, dev(np.zeros((1, 1), np.int32)),
+                                               dev(np.full(1, 3, np.int32)), want_lse=True)
+    assert np.array_equal(_f32(out)[0, 0], np.ones(D)) and np.isfinite(host(lse)[0, 0])
+    assert np.all(np.isnan(_f32(out)[0, 1:])) and np.all(np.isnan(host(lse)[0, 1:]))
