@@ -208,6 +208,12 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
           v = v * ec[k] + load1<XBF>(x.x, r + other[k]) * es[k];
         }
     }
+    // In place, a lane's store overwrites what another lane reads of the same pair.  A head's lanes belong to
+    // one wave and come here together: every one of them has read before any writes.
+    if constexpr (!VEC) {
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    }
     if (!APPEND || m == 0) {
       if (!known || pad) {
         const float v = pad ? 0.f : __builtin_nanf("");
