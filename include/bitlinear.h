@@ -596,7 +596,8 @@ int bitlinear_rope(const bl_rope_desc* descs, int64_t count, int64_t T, int64_t 
  * rows must not overlap).  dtype BL_DTYPE_BF16, or BL_DTYPE_I8 with k_scale and v_scale fp32
  * [pages][heads][page_size] contiguous: an element stands for its int8 value times its row's scale.
  * head_dim: a multiple of 8 (BF16) or 16 (I8), at most 256; strides multiples of the same; k and v
- * 16-byte aligned. */
+ * 16-byte aligned.  The stride of an axis of one element (here, and of heads and tokens elsewhere) is
+ * never a step, and may be anything. */
 typedef struct bl_kv_cache {
   void* k;
   void* v;

@@ -408,7 +408,8 @@ def _cache_check(k, v, k_scale, v_scale, index: int):
     pointers."""
     import torch
     shape, s, dtype = k.shape, k.stride(), k.dtype
-    if len(shape) != 4 or shape != v.shape or s != v.stride() or dtype is not v.dtype:
+    if (len(shape) != 4 or shape != v.shape or dtype is not v.dtype or
+            s != v.stride() and any(n > 1 and i != j for n, i, j in zip(shape, s, v.stride()))):
         raise ValueError("k_cache, v_cache: must be [pages][heads][page_size][D] with the same "
                          "shape, strides and dtype")
     if k.get_device() != index or v.get_device() != index:

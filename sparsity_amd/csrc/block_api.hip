@@ -123,6 +123,9 @@ int bitlinear_rope_table(const double* freq, int64_t half, int64_t positions, do
 
 namespace {
 
+// The stride of an axis of one element is never a step and may be anything: it counts as 0.
+int64_t step(int64_t stride, int64_t count) { return count > 1 ? stride : 0; }
+
 // Whether a strided [T][heads][D] tensor can be read (strides, alignment to one element), and
 // whether its rows are aligned to four.
 bool strided_ok(const void* p, int64_t tok, int64_t head, int dtype) {
@@ -148,22 +151,20 @@ int rope_tensors(const bl_rope_desc* d, int64_t count, int64_t T, int64_t D, int
   int64_t heads = 0;
   *vec = D % 8 == 0 && R % 8 == 0;
   for (int64_t i = 0; i < count; ++i) {
-    if (d[i].heads < 1 || heads + d[i].heads > (1 << 20)) return BL_EINVAL;
-    if (T > 0) {
-      if (!strided_ok(d[i].x, d[i].x_tok, d[i].x_head, x_dtype)) return BL_EINVAL;
-      *vec = *vec && vec4(d[i].x, d[i].x_tok, d[i].x_head, x_dtype);
-      if (i < writes) {
-        if (!strided_ok(d[i].y, d[i].y_tok, d[i].y_head, y_dtype)) return BL_EINVAL;
-        if (!apart(T, d[i].heads, D, d[i].y_tok, d[i].y_head)) return BL_EINVAL;
-        if (d[i].x == d[i].y && (x_dtype != y_dtype || (T > 1 && d[i].x_tok != d[i].y_tok) ||
-                                 (d[i].heads > 1 && d[i].x_head != d[i].y_head)))
-          return BL_EINVAL;
-        *vec = *vec && vec4(d[i].y, d[i].y_tok, d[i].y_head, y_dtype);
-      }
-    }
-    a->t[i] = {d[i].x, i < writes ? d[i].y : nullptr, d[i].x_tok, d[i].x_head, d[i].y_tok, d[i].y_head,
-               (int32_t)heads, (int32_t)d[i].heads};
-    heads += d[i].heads;
+    const int64_t n = d[i].heads;
+    if (n < 1 || heads + n > (1 << 20)) return BL_EINVAL;
+    bl::RopeTensor& t = a->t[i];
+    t = {d[i].x, i < writes ? d[i].y : nullptr, step(d[i].x_tok, T), step(d[i].x_head, n),
+         step(d[i].y_tok, T), step(d[i].y_head, n), (int32_t)heads, (int32_t)n};
+    heads += n;
+    if (T == 0) continue;
+    if (!strided_ok(t.x, t.x_tok, t.x_head, x_dtype)) return BL_EINVAL;
+    *vec = *vec && vec4(t.x, t.x_tok, t.x_head, x_dtype);
+    if (i >= writes) continue;
+    if (!strided_ok(t.y, t.y_tok, t.y_head, y_dtype)) return BL_EINVAL;
+    if (!apart(T, n, D, t.y_tok, t.y_head)) return BL_EINVAL;
+    if (t.x == t.y && (x_dtype != y_dtype || t.x_tok != t.y_tok || t.x_head != t.y_head)) return BL_EINVAL;
+    *vec = *vec && vec4(t.y, t.y_tok, t.y_head, y_dtype);
   }
   if (T > 0 && (!aligned(pos, 4) || !aligned(table, 16))) return BL_EINVAL;
   a->pos = pos;
@@ -189,8 +190,10 @@ int check_cache(const bl_kv_cache* kv, int64_t* extent) {
   struct Axis { int64_t stride, count; } ax[3] = {{kv->page_stride, kv->pages},
                                                    {kv->head_stride, kv->heads},
                                                    {kv->tok_stride, kv->page_size}};
-  for (auto& x : ax)
+  for (auto& x : ax) {
+    x.stride = step(x.stride, x.count);
     if (x.stride < 0 || x.stride % q || x.stride > ((int64_t)1 << 46)) return BL_EINVAL;
+  }
   std::sort(ax, ax + 3, [](const Axis& p, const Axis& r) { return p.stride < r.stride; });
   int64_t span = kv->head_dim;   // elements one step of the axes so far covers
   for (auto& x : ax) {
@@ -319,6 +322,8 @@ int bitlinear_paged_attn(const bl_attn_plan* plan, const void* q, int q_dtype, i
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lens, 4) || (lse_opt && !aligned(lse_opt, 4)) ||
       (blocks_per_seq > 0 && !aligned(blocks, 4)))
     return BL_EINVAL;
+  q_tok = step(q_tok, p.B);
+  q_head = step(q_head, p.q_heads);
   if (!strided_ok(q, q_tok, q_head, q_dtype) || q_tok % 8 || q_head % 8) return BL_EINVAL;
   if (!aligned(ws, 256)) return BL_EINVAL;
   if (ws_bytes < p.ws_bytes) return BL_ENOSPC;

@@ -230,3 +230,58 @@ def test_a_query_that_is_nan_in_its_last_bits():
                                                dev(np.full(1, 3, np.int32)), want_lse=True)
     assert np.array_equal(_f32(out)[0, 0], np.ones(D)) and np.isfinite(host(lse)[0, 0])
     assert np.all(np.isnan(_f32(out)[0, 1:])) and np.all(np.isnan(host(lse)[0, 1:]))
+
+
+def _repeating(g, Hk, ps, D, kv, own):
+    """A cache of `own` pages of random rows, for block tables that name its pages again and again."""
+    shape = (own, Hk, ps, D)
+    if kv == "bf16":
+        (k, kt), (v, vt) = _bf16(g.standard_normal(shape)), _bf16(g.standard_normal(shape))
+        return k, v, None, None, kt, vt, None, None
+    k, v = (g.integers(-127, 128, shape).astype(np.int8) for _ in range(2))
+    ks, vs = ((0.005 + 0.02 * g.random(shape[:3])).astype(np.float32) for _ in range(2))
+    return (k, v, ks, vs) + tuple(dev(a) for a in (k, v, ks, vs))
+
+
+def _close(out, lse, q, c, blocks, lens, window=0):
+    """Within a bound counted from the arithmetic with fp32 queries: scores of D products ((D + 6) u of the
+    absolute ones), 4 u an exponential, n + 64 sums of weights; and near the plain form's error on the
+    whole (32-bit operations give 2 to 8e-7)."""
+    D = q.shape[2]
+    want, wl, mag, smag = R.paged_attn(q, c[0], c[1], blocks, lens, D ** -0.5, window, c[2], c[3])
+    e = ((D + 6) * U * smag + 4 * U + (np.max(lens) + 64) * U)[..., None]
+    got, gl = _f32(out), host(lse)
+    assert np.all(np.abs(got - want) <= 2 * e * mag + 4 * U * np.abs(want) + 1e-30)
+    assert np.linalg.norm(got - want) <= 1e-6 * np.linalg.norm(want)
+    dead = np.isneginf(wl)
+    assert np.array_equal(np.isneginf(gl), dead)
+    assert np.all(np.abs(gl[~dead] - wl[~dead]) <= e[..., 0][~dead] + 4 * U * np.abs(wl[~dead]))
+
+
+def test_strides_of_axes_of_one():
+    """The stride of an axis of one element is never a step, whatever it is: one sequence cut out of rows
+    of odd length, a cache of one page, one head, or one slot per page."""
+    g = rng(61)
+    D, ps = 32, 4
+    x = g.standard_normal((1, 4 * D)).astype(np.float32)
+    q, qt = x.reshape(1, 4, D), dev(x).as_strided((1, 4, D), (4 * D + 3, D, 1))
+    wide = dev(x).as_strided((1, 1, D), (1, 3, 1))
+    for shape, fake in (((1, 2, ps, D), 0), ((3, 1, ps, D), 1), ((6, 2, 1, D), 2), ((1, 1, 1, D), None)):
+        pages, Hk, slots, _ = shape
+        for kv in ("bf16", "i8"):
+            c = _repeating(g, Hk, slots, D, kv, pages)
+            strides = list(c[4].stride())
+            for a in range(3):
+                if a == fake or (fake is None and shape[a] == 1):
+                    strides[a] = 3 + 2 * a
+            kt, vt = c[4].as_strided(shape, strides), c[5]
+            if kv == "bf16":                  # both alike
+                vt = vt.as_strided(shape, strides)
+            blocks = np.arange(pages, dtype=np.int32)[None]
+            lens = np.full(1, pages * slots, np.int32)
+            for a, at in ((q, qt), (q[:, :1], wide)):
+                if a.shape[1] % Hk:
+                    continue
+                out, lse = S.PagedAttn(1, a.shape[1], Hk, D, slots, 8)(
+                    at, kt, vt, dev(blocks), dev(lens), k_scale=c[6], v_scale=c[7], want_lse=True)
+                _close(out, lse, a, c, blocks, lens)
