@@ -584,7 +584,8 @@ typedef struct bl_rope_desc {
  * with separate fp32 products and sums, rounded once to y_dtype; the other elements are copied.
  * pos is int32 [T].  A token at a position below 0 is padding: its rows become 0.  One at a
  * position of `positions` or more has no table entry: its rows become NaN.  y may be x itself with
- * the same type and strides; otherwise no row of a y may overlap a row of an x or y.  Any alignment
+ * the same type and strides; otherwise no row of a y may overlap a row of an x or y, pos or the table
+ * (BL_EINVAL; slices of one buffer beside each other do not overlap).  Any alignment
  * of the elements; rows of 8-multiples (D, R) aligned to four elements take the vector path.
  * 1 <= D <= 256. */
 int bitlinear_rope(const bl_rope_desc* descs, int64_t count, int64_t T, int64_t D, int64_t R,
@@ -616,7 +617,8 @@ typedef struct bl_kv_cache {
  * the value rounded once; I8 caches what act_quant_i8 writes for them per token and head.  Nothing
  * is written for a token whose position is below 0 or has no table entry, whose sequence or block
  * is out of range, or whose page is not in [0, pages); its query row is as bitlinear_rope's.  Two
- * tokens of one call must not name the same slot. */
+ * tokens of one call must not name the same slot.  The queries may be rotated in place; otherwise no row
+ * of the output, of either cache or of the scales may overlap another of them or an input (BL_EINVAL). */
 int bitlinear_rope_append(const bl_rope_desc* qkv, int64_t T, int64_t R, int interleaved,
                           int x_dtype, int q_dtype, const int32_t* pos, const int32_t* seq,
                           const int32_t* blocks, int64_t seqs, int64_t blocks_per_seq,

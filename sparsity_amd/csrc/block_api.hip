@@ -144,6 +144,68 @@ bool apart(int64_t T, int64_t heads, int64_t D, int64_t tok, int64_t head) {
   return true;
 }
 
+// Rows of a strided buffer, in bytes: `len` each, at p plus any multiple below `count` of each axis' stride.
+typedef __int128 wide;
+struct Axis {
+  int64_t stride, count;
+};
+struct Rows {
+  const void* p;
+  wide len, end;             // end: of the last row
+  Axis ax[3];
+  Rows(const void* ptr, wide n, Axis x = {0, 1}, Axis y = {0, 1}, Axis z = {0, 1}) : p(ptr), len(n), ax{x, y, z} {
+    end = (wide)(uintptr_t)p + len;
+    for (auto& a : ax) {
+      if (a.count <= 1) a.stride = 0;
+      end += (wide)a.stride * (a.count - 1);
+    }
+  }
+};
+
+struct Steps {
+  wide stride, lo, hi;       // multiples of the stride from lo to hi
+};
+wide floor_div(wide a, wide b) { return a / b - (a % b != 0 && (a < 0) != (b < 0)); }
+// Whether at + some multiple of each of n strides, in falling order, lies in [lo, hi].
+bool reaches(const Steps* s, int n, wide at, wide lo, wide hi, int* budget) {
+  if (n == 0) return lo <= at && at <= hi;
+  wide least = 0, most = 0;  // what the smaller strides can add
+  for (int i = 1; i < n; ++i) {
+    least += s[i].stride * s[i].lo;
+    most += s[i].stride * s[i].hi;
+  }
+  const wide first = std::max(s[0].lo, -floor_div(at + most - lo, s[0].stride));
+  const wide last = std::min(s[0].hi, floor_div(hi - least - at, s[0].stride));
+  for (wide k = first; k <= last; ++k) {
+    if (--*budget < 0) return false;
+    if (reaches(s + 1, n - 1, at + k * s[0].stride, lo, hi, budget)) return true;
+  }
+  return false;
+}
+// Whether a row of a meets a row of b.  Axes of one stride in both count by their difference, so slices of
+// one buffer beside each other take a few trials; buffers that interleave with unlike strides are looked
+// at for 2^16 of them, and then taken to be apart.
+bool rows_meet(const Rows& a, const Rows& b) {
+  const wide at = (wide)(uintptr_t)a.p - (wide)(uintptr_t)b.p;
+  if (!a.p || !b.p || a.len <= 0 || b.len <= 0) return false;
+  if (a.end <= (wide)(uintptr_t)b.p || b.end <= (wide)(uintptr_t)a.p) return false;
+  Steps s[6];
+  int n = 0;
+  for (const auto& x : a.ax)
+    if (x.stride) s[n++] = {x.stride, 0, x.count - 1};
+  const int na = n;
+  for (const auto& x : b.ax) {
+    if (!x.stride) continue;
+    int i = 0;
+    while (i < na && !(s[i].stride == x.stride && s[i].lo == 0)) ++i;
+    if (i < na) s[i].lo = 1 - x.count;
+    else s[n++] = {x.stride, 1 - x.count, 0};
+  }
+  std::sort(s, s + n, [](const Steps& x, const Steps& y) { return x.stride > y.stride; });
+  int budget = 1 << 16;
+  return reaches(s, n, at, 1 - a.len, b.len - 1, &budget);
+}
+
 // Checks common to both rope calls; fills the tensors.
 int rope_tensors(const bl_rope_desc* d, int64_t count, int64_t T, int64_t D, int64_t R, int x_dtype,
                  int y_dtype, const int32_t* pos, const float* table, int64_t positions, int writes,
@@ -187,9 +249,7 @@ int check_cache(const bl_kv_cache* kv, int64_t* extent) {
       kv->heads > (1 << 16) || kv->head_dim < 1 || kv->head_dim > 256 || kv->head_dim % q)
     return BL_EINVAL;
   // rows apart: in the order of their strides, each axis steps over all of the one before
-  struct Axis { int64_t stride, count; } ax[3] = {{kv->page_stride, kv->pages},
-                                                   {kv->head_stride, kv->heads},
-                                                   {kv->tok_stride, kv->page_size}};
+  Axis ax[3] = {{kv->page_stride, kv->pages}, {kv->head_stride, kv->heads}, {kv->tok_stride, kv->page_size}};
   for (auto& x : ax) {
     x.stride = step(x.stride, x.count);
     if (x.stride < 0 || x.stride % q || x.stride > ((int64_t)1 << 46)) return BL_EINVAL;
@@ -226,6 +286,21 @@ int bitlinear_rope(const bl_rope_desc* descs, int64_t count, int64_t T, int64_t 
                               (int)count, &a, &vec);
   if (st != BL_OK) return st;
   if (T == 0) return BL_OK;
+  auto rows = [&](int i, bool y) {
+    const bl::RopeTensor& t = a.t[i];
+    const int64_t e = esize(y ? y_dtype : x_dtype);
+    return y ? Rows(t.y, D * e, {t.y_tok * e, T}, {t.y_head * e, t.heads})
+             : Rows(t.x, D * e, {t.x_tok * e, T}, {t.x_head * e, t.heads});
+  };
+  const Rows p(pos, T * 4), tab(table, positions * R * 4);
+  for (int i = 0; i < count; ++i) {
+    const Rows y = rows(i, true);
+    if (rows_meet(y, p) || rows_meet(y, tab)) return BL_EINVAL;
+    for (int j = 0; j < count; ++j) {
+      if (!(i == j && a.t[i].x == a.t[i].y) && rows_meet(y, rows(j, false))) return BL_EINVAL;
+      if (j < i && rows_meet(y, rows(j, true))) return BL_EINVAL;
+    }
+  }
   a.interleaved = interleaved != 0;
   a.inverse = inverse != 0;
   return status_of(bl::launch_rope(a, x_dtype == BL_DTYPE_BF16, y_dtype == BL_DTYPE_BF16, vec,
@@ -253,6 +328,28 @@ int bitlinear_rope_append(const bl_rope_desc* qkv, int64_t T, int64_t R, int int
   if (st != BL_OK) return st;
   if (T == 0) return BL_OK;
   if (!aligned(blocks, 4) || (seq && !aligned(seq, 4))) return BL_EINVAL;
+  const bool i8 = kv->dtype == BL_DTYPE_I8;
+  const int64_t ce = esize(kv->dtype), xe = esize(x_dtype), qe = esize(q_dtype);
+  auto cache = [&](const void* p) {
+    return Rows(p, D * ce, {step(kv->page_stride, kv->pages) * ce, kv->pages},
+                {step(kv->head_stride, kv->heads) * ce, kv->heads},
+                {step(kv->tok_stride, kv->page_size) * ce, kv->page_size});
+  };
+  auto rows = [&](const bl::RopeTensor& t) {
+    return Rows(t.x, D * xe, {t.x_tok * xe, T}, {t.x_head * xe, t.heads});
+  };
+  const wide scales = i8 ? (wide)kv->pages * kv->heads * kv->page_size * 4 : 0;
+  const bl::RopeTensor& q = a.t[0];
+  const Rows out[5] = {Rows(q.y, D * qe, {q.y_tok * qe, T}, {q.y_head * qe, q.heads}), cache(kv->k),
+                       cache(kv->v), Rows(kv->k_scale, scales), Rows(kv->v_scale, scales)};
+  const Rows in[7] = {rows(q), rows(a.t[1]), rows(a.t[2]), Rows(pos, T * 4), Rows(seq, T * 4),
+                      Rows(blocks, (wide)seqs * blocks_per_seq * 4), Rows(table, positions * R * 4)};
+  for (int i = 0; i < 5; ++i) {
+    for (int j = 0; j < 7; ++j)
+      if (!(i == 0 && j == 0 && q.x == q.y) && rows_meet(out[i], in[j])) return BL_EINVAL;
+    for (int j = 0; j < i; ++j)
+      if (rows_meet(out[i], out[j])) return BL_EINVAL;
+  }
   a.interleaved = interleaved != 0;
   a.kv = *kv;
   a.blocks = blocks;

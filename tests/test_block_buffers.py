@@ -44,3 +44,48 @@ def test_cache_strides_of_axes_of_one(kw):
     assert st == 0
     assert K.bitlinear_paged_attn(ctypes.byref(plan), None, 0, 0, 0, 1.0, _kv(**kw), None, 1, None, None, None, None,
                                   0, None) == 0
+
+
+def _rope(*descs, **kw):
+    a = dict(T=4, D=128, R=128, inter=0, inv=0, xd=0, yd=0, pos=P + 20 * SLOT, table=P + 21 * SLOT, n=64)
+    a.update(kw)
+    return K.bitlinear_rope((K.BlRopeDesc * len(descs))(*descs), *a.values(), None)
+
+
+ROW = 128 * 4                              # bytes of a head
+
+
+@pytest.mark.parametrize("descs,kw", [
+    ([_desc(P, P + ROW)], {}),                                            # shifted over itself by a head
+    ([_desc(P, P + 4 * ROW - 4, x_tok=512, y_tok=512)], {}),              # by a token less an element
+    ([_desc(P, P + SLOT), _desc(P + SLOT, P + 3 * SLOT)], {}),            # one tensor's output is another's input
+    ([_desc(P, P + SLOT), _desc(P + 2 * SLOT, P)], {}),
+    ([_desc(P, P + SLOT), _desc(P + 2 * SLOT, P + SLOT)], {}),            # two outputs in one place
+    ([_desc(P, P), _desc(P, P)], {}),                                     # one tensor in place twice
+    ([_desc(P, P), _desc(P + 3 * ROW, P + SLOT)], {}),                    # slices of a fused row that share a head
+    ([_desc(P, P), _desc(P + 4 * ROW, P + 4 * ROW), _desc(P + 8 * ROW, P + 7 * ROW + 4)], {}),
+    ([_desc(P, P + SLOT, y_head=256), _desc(P + SLOT + 3 * ROW - 4, P + 3 * SLOT, x_head=256)], {}),   # every other head
+    ([_desc(P, P + SLOT, x_tok=512), _desc(P + SLOT + 3 * 8192 + 100, P + 3 * SLOT, x_tok=640)], {}),  # unlike strides
+    ([_desc(P, P + 20 * SLOT - 64)], {}),                                 # over the positions
+    ([_desc(P, P + 21 * SLOT + 64 * 512 - 16)], {}),                      # over the table's last entries
+    ([_desc(P, P + SLOT), _desc(P + SLOT + 4, P + 3 * SLOT)], dict(xd=1, yd=0))])
+def test_rope_refuses_overlaps(descs, kw):
+    assert _rope(*descs, **kw) == EINVAL
+
+
+KV = 100 * 16 * 4 * 128                    # bytes of an int8 cache, and four times those of its scales
+
+
+@pytest.mark.parametrize("kw", [
+    dict(q=_desc(P, P + SLOT)), dict(q=_desc(P, P + 2 * SLOT + ROW)), dict(q=_desc(P, P + ROW)),
+    dict(q=_desc(P, P + 20 * SLOT)), dict(q=_desc(P, P + 21 * SLOT)), dict(q=_desc(P, P + 22 * SLOT)),
+    dict(q=_desc(P, P + 30 * SLOT + KV - 64)), dict(q=_desc(P, P + 40 * SLOT)), dict(q=_desc(P, P + 51 * SLOT + 64)),
+    dict(seq=P + 10 * SLOT), dict(k=_desc(P + 30 * SLOT + 512)), dict(v=_desc(P + 40 * SLOT)),
+    dict(kv=_kv(v=P + 30 * SLOT)), dict(kv=_kv(v=P + 30 * SLOT + KV - 128)), dict(kv=_kv(vs=P + 50 * SLOT)),
+    dict(kv=_kv(vs=P + 50 * SLOT + 100 * 64 * 4 - 4)), dict(kv=_kv(ks=P + 40 * SLOT + 256)),
+    dict(kv=_kv(k=P + 20 * SLOT)), dict(kv=_kv(ks=P + 21 * SLOT)), dict(kv=_kv(v=P + 22 * SLOT + 64)),
+    # keys and values side by side in rows or pages that are too short for both
+    dict(kv=_kv(v=P + 30 * SLOT + 112, tok=256, head=4096, page=16384)),
+    dict(kv=_kv(v=P + 30 * SLOT + 3 * 2048, page=2 * 8192, heads=4))])
+def test_append_refuses_overlaps(kw):
+    assert _append(T=4, **kw) == EINVAL
