@@ -144,10 +144,16 @@ def bitlinear_paged_attn(plan, q, q_dtype, q_tok, q_head, scale, kv, blocks, blo
 # checks read each tensor property once and name a fault only after one was found.
 # ---------------------------------------------------------------------------------------------
 
-def _stream(index: int) -> int:
-    """torch's current stream of a device."""
+def _enqueue(index: int, name: str, fn, *args) -> None:
+    """fn(*args, stream) on torch's current stream of device `index`, which is made current for the call: the
+    handle of a default stream stands for that of whichever device is."""
     import torch
-    return torch._C._cuda_getCurrentRawStream(index)
+    if torch._C._cuda_getDevice() == index:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    _check(status, name)
 
 
 def _dt(dtype, name: str) -> int:
@@ -224,9 +230,9 @@ def norm_quant(x, weight=None, residual=None, eps: float = 1e-6, lift_M: int = 0
             _rows(h, shape, ix, "h", residual.dtype)
         if rstd is not None:
             _buf(rstd, torch.float32, T, ix, "rstd")
-    _check(_lib().bitlinear_norm_quant(x.data_ptr(), xd, _ptr(residual), rd, _ptr(weight), eps, T, K,
-                                       lift_M, _ptr(h), xq.data_ptr(), scale.data_ptr(), _ptr(rstd),
-                                       _stream(ix)), "bitlinear_norm_quant")
+    _enqueue(ix, "bitlinear_norm_quant", _lib().bitlinear_norm_quant, x.data_ptr(), xd,
+             _ptr(residual), rd, _ptr(weight), eps, T, K, lift_M, _ptr(h), xq.data_ptr(),
+             scale.data_ptr(), _ptr(rstd))
     return xq, scale, x if h is None else h, rstd
 
 
@@ -275,10 +281,9 @@ def norm_quant_bwd(dn, h, rstd, weight=None, dres=None, dtype=None, want_dw: boo
     else:
         _buf(ws, torch.uint8, wsb, ix, "ws")
         wsb = ws.numel()
-    _check(_lib().bitlinear_norm_quant_bwd(dn.data_ptr(), gd, h.data_ptr(), hd, rstd.data_ptr(),
-                                           _ptr(weight), _ptr(dres), dh.data_ptr(), od, _ptr(dw), T,
-                                           K, _ptr(ws), wsb, _stream(ix)),
-           "bitlinear_norm_quant_bwd")
+    _enqueue(ix, "bitlinear_norm_quant_bwd", _lib().bitlinear_norm_quant_bwd, dn.data_ptr(), gd,
+             h.data_ptr(), hd, rstd.data_ptr(), _ptr(weight), _ptr(dres), dh.data_ptr(), od, _ptr(dw),
+             T, K, _ptr(ws), wsb)
     return dh, dw
 
 
@@ -328,8 +333,8 @@ def rope_table(positions: int, freq, mscale: float = 1.0, device="cuda", out=Non
     if out is None:
         out = freq.new_empty((positions, half, 2), dtype=torch.float32)
     _buf(out, torch.float32, positions * half * 2, ix, "out")
-    _check(_lib().bitlinear_rope_table(freq.data_ptr(), half, positions, mscale, out.data_ptr(),
-                                       _stream(ix)), "bitlinear_rope_table")
+    _enqueue(ix, "bitlinear_rope_table", _lib().bitlinear_rope_table, freq.data_ptr(), half,
+             positions, mscale, out.data_ptr())
     return out
 
 
@@ -397,8 +402,8 @@ def rope(xs, pos, table, interleaved: bool = False, inverse: bool = False, dtype
         outs = [_like(x, dtype) for x in xs]
     arr = b"".join([_ROPE.pack(x.data_ptr(), y.data_ptr(), *s)
                     for x, y, s in zip(xs, outs, strides)])
-    _check(_lib().bitlinear_rope(arr, len(xs), T, D, R, interleaved, inverse, xd, yd, pos.data_ptr(),
-                                 table.data_ptr(), positions, _stream(ix)), "bitlinear_rope")
+    _enqueue(ix, "bitlinear_rope", _lib().bitlinear_rope, arr, len(xs), T, D, R, interleaved, inverse,
+             xd, yd, pos.data_ptr(), table.data_ptr(), positions)
     return outs
 
 
@@ -470,12 +475,10 @@ def rope_append(q, k, v, pos, table, k_cache, v_cache, blocks, seq=None, k_scale
         out = _like(q, dtype)
     arr = _ROPE3.pack(q.data_ptr(), out.data_ptr(), qt, qh, ot, oh, nq, k.data_ptr(), 0, kt, kh, 0, 0,
                       nk, v.data_ptr(), 0, vt, vh, 0, 0, nv)
-    _check(_lib().bitlinear_rope_append(
-        arr, T, R, interleaved, xd, qd, pos.data_ptr(), _ptr(seq), blocks.data_ptr(), seqs, per,
-        table.data_ptr(), positions,
-        _KV.pack(k_cache.data_ptr(), v_cache.data_ptr(), 0 if k_scale is None else k_scale.data_ptr(),
-                 0 if v_scale is None else v_scale.data_ptr(), *cache),
-        _stream(ix)), "bitlinear_rope_append")
+    _enqueue(ix, "bitlinear_rope_append", _lib().bitlinear_rope_append, arr, T, R, interleaved, xd,
+             qd, pos.data_ptr(), _ptr(seq), blocks.data_ptr(), seqs, per, table.data_ptr(), positions,
+             _KV.pack(k_cache.data_ptr(), v_cache.data_ptr(), 0 if k_scale is None else
+             k_scale.data_ptr(), 0 if v_scale is None else v_scale.data_ptr(), *cache))
     return out
 
 
@@ -531,11 +534,12 @@ class PagedAttn:
             lse = q.new_empty((B, heads), dtype=torch.float32)
         if out is None:
             out = _like(q, dtype)
-        _check(_lib().bitlinear_paged_attn(
+        _enqueue(
+            ix, "bitlinear_paged_attn", _lib().bitlinear_paged_attn,
             self.plan, q.data_ptr(), qd, qt, qh, self.scale if scale is None else scale,
             _KV.pack(k_cache.data_ptr(), v_cache.data_ptr(),
                      0 if k_scale is None else k_scale.data_ptr(),
                      0 if v_scale is None else v_scale.data_ptr(), *cache),
             blocks.data_ptr(), blocks.shape[1], lens.data_ptr(), out.data_ptr(), _ptr(lse),
-            ws.data_ptr(), ws.numel(), _stream(ix)), "bitlinear_paged_attn")
+            ws.data_ptr(), ws.numel())
         return out if lse is None else (out, lse)

@@ -1,11 +1,15 @@
-"""What the operators between the projections accept and refuse of strides and overlaps (CPU only): the C ABI
-answers before it touches the HIP runtime (fake, never dereferenced device addresses; calls of no tokens
-return before a launch)."""
+"""What the operators between the projections accept and refuse of strides and overlaps, and the device they
+are enqueued on (CPU only): the C ABI answers before it touches the HIP runtime (fake, never dereferenced
+device addresses; calls of no tokens return before a launch)."""
+import contextlib
 import ctypes
 
 import pytest
+import torch
 
+import sparsity_amd as S
 from sparsity_amd import block as K
+from test_block_abi import BF, F32, I8, I32, Strided
 
 P = 1 << 40                                # fake, 256-byte aligned; buffers 16 GiB apart
 SLOT = 16 << 30
@@ -89,3 +93,50 @@ KV = 100 * 16 * 4 * 128                    # bytes of an int8 cache, and four ti
     dict(kv=_kv(v=P + 30 * SLOT + 3 * 2048, page=2 * 8192, heads=4))])
 def test_append_refuses_overlaps(kw):
     assert _append(T=4, **kw) == EINVAL
+
+
+class Placed(Strided):
+    def data_ptr(self):
+        return P
+
+
+def test_calls_run_on_the_device_of_their_tensors(monkeypatch):
+    """With another device current, a call makes its tensors' device current, takes that device's stream, and
+    leaves the current device as it was."""
+    now = [0]
+
+    @contextlib.contextmanager
+    def device(index):
+        was, now[0] = now[0], index
+        yield
+        now[0] = was
+
+    class Lib:
+        def __getattr__(self, name):
+            def call(*args):
+                calls.append((name, now[0], args[-1]))
+                return 0
+            return call
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: now[0], raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 1000 + i if now[0] == i else None,
+                        raising=False)
+    plan = S.PagedAttn(4, 8, 2, 64, 16, 100, device="cpu")
+    monkeypatch.setattr(K, "_lib", lambda: Lib())
+    for index in (1, 0, 2):
+        calls = []
+        t = lambda shape, dtype: Placed(shape, dtype, device=torch.device("cuda", index))   # noqa: B023
+        plan.ws = t(plan.plan.ws_bytes, torch.uint8)
+        x, w, h, r = t((4, 256), F32), t(256, F32), t((4, 256), BF), t(4, F32)
+        S.norm_quant(x, w, h, out=(t((4, 256), I8), r, h, r))
+        S.norm_quant_bwd(x, h, r, w, h, out=(h, None))
+        table, pos, blocks = t((50, 32, 2), F32), t(4, I32), t((4, 2), I32)
+        S.rope_table(50, t(32, torch.float64), out=table)
+        q, k, c = t((4, 8, 64), BF), t((4, 2, 64), BF), t((9, 2, 16, 64), BF)
+        S.rope([q], pos, table, outs=[q])
+        S.rope_append(q, k, k, pos, table, c, c, blocks, out=q)
+        plan(q, c, c, blocks, pos, out=q)
+        assert [n for n, _, _ in calls] == ["bitlinear_norm_quant", "bitlinear_norm_quant_bwd", "bitlinear_rope_table",
+                                            "bitlinear_rope", "bitlinear_rope_append", "bitlinear_paged_attn"]
+        assert all(d == index and s == 1000 + index for _, d, s in calls) and now == [0]
