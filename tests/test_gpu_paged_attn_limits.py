@@ -285,3 +285,53 @@ def test_strides_of_axes_of_one():
                 out, lse = S.PagedAttn(1, a.shape[1], Hk, D, slots, 8)(
                     at, kt, vt, dev(blocks), dev(lens), k_scale=c[6], v_scale=c[7], want_lse=True)
                 _close(out, lse, a, c, blocks, lens)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "i8"])
+@pytest.mark.parametrize("Hq,Hk,D,n,runs,rows", [
+    (16, 1, 64, 131072, 145, 16),    # the runs' weights fill LDS several times over
+    (16, 1, 128, 131072, 401, 16),
+    (16, 1, 256, 60000, 65, 16),     # more runs than a thread holds the maxima of
+    (5, 1, 48, 50000, 65, 16),
+    (20, 1, 64, 131072, 333, 32),    # two query tiles
+    (24, 1, 128, 70000, 33, 32)])
+def test_joins_of_many_runs(kv, Hq, Hk, D, n, runs, rows):
+    g = rng(D + n)
+    ps, own, B = 64, 37, 1
+    if rows == 32:                            # a batch whose bound asks for two tiles, one sequence alone is long
+        B = 16
+    per = -(-n // ps)
+    c = _repeating(g, Hk, ps, D, kv, own)
+    blocks = g.integers(0, own, (B, per)).astype(np.int32)
+    lens = g.integers(0, 40, B).astype(np.int32)
+    lens[B // 2] = n
+    q = g.standard_normal((B, Hq, D)).astype(np.float32)
+    plan = S.PagedAttn(B, Hq, Hk, D, ps, n)
+    assert plan.plan.q_rows == rows and plan.plan.blocks > runs
+    print(kv, Hq, Hk, D, n, plan.plan.blocks, flush=True)
+    for _ in range(2):
+        out, lse = plan(dev(q), c[4], c[5], dev(blocks), dev(lens), k_scale=c[6], v_scale=c[7], want_lse=True)
+        _close(out, lse, q, c, blocks, lens)
+
+
+@pytest.mark.parametrize("B", [63, 64, 65, 128, 129, 200, 1000])
+@pytest.mark.parametrize("kv,Hq,Hk", [("bf16", 2, 1), ("i8", 6, 3)])
+def test_batches_past_64_sequences(B, kv, Hq, Hk):
+    """The search for a block's first sequence runs 64 sequences at a time: ragged batches with empty
+    sequences, and none but empty ones, at its edges."""
+    g = rng(B)
+    D, ps, top, own = 32, 8, 500, 11
+    per = -(-top // ps)
+    c = _repeating(g, Hk, ps, D, kv, own)
+    blocks = g.integers(0, own, (B, per)).astype(np.int32)
+    lens = g.integers(0, top + 1, B).astype(np.int32)
+    for i in (0, 62, 63, 64, 65, 127, 128, B - 1):
+        if i < B:
+            lens[i] = 0
+    q = g.standard_normal((B, Hq, D)).astype(np.float32)
+    plan = S.PagedAttn(B, Hq, Hk, D, ps, top)
+    one = np.where(np.arange(B) == B - 1, top, 0).astype(np.int32)
+    late = np.where(np.arange(B) >= 64, lens, 0).astype(np.int32)
+    for n in (lens, one, late, lens, np.zeros_like(lens)):
+        out, lse = plan(dev(q), c[4], c[5], dev(blocks), dev(n), k_scale=c[6], v_scale=c[7], want_lse=True)
+        _close(out, lse, q, c, blocks, n)
