@@ -335,3 +335,21 @@ def test_batches_past_64_sequences(B, kv, Hq, Hk):
     for n in (lens, one, late, lens, np.zeros_like(lens)):
         out, lse = plan(dev(q), c[4], c[5], dev(blocks), dev(n), k_scale=c[6], v_scale=c[7], want_lse=True)
         _close(out, lse, q, c, blocks, n)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "i8"])
+@pytest.mark.parametrize("B,Hq,Hk,D,ps,top", [(1, 20, 5, 128, 16, 700), (3, 8, 8, 64, 1, 130), (5, 4, 1, 80, 24, 300),
+                                              (2, 40, 2, 128, 8, 77), (7, 2, 1, 256, 64, 1500),
+                                              (2, 33, 1, 96, 16, 520), (1, 1, 1, 16, 3, 40),
+                                              (4, 16, 1, 48, 256, 5000), (2, 6, 2, 208, 5, 600)])
+def test_fp32_queries_are_as_good_as_32_bit_operations(kv, B, Hq, Hk, D, ps, top):
+    g = rng(B * 31 + D + top)
+    per = -(-top // ps) + 1
+    c = _repeating(g, Hk, ps, D, kv, B * per)
+    blocks = g.permutation(B * per).reshape(B, per).astype(np.int32)
+    lens = g.integers(1, top + 1, B).astype(np.int32)
+    lens[0] = top
+    q = g.standard_normal((B, Hq, D)).astype(np.float32)
+    out, lse = S.PagedAttn(B, Hq, Hk, D, ps, top)(dev(q), c[4], c[5], dev(blocks), dev(lens), k_scale=c[6],
+                                                  v_scale=c[7], want_lse=True)
+    _close(out, lse, q, c, blocks, lens)
