@@ -638,8 +638,10 @@ int bitlinear_rope_append(const bl_rope_desc* qkv, int64_t T, int64_t R, int int
  *
  * The launch shares the live keys of all sequences evenly among the plan's workgroups, by the lengths
  * it finds on the device; runs of one sequence in several workgroups are joined in the same launch.
- * max_len only keeps the launch of short sequences small (longer ones are computed as well).  ws is the
- * plan's ws_bytes of device scratch (256-byte aligned), zeroed by the caller once before its first use;
+ * max_len, the length to be expected, sizes the launch, and with more than 16 query heads per key head it
+ * picks whether a workgroup takes 16 or 32 of them.  Longer sequences are computed as well; a bound far too
+ * large can cost short ones a fifth, and plans of different bounds may differ in a result's last bits.  ws
+ * is the plan's ws_bytes of device scratch (256-byte aligned), zeroed by the caller once before its first use;
  * launches that share it, of one plan or of several, must be ordered on one stream.  Scores and sums are fp32; probabilities, and fp32 queries, enter their
  * products as three bf16 terms, which hold their 24 bits.  The result does not depend on the order in
  * which blocks run. */

@@ -486,8 +486,9 @@ class PagedAttn:
     """Decode attention over a paged cache: ``PagedAttn(B, q_heads, heads, D, page_size, max_len)``
     sizes the launch and holds its workspace; calling it attends one query token per sequence.
 
-    max_len bounds the sequences' lengths (longer ones only run on too few workgroups); window > 0
-    attends the last ``window`` positions only.  Calls of one object are ordered on one stream.  Build
+    max_len is the length to be expected of the sequences, by which the launch is sized (longer ones are
+    computed as well, on too few workgroups); window > 0 attends the last ``window`` positions only.
+    Calls of one object are ordered on one stream.  Build
     it outside any graph capture (it waits for its workspace).
     """
 

@@ -8,9 +8,9 @@
 //
 // BitNet b1.58 puts a norm in front of every quantized projection.  The sum is held in fp64 so that
 // its order cannot move rstd by an ulp and an int8 value across a rounding boundary: the int8 rows
-// are those of the definition whatever the split over lanes.  At 7 to 9 bytes per element the
-// kernel is bound by memory; the fp64 adds are one instruction per element, a few percent of the
-// rate it could issue.
+// are those of the definition whatever the split over lanes.  At 3 bytes per element (bf16,
+// no residual) to 13 (fp32 onto an fp32 stream) the kernel is bound by memory; the fp64 adds are one
+// instruction per element, a few percent of the rate it could issue.
 //
 // A row belongs to W waves; a lane holds pieces of eight elements, p = lane, lane + 64 W, ..., in
 // registers from the first load to the int8 store, so every input byte is read once.
@@ -191,7 +191,10 @@ hipError_t launch_norm_quant(const NormArgs& a, bool x_bf16, bool res_bf16, hipS
 // double the sums (6553 x 2560: 41.8 us against 39.8, 1638 x 2560: 17.7 against 14.4).  Two rows per team
 // at a time gain nothing (39.6), a row asked for ahead spills and more than doubles the time.
 //
-// Measured: 8192 x 3200, fp32 dn, bf16 h, dres and dh: 48 us for the rows, 5.5 TB/s, 4.8 us for dw.
+// Measured: 8192 x 3200, fp32 dn, bf16 h, dres and dh: 48 us for the rows, 5.5 TB/s, 4.7 us for dw.
+// More than 16384 columns: a lane's four pieces and their dw sums do not fit its 128 registers, and each
+// row spills, 184 to 476 bytes a lane: 1024 x 16384 40 us, x 20480 463, x 28672 629 (bf16 dn 157), x 32768
+// 717.
 // ---------------------------------------------------------------------------------------------
 namespace {
 
@@ -246,7 +249,7 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdArgs a) {
   const int K = a.K, pieces = K / 8;
   const int p0 = threadIdx.x - team * 64 * W;
   float dw[P][8] = {};
-  // weights in registers; with four pieces per lane they would not fit and are read again per row
+  // weights in registers; with four pieces per lane they are read again per row (and the rest still spills)
   constexpr bool KEEP = P <= 2;
   float w[P][8];
   auto weights = [&]() {

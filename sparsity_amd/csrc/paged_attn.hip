@@ -26,17 +26,17 @@
 // operations; the third costs nothing over a bf16 cache, 1 to 2% over an int8 one at D = 128 and up to
 // 5% at D = 64: 16 x 8000 tokens 39.7 -> 41.6 us.)
 //
-// The launch is one block per resident place of the chip (two per CU, one where registers ask for it: a wave then has 16 KB of keys and
-// values in flight while the matrix cores work on the last 16; three waves per SIMD spill, one leaves
-// int8 caches at half the rate).  The blocks share all keys of all sequences evenly (see Work), the
+// The launch is one block per resident place of the chip (two per CU, one where registers ask for it: a
+// wave then has 16 KB of keys and values in flight while the matrix cores work on the last 16; three waves
+// per SIMD spill, one leaves int8 caches at half the rate).  The blocks share all keys of all sequences evenly (see Work), the
 // four waves of a block take quarters of its run and join in LDS; a run that is not its group's whole
 // goes to the workspace as partial sums, and the last block of the group to finish joins the runs, in
 // their order, so the result does not depend on which block that is.
 //
-// Measured: 64 x 8192 tokens, 8 key heads, 32 query heads of 128, bf16: 363 us, 5.9 TB/s; the same in
-// int8 210 us, 5.3 TB/s; one sequence of 262144 tokens, 5 key heads: 132 us, 5.1 TB/s; 48 ragged
-// sequences up to 6001 tokens, int8: 70 us, 4.3 TB/s; 700 tokens: 12 us, ten dependent round trips to
-// memory.  What is lost: 7 us to the first keys (lengths, then pages, then rows), blocks that end up to
+// Measured: 64 x 8192 tokens, 8 key heads, 32 query heads of 128, bf16: 362 us, 5.9 TB/s; the same in
+// int8 210 us, 5.3 TB/s; one sequence of 262144 tokens, 5 key heads: 131 us, 5.1 TB/s; 48 ragged
+// sequences up to 6001 tokens, int8: 71 us, 4.2 TB/s; 700 tokens: 12 us, ten dependent round trips to
+// memory; 24 heads on one key head of 256, read twice, 64 x 8000 tokens: 175 us, 3.0 TB/s.  What is lost: 7 us to the first keys (lengths, then pages, then rows), blocks that end up to
 // 12% apart under equal shares (memory serves the CUs unevenly), about 3 us for a join.
 #include <algorithm>
 
@@ -108,7 +108,8 @@ __device__ __forceinline__ void load_dw(const void* p, uint32_t* r) {
   }
 }
 
-// Resident blocks per CU (one wave of each per SIMD) that the registers allow without spilling.
+// Resident blocks per CU (one wave of each per SIMD) that the registers allow without spilling (but for 20
+// bytes with two query tiles of fp32 queries over int8 keys of 64).
 constexpr int resident(int DT, int QT) { return DT * QT <= 128 ? 2 : 1; }
 
 // The work of a launch as one run of units: sequence after sequence, group (key head and query tile)
@@ -170,7 +171,7 @@ __global__ __launch_bounds__(64 * kWaves, resident(DT, QT)) void paged_attn_kern
   constexpr int QS = QF ? 3 : 1;            // bf16 terms of a query element
   constexpr int PS = 3;                     // and of a probability
   // runs of 32 keys a wave takes at a time: 16 KB at D = 128 (fp32 queries at D = 256 leave no registers
-  // for two: 64 x 8000 tokens 589 us with spills, 424 with one)
+  // for two: 64 x 8000 tokens 589 us with spills, 418 with one)
   constexpr int KG = I8 && !(DT > 128 && QF) ? 2 : 1;
   constexpr int GK = 32 * KG;
 

@@ -12,8 +12,9 @@
 // One pass over the data, bound by memory: a block takes a token, a group of lanes a head at a
 // time, and a lane the same pairs of every head it visits, so cos and sin are read once per lane.
 // Measured (kernel time): 8192 tokens of 50 heads of 128, fp32 to bf16: 60.5 us, 5.3 TB/s (a large
-// device copy: 5.2); asking for one head ahead is worth 9%, two or four heads at a time lose 2 to 8%.
-// 1021 tokens of 40 bf16 heads of 80: 7.0 us, of which 2.6 us would be the bytes.  Append of 4096
+// device copy: 5.2); asking for one head ahead is worth 3.4%, two or four heads at a time lose 1 to 5%.
+// 1021 tokens of 40 bf16 heads of 80: 7.0 us, of which 2.6 us would be the bytes (a token of more than 512
+// is one block, so its three rounds of heads follow one another).  Append of 4096
 // tokens (48 heads of 128) to an int8 cache: 27 us, 5.4 TB/s; of 16 tokens: 4.2 us of latency.
 //
 // The int8 cache holds act_quant_i8's expressions per token and head (absmax / 127, round half to
@@ -125,7 +126,8 @@ __device__ __forceinline__ int tensor_of(const RopeArgs& a, int head) {
 // LPH lanes per head (the power of two not below D / 8), 256 / LPH heads at a time, a lane eight
 // elements.  APPEND: tensors 1 and 2 go to the cache.  VEC: D and R multiples of 8, rows aligned to
 // four elements.  Otherwise (APPEND only, D a multiple of 8) a lane takes elements 8 i .. 8 i + 7 of
-// any alignment and reads the other half of each pair itself.
+// any alignment and reads the other half of each pair itself, an element per access: 8192 tokens of 40 + 5
+// + 5 heads of 80 take 125 us at R = 20, 50 at R = 80 by the vector form.
 template <bool XBF, bool YBF, bool APPEND, bool VEC, int LPH>
 __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
   constexpr int HPB = 256 / LPH;
@@ -265,7 +267,8 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
 }
 
 // Scalar form of rope (any even R, any D, any strides): a thread takes pairs, or single elements
-// that pass through.
+// that pass through.  8192 tokens of 50 heads of 80, fp32 to bf16: 165 us at R = 20, 1.2 TB/s, for an
+// element per access and a division per pair (47 us at R = 80 by the vector form).
 template <bool XBF, bool YBF>
 __global__ __launch_bounds__(256) void rope_scalar_kernel(RopeArgs a) {
   const int64_t t = blockIdx.x;
