@@ -665,6 +665,56 @@ int bitlinear_paged_attn(const bl_attn_plan* plan, const void* q, int q_dtype, i
                          int64_t blocks_per_seq, const int32_t* lens, void* out, float* lse_opt,
                          void* ws, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Around a model's blocks: pages and slots of a step's tokens, embedding rows and their gradient.
+ *
+ * bitlinear_kv_step: block tables and slot maps of a step, from request lengths on the device.
+ *
+ * Request b has cached[b] tokens in the cache, its pages the first ceil(cached / page_size) entries of
+ * blocks[b] (int32 [B][blocks_per_seq]), and adds fresh[b] tokens; fresh[b] < 0 says that it has ended.
+ * free_pages[0 .. *free_count) is a stack of pages that no request holds (int32, free_cap entries).
+ *   1. Ended requests push their pages, in the order of requests and of their tables (what does not fit
+ *      in free_cap entries is dropped); their lens become 0 and their tables stay as they are.
+ *   2. A request is served if its pages fit its table's row, if it wants no new page or the pages wanted
+ *      by all requests up to it (served or not) are there, and if the tokens wanted by all requests up
+ *      to it are at most T.  A request that is not served adds nothing: lens[b] = cached[b].
+ *   3. New pages come from the top of the stack, in the order of requests and of their tables, whose
+ *      entries from ceil(cached / page_size) on they become; other entries stay as they are.
+ *   4. Token rows, requests in order: seq[t] = b, pos[t] = the token's position, slot[t] = page *
+ *      page_size + pos % page_size (int64; NULL: not wanted).  Rows from starts[B] to T are padding:
+ *      seq, pos and slot -1 (bitlinear_rope_append writes nothing for them).
+ * lens[b] (int32 [B]) is the length with the new tokens, what bitlinear_paged_attn reads; starts (int32
+ * [B + 1]) the first row of each request, starts[b + 1] - starts[b] what was served; *free_count_out the
+ * pages left.  lens may be cached and free_count_out free_count (in place); otherwise no output may
+ * overlap another buffer (BL_EINVAL).  Lengths below 0 count as 0, a free_count outside [0, free_cap]
+ * as the nearest of them; tables and the stack must hold page numbers of the caller's cache, which are
+ * moved and multiplied, never dereferenced.  0 <= B <= 2^20, T < 2^22, page_size >= 1, B * blocks_per_seq
+ * < 2^40.  One launch, two above 4096 rows. */
+int bitlinear_kv_step(const int32_t* cached, const int32_t* fresh, int64_t B, int32_t* blocks,
+                      int64_t blocks_per_seq, int64_t page_size, int32_t* free_pages,
+                      int64_t free_cap, const int32_t* free_count, int32_t* free_count_out, int64_t T,
+                      int32_t* seq, int32_t* pos, int64_t* slot_opt, int32_t* lens, int32_t* starts,
+                      void* stream);
+
+/* Embedding: y[t] = scale * table[ids[t]] in fp32, rounded once to y_dtype.  table is table_dtype
+ * [V][K], ids int32 [T], y y_dtype [T][K].  An id below 0 is padding: its row becomes 0.  One of V or
+ * more has no row: its row becomes NaN.  T < 2^22, 1 <= V < 2^31, K % 8 == 0, K <= 32768 (BL_ENOTSUP
+ * beyond), scale finite.  y may overlap nothing.  One launch. */
+int bitlinear_embed(const void* table, int table_dtype, int64_t V, int64_t K, const int32_t* ids,
+                    int64_t T, float scale, void* y, int y_dtype, void* stream);
+
+/* Its gradient: dtable[v] = scale * sum over t with ids[t] == v of dy[t] (fp32 [V][K]; dy is dy_dtype
+ * [T][K]), added to what dtable holds with BL_EMBED_ACCUM (rows without a token are not touched then).
+ * Ids outside [0, V) have no row.  Sums are fp32 in a fixed order: results do not vary from run to run.
+ * ws: bitlinear_embed_bwd_workspace_bytes of device scratch (256-byte aligned; contents on entry
+ * irrelevant).  dtable and ws may overlap nothing.  T == 0 writes zeros (or, accumulating, nothing).
+ * Two to four launches. */
+#define BL_EMBED_ACCUM 1
+int bitlinear_embed_bwd_workspace_bytes(int64_t T, int64_t K, size_t* ws_bytes);
+int bitlinear_embed_bwd(const void* dy, int dy_dtype, const int32_t* ids, int64_t T, int64_t V,
+                        int64_t K, float scale, float* dtable, int flags, void* ws, size_t ws_bytes,
+                        void* stream);
+
 /* Static description of a status code. */
 const char* bitlinear_strerror(int status);
 

@@ -26,3 +26,7 @@ from .block import (  # noqa: F401
     bitlinear_paged_attn_plan, bitlinear_rope, bitlinear_rope_append, bitlinear_rope_table,
     norm_quant, norm_quant_bwd, rope, rope_append, rope_frequencies, rope_table,
 )
+from .step import (  # noqa: F401
+    BL_EMBED_ACCUM, KvStep, bitlinear_embed, bitlinear_embed_bwd, bitlinear_embed_bwd_workspace_bytes,
+    bitlinear_kv_step, embed, embed_bwd, kv_step,
+)

@@ -1,0 +1,89 @@
+// Launchers and argument records of the operators around a model's blocks: pages and slots of a step,
+// embedding rows and their gradient, products with 4-bit weights, sampling.  Arguments are validated
+// by step_api.hip.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "bitlinear.h"
+
+namespace bl {
+
+// ---- pages and slots of a step ----
+struct KvStepArgs {
+  const int32_t* cached;
+  const int32_t* fresh;
+  int32_t* blocks;
+  int32_t* free_pages;
+  const int32_t* count;
+  int32_t* count_out;
+  int32_t* seq;
+  int32_t* pos;
+  int64_t* slot;         // nullptr: not wanted
+  int32_t* lens;
+  int32_t* starts;
+  int64_t B, per, cap, T;
+  uint32_t page;
+};
+hipError_t launch_kv_step(const KvStepArgs& a, hipStream_t s);
+
+// ---- embedding ----
+constexpr int64_t kEmbedMaxK = 32768;
+
+struct EmbedArgs {
+  const void* table;
+  const int32_t* ids;
+  void* y;
+  float scale;
+  int64_t V;
+  int32_t T, K;
+};
+hipError_t launch_embed(const EmbedArgs& a, bool table_bf16, bool y_bf16, hipStream_t s);
+
+// Workspace of the gradient, segments 256-byte aligned:
+//   chunk_id, chunk_tok  [chunks * chunk] ids of a chunk of tokens in order, and their tokens
+//   id, tok              [T] the same of all tokens (one chunk: the two are one)
+//   runs                 [1 + 2 * (T / kEmbedLong + 1)] long runs: their number, then first position and id
+//   part                 [tiles][2][K] sums of the pieces of long runs
+constexpr int kEmbedTile = 16;      // sorted positions a wave takes
+constexpr int kEmbedLong = 32;      // a run of more positions is summed in pieces
+
+struct EmbedBwdWs {
+  int64_t chunk, chunks, tiles;
+  size_t chunk_id, chunk_tok, id, tok, runs, part, total;
+};
+inline EmbedBwdWs embed_bwd_ws(int64_t T, int64_t K) {
+  auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+  EmbedBwdWs w = {};
+  w.chunk = T <= 16384 ? 1024 : 4096;
+  w.chunks = (T + w.chunk - 1) / w.chunk;
+  w.tiles = (T + kEmbedTile - 1) / kEmbedTile;
+  const size_t all = up((size_t)(w.chunks * w.chunk) * 4);
+  size_t off = 0;
+  w.chunk_id = off; off += all;
+  w.chunk_tok = off; off += all;
+  w.id = w.chunk_id; w.tok = w.chunk_tok;
+  if (w.chunks > 1) {
+    w.id = off; off += up((size_t)T * 4);
+    w.tok = off; off += up((size_t)T * 4);
+  }
+  w.runs = off; off += up((size_t)(1 + 2 * (T / kEmbedLong + 1)) * 4);
+  w.part = off;
+  if (T > kEmbedLong) off += up((size_t)w.tiles * 2 * (size_t)K * 4);
+  w.total = off;
+  return w;
+}
+
+struct EmbedBwdArgs {
+  const void* dy;
+  const int32_t* ids;
+  float* dtable;
+  float scale;
+  int32_t accumulate;
+  int64_t V, T;
+  int32_t K;
+  char* ws;
+};
+hipError_t launch_embed_bwd(const EmbedBwdArgs& a, bool dy_bf16, hipStream_t s);
+
+}  // namespace bl

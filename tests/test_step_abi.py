@@ -1,0 +1,216 @@
+"""Refusals of the operators around a model's blocks (CPU only): the C ABI rejects bad arguments before it
+touches the HIP runtime (fake, never dereferenced device addresses are passed), and the torch wrappers
+reject wrong tensors before anything reaches the C ABI."""
+import contextlib
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle.step_ref as R
+import sparsity_amd as S
+from sparsity_amd import step as K
+from test_block_abi import BF, F32, I8, I32, Strided
+
+P = 1 << 40                                # fake, 256-byte aligned; buffers 16 GiB apart
+SLOT = 16 << 30
+EINVAL, ENOTSUP, ENOSPC = -22, -95, -28
+NAN, INF = math.nan, math.inf
+
+
+def _kv(**kw):
+    a = dict(cached=P, fresh=P + SLOT, B=4, blocks=P + 2 * SLOT, per=8, page=16, free=P + 3 * SLOT, cap=64,
+             count=P + 4 * SLOT, left=P + 5 * SLOT, T=100, seq=P + 6 * SLOT, pos=P + 7 * SLOT, slot=P + 8 * SLOT,
+             lens=P + 9 * SLOT, starts=P + 10 * SLOT)
+    a.update(kw)
+    return K.bitlinear_kv_step(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(B=-1), dict(B=(1 << 20) + 1), dict(T=-1), dict(T=1 << 22), dict(per=0), dict(per=1 << 31), dict(page=0),
+    dict(page=1 << 31), dict(cap=-1), dict(cap=1 << 31), dict(B=1 << 20, per=1 << 20), dict(cached=None),
+    dict(cached=P + 2), dict(fresh=None), dict(fresh=P + SLOT + 1), dict(blocks=None), dict(free=None),
+    dict(count=None), dict(count=P + 4 * SLOT + 2), dict(left=None), dict(seq=None), dict(pos=None),
+    dict(slot=P + 8 * SLOT + 4), dict(lens=None), dict(starts=None), dict(starts=P + 10 * SLOT + 2),
+    dict(lens=P + 4), dict(lens=P + SLOT), dict(left=P + 9 * SLOT + 12),
+    dict(left=P), dict(blocks=P + 12), dict(free=P + SLOT + 8), dict(free=P + 2 * SLOT + 4 * 8 * 4 - 4),
+    dict(seq=P + 6 * SLOT, pos=P + 6 * SLOT + 396), dict(slot=P + 7 * SLOT + 392), dict(starts=P + 9 * SLOT + 12),
+    dict(starts=P), dict(seq=P + 2 * SLOT), dict(pos=P + 3 * SLOT + 252), dict(slot=P + 4 * SLOT), dict(lens=P + 2 * SLOT)])
+def test_kv_step_rejects(kw):
+    assert _kv(**kw) == EINVAL
+
+
+def _embed(**kw):
+    a = dict(table=P, td=0, V=100, K=256, ids=P + SLOT, T=4, scale=1.0, y=P + 2 * SLOT, yd=1)
+    a.update(kw)
+    return K.bitlinear_embed(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(td=2), ENOTSUP), (dict(yd=-1), ENOTSUP), (dict(K=12), EINVAL), (dict(K=0), EINVAL), (dict(K=32776), ENOTSUP),
+    (dict(T=-1), EINVAL), (dict(T=1 << 22), EINVAL), (dict(V=0), EINVAL), (dict(V=1 << 31), EINVAL),
+    (dict(scale=NAN), EINVAL), (dict(scale=-INF), EINVAL), (dict(table=None), EINVAL), (dict(table=P + 8), EINVAL),
+    (dict(ids=None), EINVAL), (dict(ids=P + SLOT + 2), EINVAL), (dict(y=None), EINVAL), (dict(y=P + 2 * SLOT + 4), EINVAL),
+    (dict(y=P), EINVAL), (dict(y=P + 100 * 1024 - 16), EINVAL), (dict(y=P + SLOT), EINVAL),
+    (dict(T=0, table=None, ids=None, y=None), 0)])
+def test_embed_rejects(kw, want):
+    assert _embed(**kw) == want
+
+
+def _embed_bwd(**kw):
+    a = dict(dy=P, dd=0, ids=P + SLOT, T=100, V=50, K=256, scale=1.0, dtable=P + 2 * SLOT, flags=0, ws=P + 3 * SLOT,
+             wsb=1 << 24)
+    a.update(kw)
+    return K.bitlinear_embed_bwd(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(dd=2), ENOTSUP), (dict(K=100), EINVAL), (dict(K=1 << 16), ENOTSUP), (dict(T=-2), EINVAL),
+    (dict(T=1 << 22), EINVAL), (dict(V=0), EINVAL), (dict(V=1 << 31), EINVAL), (dict(scale=INF), EINVAL),
+    (dict(flags=2), EINVAL), (dict(dy=None), EINVAL), (dict(dy=P + 2), EINVAL), (dict(ids=None), EINVAL),
+    (dict(dtable=None), EINVAL), (dict(dtable=P + 2 * SLOT + 8), EINVAL), (dict(ws=None), EINVAL),
+    (dict(ws=P + 3 * SLOT + 128), EINVAL), (dict(wsb=K.bitlinear_embed_bwd_workspace_bytes(100, 256)[1] - 1), ENOSPC),
+    (dict(wsb=0), ENOSPC), (dict(dtable=P), EINVAL), (dict(dtable=P + SLOT), EINVAL), (dict(ws=P), EINVAL),
+    (dict(ws=P + 2 * SLOT + 256), EINVAL), (dict(ws=P + SLOT), EINVAL),
+    (dict(T=0, flags=1, dy=None, ids=None, dtable=None, ws=None, wsb=0), 0)])
+def test_embed_grad_rejects(kw, want):
+    assert _embed_bwd(**kw) == want
+
+
+def test_embed_grad_workspace():
+    assert K.bitlinear_embed_bwd_workspace_bytes(0, 64) == (0, 0)
+    for bad in ((-1, 64), (4, 12), (1 << 22, 64)):
+        assert K.bitlinear_embed_bwd_workspace_bytes(*bad)[0] == EINVAL
+    assert K.bitlinear_embed_bwd_workspace_bytes(4, 1 << 16)[0] == ENOTSUP
+    sizes = [K.bitlinear_embed_bwd_workspace_bytes(T, 64) for T in (1, 32, 33, 1024, 1025, 16384, 16385, (1 << 22) - 1)]
+    assert all(st == 0 and n % 256 == 0 for st, n in sizes) and [n for _, n in sizes] == sorted(n for _, n in sizes)
+
+
+# ---- the torch wrappers ----
+
+def _kv_args(**kw):
+    a = dict(cached=Strided(4, I32), fresh=Strided(4, I32), blocks=Strided((4, 8), I32), free=Strided(64, I32),
+             count=Strided(1, I32), page=16, T=100)
+    a.update(kw)
+    return a
+
+
+I64 = torch.int64
+OUT = S.KvStep(Strided(100, I32), Strided(100, I32), Strided(100, I64), Strided(4, I32), Strided(5, I32), Strided(1, I32))
+OTHER = torch.device("cuda:1")
+
+
+@pytest.mark.parametrize("kw", [
+    dict(blocks=Strided(32, I32)), dict(blocks=Strided((4, 8), I64)), dict(blocks=Strided((4, 8), I32, (16, 1))),
+    dict(blocks=Strided((4, 8), I32, device=torch.device("cpu"))), dict(cached=Strided(3, I32)),
+    dict(cached=Strided(4, I64)), dict(fresh=Strided(4, I32, device=OTHER)), dict(fresh=Strided(2, I32)),
+    dict(free=Strided(64, I64)), dict(count=Strided(0, I32)), dict(count=Strided(1, I64)), dict(T=-1),
+    dict(out=OUT._replace(seq=Strided(99, I32))), dict(out=OUT._replace(pos=Strided(100, I64))),
+    dict(out=OUT._replace(slot=Strided(100, I32))), dict(out=OUT._replace(lens=Strided(3, I32))),
+    dict(out=OUT._replace(starts=Strided(4, I32))), dict(out=OUT._replace(count=None))])
+def test_kv_step_wrapper_rejects(kw):
+    kw = dict(kw)
+    out = kw.pop("out", OUT)
+    with pytest.raises(ValueError):
+        S.kv_step(*_kv_args(**kw).values(), out=out)
+
+
+def test_embed_wrappers_reject():
+    ids, table, y = Strided(4, I32), Strided((50, 64), F32), Strided((4, 64), BF)
+    for i, t, kw in [(ids, Strided(50, F32), {}), (ids, Strided((50, 64), torch.float16), {}),
+                     (ids, Strided((50, 64), F32, (128, 1)), {}), (Strided(4, I64), table, {}),
+                     (Strided((4, 1), I32), table, {}), (Strided(4, I32, device=OTHER), table, {}),
+                     (ids, Strided((50, 64), F32, device=torch.device("cpu")), {}),
+                     (ids, table, dict(out=Strided((3, 64), BF))), (ids, table, dict(dtype=F32)),
+                     (ids, table, dict(out=Strided((4, 64), torch.float16)))]:
+        with pytest.raises(ValueError):
+            S.embed(i, t, **dict(dict(out=y), **kw))
+    dy, ws, out = Strided((4, 64), BF), Strided(1 << 20, torch.uint8), Strided((50, 64), F32)
+    for d, i, kw in [(Strided(4, BF), ids, {}), (Strided((4, 64), torch.float16), ids, {}), (dy, Strided(3, I32), {}),
+                     (dy, Strided(4, I64), {}), (dy, ids, dict(out=Strided((49, 64), F32))),
+                     (dy, ids, dict(out=Strided((50, 64), BF))), (dy, ids, dict(out=None, accumulate=True)),
+                     (dy, ids, dict(ws=Strided(64, torch.uint8))), (dy, ids, dict(ws=Strided(1 << 20, I8)))]:
+        with pytest.raises(ValueError):
+            S.embed_bwd(d, i, 50, **dict(dict(out=out, ws=ws), **kw))
+    for k in (60, 1 << 16):
+        with pytest.raises(S.BitLinearError):
+            S.embed_bwd(Strided((4, k), F32), ids, 50, out=Strided((50, k), F32), ws=ws)
+
+
+class Placed(Strided):
+    def data_ptr(self):
+        return P
+
+
+def _on_devices(monkeypatch, calls_of):
+    """Runs calls_of(t) with tensors of devices 1, 0 and 2 while device 0 is current: a call makes its tensors'
+    device current, takes that device's stream, and leaves the current device as it was."""
+    now = [0]
+
+    @contextlib.contextmanager
+    def device(index):
+        was, now[0] = now[0], index
+        yield
+        now[0] = was
+
+    class Lib:
+        def __getattr__(self, name):
+            if name.endswith("_bytes"):
+                return getattr(real, name)
+
+            def call(*args):
+                calls.append((name, now[0], args[-1]))
+                return 0
+            return call
+
+    real = K._lib()
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: now[0], raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 1000 + i if now[0] == i else None,
+                        raising=False)
+    monkeypatch.setattr(K, "_lib", lambda: Lib())
+    for index in (1, 0, 2):
+        calls = []
+        names = calls_of(lambda shape, dtype: Placed(shape, dtype, device=torch.device("cuda", index)))  # noqa: B023
+        assert [n for n, _, _ in calls] == names
+        assert all(d == index and s == 1000 + index for _, d, s in calls) and now == [0]
+
+
+def test_calls_run_on_the_device_of_their_tensors(monkeypatch):
+    def calls(t):
+        a = _kv_args(**{n: t(v.shape, v.dtype) for n, v in _kv_args().items() if isinstance(v, Strided)})
+        S.kv_step(*a.values(), out=S.KvStep(*(t(v.shape, v.dtype) for v in OUT)))
+        ids, table, ws = t(4, I32), t((50, 64), F32), t(1 << 20, torch.uint8)
+        S.embed(ids, table, out=t((4, 64), BF))
+        S.embed_bwd(t((4, 64), BF), ids, 50, out=table, ws=ws)
+        return ["bitlinear_kv_step", "bitlinear_embed", "bitlinear_embed_bwd"]
+    _on_devices(monkeypatch, calls)
+
+
+# ---- pins of the plain implementations ----
+
+def test_kv_reference_by_hand():
+    """Two pages of three tokens a request: one ends, one grows into a new page, one begins, one waits."""
+    blocks = np.array([[4, 5], [1, -1], [-1, -1], [-1, -1]], np.int32)
+    free = np.array([7, 0, 0, 0], np.int32)
+    seq, pos, slot, lens, starts, count = R.kv_step([5, 3, 0, 0], [-1, 1, 4, 1], blocks, free, 1, 3, 8)
+    # pages 4 and 5 come back on top of 7: request 1 takes 5, request 2 takes 4 and 7, request 3 finds none
+    assert free[:3].tolist() == [7, 4, 5] and count == 0
+    assert blocks.tolist() == [[4, 5], [1, 5], [4, 7], [-1, -1]]
+    assert lens.tolist() == [0, 4, 4, 0] and starts.tolist() == [0, 0, 1, 5, 5]
+    assert seq.tolist() == [1, 2, 2, 2, 2, -1, -1, -1] and pos.tolist() == [3, 0, 1, 2, 3, -1, -1, -1]
+    assert slot.tolist() == [15, 12, 13, 14, 21, -1, -1, -1]
+
+
+def test_embed_reference_by_differences():
+    g = np.random.default_rng(2)
+    table, c = g.standard_normal((5, 8)), g.standard_normal((7, 8))
+    ids = np.array([0, 3, 3, -1, 4, 3, 9])
+    d, _, n = R.embed_grad(c, ids, 5, 2.0)
+    assert n.tolist() == [1, 0, 0, 3, 1]
+    f = lambda t: (np.nan_to_num(R.embed(ids, t, 2.0).astype(np.float64)) * c).sum()  # noqa: E731
+    for v in range(5):
+        e = np.zeros((5, 8))
+        e[v, 2] = 0.5
+        assert abs((f(table + e) - f(table - e)) - d[v, 2]) < 1e-5
