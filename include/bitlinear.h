@@ -715,6 +715,38 @@ int bitlinear_embed_bwd(const void* dy, int dy_dtype, const int32_t* ids, int64_
                         int64_t K, float scale, float* dtable, int flags, void* ws, size_t ws_bytes,
                         void* stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Weights in 4 bits with a scale per group of columns, times int8 rows: for layers that are kept out of
+ * the ternary body, an output head above all.
+ *
+ * A row's K columns are groups of 32, 64 or 128 (K % group == 0).  For each group of a row
+ *   s = bf16(fl32(max|w| / 7)), rounded to nearest even
+ *   q = clamp(rint(fl32(w / s)), -7, 7), rint = round half to even; 0 where s is 0
+ * A group that holds an infinity or a NaN gets s = NaN (and so do its products).
+ *   y[t][o] = x_scale[t] * sum_g s[o][g] * (sum_{k in g} q[o][k] * xq[t][k])
+ * with (xq, x_scale) the int8 rows of act_quant_i8 or bitlinear_norm_quant (lift_M = 0).  A group's inner sum
+ * is exact (int32); groups are joined in fp32 in a fixed order, which may differ with T.
+ *
+ * Layout: rows are padded to tiles of 16, columns to blocks of 128 (padding: q = 0, s = 0).  Tile i, block j
+ * of NB = ceil(K / 128):
+ *   codes   64 lanes x four little-endian dwords at byte ((i * NB + j) * 64 + l) * 16: lane l is row
+ *           16 i + l % 16; with h = l / 16, dword w holds the eight columns from 128 j + c on,
+ *           c = 64 (w / 2) + 16 h + 8 (w % 2) for groups of 64 and 128, 32 w + 8 h for groups of 32: the first
+ *           four in the low nibbles of its bytes, the others in the high ones, two's complement
+ *   scales  bf16 at ((i * NB + j) * 4 + h) * (512 / group) + 4 g + r: row 16 i + 4 h + r, columns from
+ *           128 j + group * g on
+ * codes and scales are 16-byte aligned, of the sizes that bitlinear_q4_bytes gives.  1 <= n <= 2^27, K <= 2^16,
+ * T < 2^22, ceil(n / 128) * ceil(T / 64) < 2^22. */
+int bitlinear_q4_bytes(int64_t n, int64_t K, int group, size_t* code_bytes, size_t* scale_bytes);
+
+/* Packs W (w_dtype [n][K]).  One launch. */
+int bitlinear_q4_pack(const void* W, int w_dtype, int64_t n, int64_t K, int group, uint8_t* codes,
+                      uint16_t* scales, void* stream);
+
+/* y (fp32 [T][n]) of T int8 rows.  y may overlap nothing.  One launch; up to 64 tokens read the weights once. */
+int bitlinear_q4_fwd(const int8_t* xq, const float* x_scale, int64_t T, int64_t K, const uint8_t* codes,
+                     const uint16_t* scales, int group, int64_t n, float* y, void* stream);
+
 /* Static description of a status code. */
 const char* bitlinear_strerror(int status);
 

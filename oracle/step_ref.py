@@ -64,3 +64,62 @@ def embed_grad(dy, ids, V, scale, into=None):
     if into is not None:
         out, mag = out + into, mag + np.abs(into)
     return out, mag, np.bincount(ids[ok], minlength=V)
+
+
+def bf16_bits(x):
+    """Bit patterns of fp32 values that bfloat16 holds."""
+    return (np.ascontiguousarray(x, F).view(np.uint32) >> 16).astype(np.uint16)
+
+
+def q4_quantize(W, group):
+    """(q int8 [n][K], s fp32 [n][K / group]) of fp32 weights; groups with an infinity or a NaN: 0, NaN."""
+    from .block_ref import bf16_round
+    n, K = W.shape
+    w = np.asarray(W, F).reshape(n, K // group, group)
+    amax = np.abs(w).max(-1)                 # NaN if there is one
+    ok = np.isfinite(amax)
+    s = np.where(ok, bf16_round(np.where(ok, amax, F(0)) / F(7)), F(np.nan)).astype(F)
+    live = ok & (s > 0)
+    with np.errstate(all="ignore"):
+        r = np.rint(w / np.where(live, s, F(1))[..., None])
+    q = np.where(live[..., None], np.clip(r, -7, 7), 0)
+    return q.astype(np.int8).reshape(n, K), s
+
+
+def q4_pack(q, s, group):
+    """The documented layout, element by element: (codes uint8, scales uint16)."""
+    n, K = q.shape
+    NB, nt = -(-K // 128), -(-n // 16)
+    qp = np.zeros((nt * 16, NB * 128), np.uint8)
+    qp[:n, :K] = q.astype(np.uint8) & 15
+    sp = np.zeros((nt * 16, NB * 128 // group), np.uint16)
+    sp[:n, :K // group] = bf16_bits(s)
+    sp[:n, :K // group][np.isnan(s)] = 0x7FC0
+    codes = np.zeros((nt, NB, 64, 4, 4), np.uint8)
+    scales = np.zeros((nt, NB, 4, 128 // group, 4), np.uint16)
+    for l in range(64):
+        h = l // 16
+        for w in range(4):
+            c = 32 * w + 8 * h if group == 32 else 64 * (w // 2) + 16 * h + 8 * (w % 2)
+            for j in range(4):
+                lo, hi = qp[l % 16::16, c + j::128], qp[l % 16::16, c + 4 + j::128]
+                codes[:, :, l, w, j] = lo | hi << 4
+    for h in range(4):
+        for g in range(128 // group):
+            for r in range(4):
+                scales[:, :, h, g, r] = sp[4 * h + r::16, g::128 // group]
+    return codes.reshape(-1), scales.reshape(-1)
+
+
+def q4_forward(xq, x_scale, q, s, group):
+    """(y, sum over groups of magnitudes) in fp64."""
+    n, K = q.shape
+    x = np.asarray(xq, np.float64).reshape(len(xq), K // group, group)
+    w = np.asarray(q, np.float64).reshape(n, K // group, group)
+    y, mag = (np.zeros((len(xq), n)) for _ in range(2))
+    for g in range(K // group):
+        part = (x[:, g] @ w[:, g].T) * np.asarray(s[:, g], np.float64)
+        y += part
+        mag += np.abs(part)
+    xs = np.asarray(x_scale, np.float64)[:, None]
+    return y * xs, mag * xs

@@ -23,6 +23,8 @@ bool clash(const Span (&in)[NI], const Span (&out)[NO], const int (&same)[NO]) {
   return false;
 }
 
+constexpr int64_t kQ4MaxN = (int64_t)1 << 27, kQ4MaxK = (int64_t)1 << 16;
+
 }  // namespace
 
 extern "C" {
@@ -95,6 +97,46 @@ int bitlinear_embed_bwd(const void* dy, int dy_dtype, const int32_t* ids, int64_
   if (clash(in, out, {-1, -1})) return BL_EINVAL;
   const bl::EmbedBwdArgs a = {dy, ids, dtable, scale, flags & BL_EMBED_ACCUM, V, T, (int32_t)K, (char*)ws};
   return status_of(bl::launch_embed_bwd(a, dy_dtype == BL_DTYPE_BF16, (hipStream_t)stream));
+}
+
+int bitlinear_q4_bytes(int64_t n, int64_t K, int group, size_t* code_bytes, size_t* scale_bytes) {
+  if (group != 32 && group != 64 && group != 128) return BL_ENOTSUP;
+  if (n < 1 || n > kQ4MaxN || K < group || K > kQ4MaxK || K % group || !code_bytes || !scale_bytes) return BL_EINVAL;
+  const size_t blocks = (size_t)((n + 15) / 16) * (size_t)((K + 127) / 128);
+  *code_bytes = blocks * 1024;
+  *scale_bytes = blocks * (size_t)(2048 / group) * 2;
+  return BL_OK;
+}
+
+int bitlinear_q4_pack(const void* W, int w_dtype, int64_t n, int64_t K, int group, uint8_t* codes,
+                      uint16_t* scales, void* stream) {
+  if (!float_dtype(w_dtype)) return BL_ENOTSUP;
+  size_t cb = 0, sb = 0;
+  const int st = bitlinear_q4_bytes(n, K, group, &cb, &sb);
+  if (st != BL_OK) return st;
+  if (!aligned(W, 16) || !aligned(codes, 16) || !aligned(scales, 16)) return BL_EINVAL;
+  const Span in[1] = {{W, (uint64_t)(n * K * esize(w_dtype))}};
+  const Span out[2] = {{codes, cb}, {scales, sb}};
+  if (clash(in, out, {-1, -1})) return BL_EINVAL;
+  const bl::Q4PackArgs a = {W, (uint32_t*)codes, scales, n, K, (n + 15) / 16, (K + 127) / 128, group};
+  return status_of(bl::launch_q4_pack(a, w_dtype == BL_DTYPE_BF16, (hipStream_t)stream));
+}
+
+int bitlinear_q4_fwd(const int8_t* xq, const float* x_scale, int64_t T, int64_t K, const uint8_t* codes,
+                     const uint16_t* scales, int group, int64_t n, float* y, void* stream) {
+  size_t cb = 0, sb = 0;
+  const int st = bitlinear_q4_bytes(n, K, group, &cb, &sb);
+  if (st != BL_OK) return st;
+  if (T < 0 || T > kMaxTokens || (n + 127) / 128 * ((T + 63) / 64) >= ((int64_t)1 << 22)) return BL_EINVAL;
+  if (T == 0) return BL_OK;
+  if (!aligned(xq, 16) || !aligned(x_scale, 4) || !aligned(codes, 16) || !aligned(scales, 16) || !aligned(y, 16))
+    return BL_EINVAL;
+  const Span in[4] = {{xq, (uint64_t)(T * K)}, {x_scale, (uint64_t)T * 4}, {codes, cb}, {scales, sb}};
+  const Span out[1] = {{y, (uint64_t)(T * n) * 4}};
+  if (clash(in, out, {-1})) return BL_EINVAL;
+  const bl::Q4Args a = {xq, x_scale, codes, scales, y, n, (n + 15) / 16, (int32_t)T, (int32_t)K,
+                        (int32_t)((K + 127) / 128), 0, 0, 0};
+  return status_of(bl::launch_q4_fwd(a, group, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -86,4 +86,27 @@ struct EmbedBwdArgs {
 };
 hipError_t launch_embed_bwd(const EmbedBwdArgs& a, bool dy_bf16, hipStream_t s);
 
+// ---- weights in 4 bits ----
+struct Q4PackArgs {
+  const void* W;
+  uint32_t* codes;
+  uint16_t* scales;
+  int64_t n, K;
+  int64_t tiles, blocks;   // of 16 rows, of 128 columns
+  int32_t group;
+};
+hipError_t launch_q4_pack(const Q4PackArgs& a, bool bf16, hipStream_t s);
+
+struct Q4Args {
+  const int8_t* xq;
+  const float* x_scale;
+  const uint8_t* codes;
+  const uint16_t* scales;
+  float* y;
+  int64_t n, tiles;
+  int32_t T, K, blocks;
+  int32_t chunk, ksplit, token_tiles;   // set by the launcher
+};
+hipError_t launch_q4_fwd(const Q4Args& a, int group, hipStream_t s);
+
 }  // namespace bl

@@ -2,13 +2,15 @@
 first block's input.
 
 Raw calls mirror the C ABI (``include/bitlinear.h``): ``bitlinear_kv_step``, ``bitlinear_embed``,
-``bitlinear_embed_bwd_workspace_bytes``, ``bitlinear_embed_bwd``.  ``kv_step`` / ``embed`` /
-``embed_bwd`` take torch tensors, check them (the C ABI receives bare pointers), allocate outputs that
+``bitlinear_embed_bwd_workspace_bytes``, ``bitlinear_embed_bwd``, ``bitlinear_q4_bytes``,
+``bitlinear_q4_pack``, ``bitlinear_q4_fwd``.  ``kv_step`` / ``embed`` / ``embed_bwd`` / ``q4_pack`` /
+``q4_fwd`` take torch tensors, check them (the C ABI receives bare pointers), allocate outputs that
 are not given and enqueue on torch's current stream.  Every step runs in HIP kernels.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple
 
 from . import bitlinear as _B
@@ -30,7 +32,11 @@ def _lib():
         L.bitlinear_embed.argtypes = [_VP, _I32, _I64, _I64, _VP, _I64, _F32, _VP, _I32, _VP]
         L.bitlinear_embed_bwd_workspace_bytes.argtypes = [_I64, _I64, ctypes.POINTER(_SZ)]
         L.bitlinear_embed_bwd.argtypes = [_VP, _I32, _VP, _I64, _I64, _I64, _F32, _VP, _I32, _VP, _SZ, _VP]
-        for f in (L.bitlinear_kv_step, L.bitlinear_embed, L.bitlinear_embed_bwd_workspace_bytes,
+        szp = ctypes.POINTER(_SZ)
+        L.bitlinear_q4_bytes.argtypes = [_I64, _I64, _I32, szp, szp]
+        L.bitlinear_q4_pack.argtypes = [_VP, _I32, _I64, _I64, _I32, _VP, _VP, _VP]
+        L.bitlinear_q4_fwd.argtypes = [_VP, _VP, _I64, _I64, _VP, _VP, _I32, _I64, _VP, _VP]
+        for f in (L.bitlinear_q4_bytes, L.bitlinear_q4_pack, L.bitlinear_q4_fwd, L.bitlinear_kv_step, L.bitlinear_embed, L.bitlinear_embed_bwd_workspace_bytes,
                   L.bitlinear_embed_bwd):
             f.restype = ctypes.c_int
         _fns = L
@@ -60,6 +66,21 @@ def bitlinear_embed_bwd_workspace_bytes(T, K):
 
 def bitlinear_embed_bwd(dy, dy_dtype, ids, T, V, K, scale, dtable, flags, ws, ws_bytes, stream) -> int:
     return _lib().bitlinear_embed_bwd(dy, dy_dtype, ids, T, V, K, scale, dtable, flags, ws, ws_bytes, stream)
+
+
+def bitlinear_q4_bytes(n, K, group):
+    """Returns (status, code_bytes, scale_bytes)."""
+    c, s = _SZ(), _SZ()
+    st = _lib().bitlinear_q4_bytes(n, K, group, ctypes.byref(c), ctypes.byref(s))
+    return st, c.value, s.value
+
+
+def bitlinear_q4_pack(W, w_dtype, n, K, group, codes, scales, stream) -> int:
+    return _lib().bitlinear_q4_pack(W, w_dtype, n, K, group, codes, scales, stream)
+
+
+def bitlinear_q4_fwd(xq, x_scale, T, K, codes, scales, group, n, y, stream) -> int:
+    return _lib().bitlinear_q4_fwd(xq, x_scale, T, K, codes, scales, group, n, y, stream)
 
 
 # ---------------------------------------------------------------------------------------------
@@ -178,4 +199,50 @@ def embed_bwd(dy, ids, V: int, scale: float = 1.0, accumulate: bool = False, out
         _buf(ws, torch.uint8, wsb, ix, "ws")
     _enqueue(ix, "bitlinear_embed_bwd", _lib().bitlinear_embed_bwd, dy.data_ptr(), gd, ids.data_ptr(), T, V, K,
              scale, out.data_ptr(), BL_EMBED_ACCUM if accumulate else 0, ws.data_ptr(), ws.numel())
+    return out
+
+
+_q4_sizes = functools.lru_cache(maxsize=64)(bitlinear_q4_bytes)
+
+
+def q4_pack(W, group: int = 64, out=None):
+    """W [n][K] (fp32 or bf16) in 4 bits with a bf16 scale per ``group`` (32, 64 or 128) columns of a row.
+
+    Returns (codes uint8, scales bf16), laid out as ``q4_fwd`` takes them; ``out`` may supply them."""
+    import torch
+    n, K = _table(W, "W")
+    ix = _device(W, "W")
+    wd = _rows(W, W.shape, ix, "W")
+    st, cb, sb = _q4_sizes(n, K, group)
+    _check(st, "bitlinear_q4_bytes")
+    if out is None:
+        out = W.new_empty(cb, dtype=torch.uint8), W.new_empty(sb // 2, dtype=torch.bfloat16)
+    codes, scales = out
+    _buf(codes, torch.uint8, cb, ix, "codes")
+    _buf(scales, torch.bfloat16, sb // 2, ix, "scales")
+    _enqueue(ix, "bitlinear_q4_pack", _lib().bitlinear_q4_pack, W.data_ptr(), wd, n, K, group, codes.data_ptr(),
+             scales.data_ptr())
+    return codes, scales
+
+
+def q4_fwd(xq, scale, K: int, codes, scales, n: int, group: int = 64, out=None):
+    """y [T][n] fp32 of int8 rows xq [T][K] with their scales [T] (``norm_quant``'s or ``act_quant``'s) and
+    weights from ``q4_pack``.  ``out`` may supply y."""
+    import torch
+    if len(xq.shape) != 2 or xq.shape[1] != K:
+        raise ValueError(f"xq: must be [T][{K}], got {tuple(xq.shape)}")
+    T = xq.shape[0]
+    ix = _device(xq, "xq")
+    _buf(xq, torch.int8, T * K, ix, "xq")
+    _buf(scale, torch.float32, T, ix, "scale")
+    st, cb, sb = _q4_sizes(n, K, group)
+    _check(st, "bitlinear_q4_bytes")
+    _buf(codes, torch.uint8, cb, ix, "codes")
+    _buf(scales, torch.bfloat16, sb // 2, ix, "scales")
+    if out is None:
+        out = scale.new_empty((T, n))
+    else:
+        _rows(out, (T, n), ix, "out", torch.float32)
+    _enqueue(ix, "bitlinear_q4_fwd", _lib().bitlinear_q4_fwd, xq.data_ptr(), scale.data_ptr(), T, K,
+             codes.data_ptr(), scales.data_ptr(), group, n, out.data_ptr())
     return out

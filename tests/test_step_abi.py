@@ -214,3 +214,92 @@ def test_embed_reference_by_differences():
         e = np.zeros((5, 8))
         e[v, 2] = 0.5
         assert abs((f(table + e) - f(table - e)) - d[v, 2]) < 1e-5
+
+
+# ---- weights in 4 bits ----
+
+@pytest.mark.parametrize("n,cols,group,want", [
+    (16, 128, 64, 0), (1, 32, 32, 0), (0, 128, 64, EINVAL), (-1, 128, 64, EINVAL), ((1 << 27) + 1, 128, 64, EINVAL),
+    (16, 0, 64, EINVAL), (16, 96, 64, EINVAL), (16, 64, 128, EINVAL), (16, 1 << 17, 128, EINVAL), (16, 128, 16, ENOTSUP),
+    (16, 128, 0, ENOTSUP), (16, 128, 256, ENOTSUP)])
+def test_q4_sizes(n, cols, group, want):
+    st, codes, scales = K.bitlinear_q4_bytes(n, cols, group)
+    assert st == want
+    if not st:
+        blocks = -(-n // 16) * -(-cols // 128)
+        assert codes == 1024 * blocks and scales == blocks * 16 * (128 // group) * 2
+
+
+def _q4_pack(**kw):
+    a = dict(W=P, wd=0, n=100, K=256, group=64, codes=P + SLOT, scales=P + 2 * SLOT)
+    a.update(kw)
+    return K.bitlinear_q4_pack(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(wd=2), ENOTSUP), (dict(group=48), ENOTSUP), (dict(n=0), EINVAL), (dict(K=200), EINVAL), (dict(W=None), EINVAL),
+    (dict(W=P + 8), EINVAL), (dict(codes=None), EINVAL), (dict(codes=P + SLOT + 4), EINVAL), (dict(scales=None), EINVAL),
+    (dict(scales=P + 2 * SLOT + 2), EINVAL), (dict(codes=P + 16), EINVAL), (dict(scales=P + 100 * 1024 - 16), EINVAL),
+    (dict(scales=P + SLOT + 14 * 1024 - 16), EINVAL)])
+def test_q4_pack_rejects(kw, want):
+    assert _q4_pack(**kw) == want
+
+
+def _q4_fwd(**kw):
+    a = dict(xq=P, xs=P + SLOT, T=4, K=256, codes=P + 2 * SLOT, scales=P + 3 * SLOT, group=64, n=100, y=P + 4 * SLOT)
+    a.update(kw)
+    return K.bitlinear_q4_fwd(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(group=1), ENOTSUP), (dict(n=0), EINVAL), (dict(K=0), EINVAL), (dict(K=160), EINVAL), (dict(T=-1), EINVAL),
+    (dict(T=1 << 22), EINVAL), (dict(T=1 << 20, n=1 << 20), EINVAL), (dict(xq=None), EINVAL), (dict(xq=P + 8), EINVAL),
+    (dict(xs=None), EINVAL), (dict(xs=P + SLOT + 2), EINVAL), (dict(codes=None), EINVAL), (dict(codes=P + 2 * SLOT + 8), EINVAL),
+    (dict(scales=P + 3 * SLOT + 8), EINVAL), (dict(scales=None), EINVAL), (dict(y=None), EINVAL), (dict(y=P + 4 * SLOT + 8), EINVAL),
+    (dict(y=P), EINVAL), (dict(y=P + SLOT), EINVAL), (dict(y=P + 2 * SLOT + 14 * 1024 - 16), EINVAL), (dict(y=P + 3 * SLOT), EINVAL),
+    (dict(T=0, xq=None, xs=None, codes=None, scales=None, y=None), 0)])
+def test_q4_fwd_rejects(kw, want):
+    assert _q4_fwd(**kw) == want
+
+
+def test_q4_wrappers_reject():
+    W, U8 = Strided((100, 256), F32), torch.uint8
+    codes, scales = Strided(14 * 1024, U8), Strided(14 * 32, BF)
+    for w, kw in [(Strided(256, F32), {}), (Strided((100, 256), torch.float16), {}), (Strided((100, 256), F32, (512, 1)), {}),
+                  (W, dict(out=(Strided(14 * 1024 - 1, U8), scales))), (W, dict(out=(Strided(14 * 1024, I8), scales))),
+                  (W, dict(out=(codes, Strided(14 * 32 - 1, BF)))), (W, dict(out=(codes, Strided(14 * 32, F32))))]:
+        with pytest.raises(ValueError):
+            S.q4_pack(w, **dict(dict(out=(codes, scales)), **kw))
+    for k, group in ((200, 64), (256, 16)):
+        with pytest.raises(S.BitLinearError):
+            S.q4_pack(Strided((100, k), F32), group, out=(codes, scales))
+    ok = dict(xq=Strided((4, 256), I8), scale=Strided(4, F32), K=256, codes=codes, scales=scales, n=100)
+    y = Strided((4, 100), F32)
+    for kw in [dict(xq=Strided(256, I8)), dict(xq=Strided((4, 128), I8)), dict(xq=Strided((4, 256), U8)), dict(scale=Strided(3, F32)),
+               dict(scale=Strided(4, BF)), dict(codes=Strided(1024, U8)), dict(scales=Strided(14 * 16, BF)), dict(n=113),
+               dict(scales=Strided(14 * 32, BF, device=OTHER)), dict(out=Strided((4, 99), F32)), dict(out=Strided((4, 100), BF))]:
+        with pytest.raises(ValueError):
+            S.q4_fwd(**dict(ok, **dict(dict(out=y), **kw)))
+    with pytest.raises(S.BitLinearError):
+        S.q4_fwd(**dict(ok, out=y, group=33))
+
+
+def test_q4_calls_run_on_the_device_of_their_tensors(monkeypatch):
+    def calls(t):
+        codes, scales = t(14 * 1024, torch.uint8), t(14 * 32, BF)
+        S.q4_pack(t((100, 256), F32), out=(codes, scales))
+        S.q4_fwd(t((4, 256), I8), t(4, F32), 256, codes, scales, 100, out=t((4, 100), F32))
+        return ["bitlinear_q4_pack", "bitlinear_q4_fwd"]
+    _on_devices(monkeypatch, calls)
+
+
+def test_q4_reference_layout_by_hand():
+    """One element of each kind in its place."""
+    q, s = np.zeros((17, 256), np.int8), np.zeros((17, 4), np.float32)
+    q[3, 70], q[16, 128 + 5], s[3, 1], s[16, 2] = -3, 6, 1.0, 2.0
+    codes, scales = R.q4_pack(q, s, 64)
+    # row 3, block 0, column 70 = 64 + 6: step 1, h 0, dword 2, byte 2 high nibble; row 16: tile 1, block 1, column 5
+    assert codes[3 * 16 + 2 * 4 + 2] == 13 << 4 and codes[(3 * 64) * 16 + 1] == 6 << 4 and np.count_nonzero(codes) == 2
+    assert scales[(0 * 4 + 0) * 8 + 4 + 3] == 0x3F80 and scales[(3 * 4 + 0) * 8 + 0] == 0x4000
+    q, s = R.q4_quantize(np.array([[7, -7, 3.5, 0.5, 1.5, 0.2] + [0] * 26], np.float32), 32)
+    assert s[0, 0] == 1.0 and q[0, :6].tolist() == [7, -7, 4, 0, 2, 0]
