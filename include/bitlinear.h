@@ -747,6 +747,35 @@ int bitlinear_q4_pack(const void* W, int w_dtype, int64_t n, int64_t K, int grou
 int bitlinear_q4_fwd(const int8_t* xq, const float* x_scale, int64_t T, int64_t K, const uint8_t* codes,
                      const uint16_t* scales, int group, int64_t n, float* y, void* stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * A token per row of logits, drawn by one given number per row.
+ *
+ * x is x_dtype [B][V] with rows row_stride elements apart (row_stride >= V; any alignment of the elements;
+ * 16-byte aligned rows take the vector path).  A logit that is -inf or NaN is masked.  With top the row's largest
+ * logit and its tokens in the order of falling logits, equal ones by index (-0 equals 0):
+ *   w_i    = rint(2^40 * exp((x_i - top) / temperature)), a whole number, from fp64 within a few ulp; where
+ *            top is +inf, 2^40 for its equals and 0 for the others
+ *   S_k    = the sum of the first top_k weights
+ *   S_p    = the sum of the shortest prefix of at least double(top_p) * double(S_k)
+ *   S_m    = the sum of the weights of at least double(min_p) * 2^40, of the first one at least
+ *   token  = the first one at which the running sum passes min(S - 1, floor(u * double(S))),
+ *            S = min(S_k, S_p, S_m)
+ * Sums of whole numbers do not depend on their order: the token is the same in every run.  Settings are per row,
+ * on the device: temperature (fp32; not above 0, or NaN: the largest logit, the lowest index among equals; NULL:
+ * 1), top_k (int32; below 1, or NULL: off), top_p (fp32; from 1 on, NaN or NULL: off; not above 0: the largest
+ * alone), min_p (fp32; not above 0, NaN or NULL: off).  u is fp64 [B], in [0, 1) (below 0 or NaN counts as 0, from 1 on
+ * as the last token that is left).  logprob_opt (fp32 [B], or NULL) is the token's log probability under the
+ * logits themselves, whatever the settings: x - log(sum exp(x)).  A row whose logits are all masked gives token -1
+ * and logprob -inf.
+ *
+ * token is int32 [B]; token, logprob_opt and ws may overlap nothing.  ws: bitlinear_sample_workspace_bytes of device
+ * scratch (256-byte aligned; contents on entry irrelevant).  0 <= B <= 65535, 1 <= V < 2^31.  Three launches. */
+int bitlinear_sample_workspace_bytes(int64_t B, int64_t V, size_t* ws_bytes);
+int bitlinear_sample(const void* x, int x_dtype, int64_t B, int64_t V, int64_t row_stride,
+                     const float* temperature_opt, const int32_t* top_k_opt, const float* top_p_opt,
+                     const float* min_p_opt, const double* u, int32_t* token, float* logprob_opt,
+                     void* ws, size_t ws_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* bitlinear_strerror(int status);
 

@@ -123,3 +123,35 @@ def q4_forward(xq, x_scale, q, s, group):
         mag += np.abs(part)
     xs = np.asarray(x_scale, np.float64)[:, None]
     return y * xs, mag * xs
+
+
+def sample_row(x, u, temperature=1.0, k=0, p=1.0, min_p=0.0):
+    """(token, log probability, its sum of p_i |x_i - top|) of one row, by walking down its tokens."""
+    x = np.asarray(x, np.float64) + 0.0
+    x = np.where(np.isnan(x), -np.inf, x)
+    order = sorted(range(len(x)), key=lambda i: (-x[i], i))
+    top = x[order[0]]
+    if top == -np.inf:
+        return -1, -np.inf, 0.0
+    d = np.where(x == top, 0.0, np.where(np.isinf(x) | (top == np.inf), -np.inf, x - (0 if top == np.inf else top)))
+    e = np.exp(d)
+    token = order[0]
+    if temperature > 0:
+        with np.errstate(all="ignore"):
+            z = np.where(d == 0, 0.0, np.where(d == -np.inf, d, d / np.float64(temperature)))
+        w = [int(v) for v in np.rint(np.exp(z) * 2.0 ** 40)]
+        left = order[:k] if 0 < k < len(order) else order
+        p = 1.0 if not p < 1 else max(float(p), 0.0)
+        goal, total = p * float(sum(w[i] for i in left)), 0
+        for n, i in enumerate(left):
+            if n and (p < 1 and float(total) >= goal or min_p > 0 and float(w[i]) < float(min_p) * 2.0 ** 40):
+                break
+            total += w[i]
+        r = min(int(min(u, 1.0) * float(total)) if u > 0 else 0, total - 1)
+        for i in left:
+            r -= w[i]
+            if r < 0:
+                token = i
+                break
+    live = e > 0
+    return token, d[token] - np.log(e.sum()), float((e[live] * -d[live]).sum() / e.sum())

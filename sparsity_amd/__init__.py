@@ -28,6 +28,6 @@ from .block import (  # noqa: F401
 )
 from .step import (  # noqa: F401
     BL_EMBED_ACCUM, KvStep, bitlinear_embed, bitlinear_embed_bwd, bitlinear_embed_bwd_workspace_bytes,
-    bitlinear_kv_step, bitlinear_q4_bytes, bitlinear_q4_fwd, bitlinear_q4_pack, embed, embed_bwd, kv_step,
-    q4_fwd, q4_pack,
+    bitlinear_kv_step, bitlinear_q4_bytes, bitlinear_q4_fwd, bitlinear_q4_pack, bitlinear_sample,
+    bitlinear_sample_workspace_bytes, embed, embed_bwd, kv_step, q4_fwd, q4_pack, sample,
 )

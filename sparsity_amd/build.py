@@ -11,7 +11,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libbitlinear.so")
 SOURCES = ["bitlinear_api.hip", "pack.hip", "act_quant.hip", "fwd.hip", "gemv_group.hip", "bwd.hip",
            "chain.hip", "gemv6.hip", "block_api.hip", "norm.hip", "rope.hip", "paged_attn.hip",
-           "step_api.hip", "kv_step.hip", "embed.hip", "q4.hip"]
+           "step_api.hip", "kv_step.hip", "embed.hip", "q4.hip", "sample.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

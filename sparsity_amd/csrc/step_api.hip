@@ -24,6 +24,7 @@ bool clash(const Span (&in)[NI], const Span (&out)[NO], const int (&same)[NO]) {
 }
 
 constexpr int64_t kQ4MaxN = (int64_t)1 << 27, kQ4MaxK = (int64_t)1 << 16;
+constexpr int64_t kSampleMaxB = 65535;
 
 }  // namespace
 
@@ -137,6 +138,55 @@ int bitlinear_q4_fwd(const int8_t* xq, const float* x_scale, int64_t T, int64_t 
   const bl::Q4Args a = {xq, x_scale, codes, scales, y, n, (n + 15) / 16, (int32_t)T, (int32_t)K,
                         (int32_t)((K + 127) / 128), 0, 0, 0};
   return status_of(bl::launch_q4_fwd(a, group, (hipStream_t)stream));
+}
+
+int bitlinear_sample_workspace_bytes(int64_t B, int64_t V, size_t* ws_bytes) {
+  if (B < 0 || B > kSampleMaxB || V < 1 || V > INT32_MAX || !ws_bytes) return BL_EINVAL;
+  bl::SampleArgs a = {};
+  a.B = B;
+  a.V = V;
+  *ws_bytes = B ? bl::sample_split(a, nullptr) : 0;
+  return BL_OK;
+}
+
+int bitlinear_sample(const void* x, int x_dtype, int64_t B, int64_t V, int64_t row_stride,
+                     const float* temperature_opt, const int32_t* top_k_opt, const float* top_p_opt,
+                     const float* min_p_opt, const double* u, int32_t* token, float* logprob_opt,
+                     void* ws, size_t ws_bytes, void* stream) {
+  if (!float_dtype(x_dtype)) return BL_ENOTSUP;
+  size_t need = 0;
+  const int st = bitlinear_sample_workspace_bytes(B, V, &need);
+  if (st != BL_OK) return st;
+  if (B > 1 && (row_stride < V || row_stride > ((int64_t)1 << 40))) return BL_EINVAL;
+  if (B == 0) return BL_OK;
+  if (B == 1) row_stride = V;              // never a step
+  const int64_t e = esize(x_dtype);
+  if (!aligned(x, e) || !aligned(u, 8) || !aligned(token, 4) || !aligned(ws, 256)) return BL_EINVAL;
+  if ((temperature_opt && !aligned(temperature_opt, 4)) || (top_k_opt && !aligned(top_k_opt, 4)) ||
+      (top_p_opt && !aligned(top_p_opt, 4)) || (min_p_opt && !aligned(min_p_opt, 4)) ||
+      (logprob_opt && !aligned(logprob_opt, 4)))
+    return BL_EINVAL;
+  if (ws_bytes < need) return BL_ENOSPC;
+  const uint64_t b4 = (uint64_t)B * 4;
+  const Span in[6] = {{x, (uint64_t)((B - 1) * row_stride + V) * e}, {temperature_opt, b4}, {top_k_opt, b4},
+                      {top_p_opt, b4}, {min_p_opt, b4}, {u, b4 * 2}};
+  const Span out[3] = {{token, b4}, {logprob_opt, b4}, {ws, need}};
+  if (clash(in, out, {-1, -1, -1})) return BL_EINVAL;
+  bl::SampleArgs a = {};
+  a.x = x;
+  a.stride = row_stride;
+  a.B = B;
+  a.V = V;
+  a.temperature = temperature_opt;
+  a.top_k = top_k_opt;
+  a.top_p = top_p_opt;
+  a.min_p = min_p_opt;
+  a.u = u;
+  a.token = token;
+  a.logprob = logprob_opt;
+  bl::sample_split(a, (char*)ws);
+  const bool vec = aligned(x, 16) && (B == 1 || row_stride * e % 16 == 0);
+  return status_of(bl::launch_sample(a, x_dtype == BL_DTYPE_BF16, vec, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -109,4 +109,50 @@ struct Q4Args {
 };
 hipError_t launch_q4_fwd(const Q4Args& a, int group, hipStream_t s);
 
+// ---- sampling ----
+constexpr int kSampleBins = 512;
+
+struct SampleArgs {
+  const void* x;
+  int64_t stride, B, V;
+  const float* temperature;   // nullptr: 1
+  const int32_t* top_k;       // nullptr: off, like the next two
+  const float* top_p;
+  const float* min_p;
+  const double* u;
+  int32_t* token;
+  float* logprob;             // nullptr: not wanted
+  int64_t chunk, chunks;      // of a row: logits each, number
+  // workspace, [B][chunks] each
+  unsigned long long* top;    // largest logit and its index
+  unsigned long long* kept;   // weights that min-p keeps
+  double* exps;               // exp(x - the row's largest)
+  unsigned long long* w_bins; // [kSampleBins] weights
+  uint32_t* n_bins;           // [kSampleBins] tokens
+  float* least;               // least finite logit
+};
+// Fills chunk and chunks, and the workspace's pointers from ws; returns its bytes.
+inline size_t sample_split(SampleArgs& a, char* ws) {
+  // a few blocks per CU from all rows together, of 2048 logits at least
+  int64_t most = 1024 / (a.B > 0 ? a.B : 1);
+  most = most < 4 ? 4 : most > 32 ? 32 : most;
+  a.chunk = ((a.V + most - 1) / most + 2047) / 2048 * 2048;
+  a.chunks = (a.V + a.chunk - 1) / a.chunk;
+  const size_t n = (size_t)a.B * (size_t)a.chunks;
+  size_t off = 0;
+  auto part = [&](size_t bytes) {
+    char* p = ws + off;
+    off += (bytes + 255) / 256 * 256;
+    return p;
+  };
+  a.top = (unsigned long long*)part(n * 8);
+  a.kept = (unsigned long long*)part(n * 8);
+  a.exps = (double*)part(n * 8);
+  a.w_bins = (unsigned long long*)part(n * kSampleBins * 8);
+  a.n_bins = (uint32_t*)part(n * kSampleBins * 4);
+  a.least = (float*)part(n * 4);
+  return off;
+}
+hipError_t launch_sample(const SampleArgs& a, bool bf16, bool vec, hipStream_t s);
+
 }  // namespace bl

@@ -1,10 +1,10 @@
 """ctypes binding of the operators around a model's blocks: what turns requests and token ids into the
-first block's input.
+first block's input, and the last block's output into the next token ids.
 
 Raw calls mirror the C ABI (``include/bitlinear.h``): ``bitlinear_kv_step``, ``bitlinear_embed``,
 ``bitlinear_embed_bwd_workspace_bytes``, ``bitlinear_embed_bwd``, ``bitlinear_q4_bytes``,
-``bitlinear_q4_pack``, ``bitlinear_q4_fwd``.  ``kv_step`` / ``embed`` / ``embed_bwd`` / ``q4_pack`` /
-``q4_fwd`` take torch tensors, check them (the C ABI receives bare pointers), allocate outputs that
+``bitlinear_q4_pack``, ``bitlinear_q4_fwd``, ``bitlinear_sample_workspace_bytes``, ``bitlinear_sample``.
+``kv_step`` / ``embed`` / ``embed_bwd`` / ``q4_pack`` / ``q4_fwd`` / ``sample`` take torch tensors, check them (the C ABI receives bare pointers), allocate outputs that
 are not given and enqueue on torch's current stream.  Every step runs in HIP kernels.
 """
 from __future__ import annotations
@@ -36,7 +36,9 @@ def _lib():
         L.bitlinear_q4_bytes.argtypes = [_I64, _I64, _I32, szp, szp]
         L.bitlinear_q4_pack.argtypes = [_VP, _I32, _I64, _I64, _I32, _VP, _VP, _VP]
         L.bitlinear_q4_fwd.argtypes = [_VP, _VP, _I64, _I64, _VP, _VP, _I32, _I64, _VP, _VP]
-        for f in (L.bitlinear_q4_bytes, L.bitlinear_q4_pack, L.bitlinear_q4_fwd, L.bitlinear_kv_step, L.bitlinear_embed, L.bitlinear_embed_bwd_workspace_bytes,
+        L.bitlinear_sample_workspace_bytes.argtypes = [_I64, _I64, szp]
+        L.bitlinear_sample.argtypes = [_VP, _I32, _I64, _I64, _I64, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]
+        for f in (L.bitlinear_sample_workspace_bytes, L.bitlinear_sample, L.bitlinear_q4_bytes, L.bitlinear_q4_pack, L.bitlinear_q4_fwd, L.bitlinear_kv_step, L.bitlinear_embed, L.bitlinear_embed_bwd_workspace_bytes,
                   L.bitlinear_embed_bwd):
             f.restype = ctypes.c_int
         _fns = L
@@ -81,6 +83,19 @@ def bitlinear_q4_pack(W, w_dtype, n, K, group, codes, scales, stream) -> int:
 
 def bitlinear_q4_fwd(xq, x_scale, T, K, codes, scales, group, n, y, stream) -> int:
     return _lib().bitlinear_q4_fwd(xq, x_scale, T, K, codes, scales, group, n, y, stream)
+
+
+def bitlinear_sample_workspace_bytes(B, V):
+    """Returns (status, ws_bytes)."""
+    ws = _SZ()
+    st = _lib().bitlinear_sample_workspace_bytes(B, V, ctypes.byref(ws))
+    return st, ws.value
+
+
+def bitlinear_sample(x, x_dtype, B, V, row_stride, temperature, top_k, top_p, min_p, u, token, logprob, ws,
+                     ws_bytes, stream) -> int:
+    return _lib().bitlinear_sample(x, x_dtype, B, V, row_stride, temperature, top_k, top_p, min_p, u, token, logprob,
+                                   ws, ws_bytes, stream)
 
 
 # ---------------------------------------------------------------------------------------------
@@ -246,3 +261,55 @@ def q4_fwd(xq, scale, K: int, codes, scales, n: int, group: int = 64, out=None):
     _enqueue(ix, "bitlinear_q4_fwd", _lib().bitlinear_q4_fwd, xq.data_ptr(), scale.data_ptr(), T, K,
              codes.data_ptr(), scales.data_ptr(), group, n, out.data_ptr())
     return out
+
+
+_sample_ws = functools.lru_cache(maxsize=64)(bitlinear_sample_workspace_bytes)
+
+
+def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, want_logprob: bool = False, out=None,
+           ws=None):
+    """A token per row of logits [B][V] (fp32 or bf16, any row stride): (int32 [B], log probabilities or None).
+
+    u (fp64 [B], in [0, 1)) draws the tokens: the same numbers give the same tokens.  Each row has its own
+    settings, tensors [B]: temperature (fp32; 0: the largest logit), top_k (int32; 0: off), top_p (fp32; 1: off), min_p
+    (fp32; 0: off), applied in this order; None: 1, and off.  Logits that are -inf or NaN are masked; a row of
+    them gives -1.  The log probability (fp32 [B]) is that of the token under the logits themselves.  ``out``
+    may supply (tokens, log probabilities or None), ``ws`` a uint8 workspace.
+    """
+    import torch
+    shape = logits.shape
+    if len(shape) != 2:
+        raise ValueError(f"logits: must be [B][V], got {tuple(shape)}")
+    B, V = shape
+    ix = _device(logits, "logits")
+    xd = _dt(logits.dtype, "logits")
+    s = logits.stride()
+    if s[1] != 1 and V > 1:
+        raise ValueError("logits: the last dimension must be contiguous")
+    _buf(u, torch.float64, B, ix, "u")
+    if temperature is not None:
+        _buf(temperature, torch.float32, B, ix, "temperature")
+    if top_k is not None:
+        _buf(top_k, torch.int32, B, ix, "top_k")
+    if top_p is not None:
+        _buf(top_p, torch.float32, B, ix, "top_p")
+    if min_p is not None:
+        _buf(min_p, torch.float32, B, ix, "min_p")
+    if out is None:
+        token = u.new_empty(B, dtype=torch.int32)
+        logprob = u.new_empty(B, dtype=torch.float32) if want_logprob else None
+    else:
+        token, logprob = out
+        _buf(token, torch.int32, B, ix, "token")
+        if logprob is not None:
+            _buf(logprob, torch.float32, B, ix, "logprob")
+    st, wsb = _sample_ws(B, V)
+    _check(st, "bitlinear_sample_workspace_bytes")
+    if ws is None:
+        ws = u.new_empty(wsb, dtype=torch.uint8)
+    else:
+        _buf(ws, torch.uint8, wsb, ix, "ws")
+    _enqueue(ix, "bitlinear_sample", _lib().bitlinear_sample, logits.data_ptr(), xd, B, V, s[0],
+             _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), u.data_ptr(), token.data_ptr(), _ptr(logprob),
+             ws.data_ptr(), ws.numel())
+    return token, logprob

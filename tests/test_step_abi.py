@@ -303,3 +303,73 @@ def test_q4_reference_layout_by_hand():
     assert scales[(0 * 4 + 0) * 8 + 4 + 3] == 0x3F80 and scales[(3 * 4 + 0) * 8 + 0] == 0x4000
     q, s = R.q4_quantize(np.array([[7, -7, 3.5, 0.5, 1.5, 0.2] + [0] * 26], np.float32), 32)
     assert s[0, 0] == 1.0 and q[0, :6].tolist() == [7, -7, 4, 0, 2, 0]
+
+
+# ---- sampling ----
+
+@pytest.mark.parametrize("B,V,want", [(1, 1, 0), (65535, 1000, 0), (0, 10, 0), (-1, 10, EINVAL), (65536, 10, EINVAL),
+                                      (1, 0, EINVAL), (1, -5, EINVAL), (1, 1 << 31, EINVAL)])
+def test_sample_workspace(B, V, want):
+    st, n = K.bitlinear_sample_workspace_bytes(B, V)
+    assert st == want and (st or n % 256 == 0 and (n > 0) == (B > 0))
+
+
+def _sample(**kw):
+    a = dict(x=P, xd=0, B=4, V=1000, stride=1000, temp=P + SLOT, k=P + 2 * SLOT, p=P + 3 * SLOT, m=P + 4 * SLOT,
+             u=P + 5 * SLOT, token=P + 6 * SLOT, logprob=P + 7 * SLOT, ws=P + 8 * SLOT, wsb=1 << 20)
+    a.update(kw)
+    return K.bitlinear_sample(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(xd=2), ENOTSUP), (dict(B=-1), EINVAL), (dict(B=65536), EINVAL), (dict(V=0), EINVAL), (dict(stride=999), EINVAL),
+    (dict(stride=0), EINVAL), (dict(stride=(1 << 40) + 1), EINVAL), (dict(x=None), EINVAL), (dict(x=P + 2), EINVAL),
+    (dict(xd=1, x=P + 1), EINVAL), (dict(temp=P + SLOT + 1), EINVAL), (dict(k=P + 2 * SLOT + 2), EINVAL),
+    (dict(p=P + 3 * SLOT + 1), EINVAL), (dict(m=P + 4 * SLOT + 2), EINVAL), (dict(u=None), EINVAL),
+    (dict(u=P + 5 * SLOT + 4), EINVAL), (dict(token=None), EINVAL), (dict(token=P + 6 * SLOT + 2), EINVAL),
+    (dict(logprob=P + 7 * SLOT + 2), EINVAL), (dict(ws=None), EINVAL), (dict(ws=P + 8 * SLOT + 128), EINVAL),
+    (dict(wsb=0), ENOSPC), (dict(wsb=K.bitlinear_sample_workspace_bytes(4, 1000)[1] - 1), ENOSPC), (dict(token=P), EINVAL),
+    (dict(token=P + 15996), EINVAL), (dict(token=P + SLOT), EINVAL), (dict(logprob=P + 2 * SLOT), EINVAL),
+    (dict(token=P + 5 * SLOT + 28), EINVAL), (dict(logprob=P + 6 * SLOT + 8), EINVAL), (dict(ws=P + 256), EINVAL),
+    (dict(ws=P + 3 * SLOT), EINVAL), (dict(ws=P + 7 * SLOT), EINVAL), (dict(token=P + 4 * SLOT), EINVAL),
+    (dict(B=0, x=None, u=None, token=None, ws=None, wsb=0), 0)])
+def test_sample_rejects(kw, want):
+    assert _sample(**kw) == want
+
+
+def test_sample_wrapper_rejects():
+    U8, F64 = torch.uint8, torch.float64
+    ok = dict(logits=Strided((4, 1000), F32), u=Strided(4, F64), out=(Strided(4, I32), Strided(4, F32)), ws=Strided(1 << 20, U8))
+    for kw in [dict(logits=Strided(1000, F32)), dict(logits=Strided((4, 1000), torch.float16)),
+               dict(logits=Strided((4, 1000), F32, (1, 4))), dict(logits=Strided((4, 1000), F32, device=torch.device("cpu"))),
+               dict(u=Strided(4, F32)), dict(u=Strided(3, F64)), dict(u=Strided(4, F64, device=OTHER)),
+               dict(temperature=Strided(3, F32)), dict(temperature=Strided(4, F64)), dict(top_k=Strided(4, I64)),
+               dict(top_k=Strided(1, I32)), dict(top_p=Strided(4, BF)), dict(min_p=Strided(4, I32)), dict(min_p=Strided(2, F32)),
+               dict(out=(Strided(4, I64), None)), dict(out=(Strided(3, I32), None)), dict(out=(Strided(4, I32), Strided(4, BF))),
+               dict(ws=Strided(64, U8)), dict(ws=Strided(1 << 20, I8))]:
+        with pytest.raises(ValueError):
+            S.sample(**dict(ok, **kw))
+    with pytest.raises(S.BitLinearError):
+        S.sample(Strided((4, 0), F32), ok["u"])
+
+
+def test_sample_calls_run_on_the_device_of_their_tensors(monkeypatch):
+    def calls(t):
+        S.sample(t((4, 1000), F32), t(4, torch.float64), t(4, F32), out=(t(4, I32), None), ws=t(1 << 20, torch.uint8))
+        return ["bitlinear_sample"]
+    _on_devices(monkeypatch, calls)
+
+
+def test_sample_reference_by_hand():
+    """Probabilities 1/2, 1/4, 1/8, 1/8 (two equal logits)."""
+    x = np.log([0.125, 0.5, 0.25, 0.125]) + 3
+    x[0] = x[3]
+    draw = lambda u, **kw: R.sample_row(x, u, **kw)[0]  # noqa: E731
+    assert [draw(u) for u in (0.0, 0.49, 0.51, 0.74, 0.76, 0.87, 0.88, 0.999)] == [1, 1, 2, 2, 0, 0, 3, 3]
+    assert [draw(u, k=2) for u in (0.6, 0.7, 0.999)] == [1, 2, 2]
+    assert [draw(0.999, p=p) for p in (0.4, 0.6, 0.8, 0.9, 1.0)] == [1, 2, 0, 3, 3]
+    assert [draw(0.999, min_p=m) for m in (0.9, 0.45, 0.2, 0.0)] == [1, 2, 3, 3]
+    assert draw(0.999, k=3, p=0.7) == 2            # 0.7 of the 7/8 that top-k leaves: 0.6125 of 0.75
+    assert draw(0.999, temperature=0.0) == 1
+    assert abs(R.sample_row(x, 0.6)[1] - np.log(0.25)) < 1e-12
+    assert R.sample_row([-np.inf, np.nan], 0.5)[:2] == (-1, -np.inf)
