@@ -111,6 +111,17 @@ hipError_t launch_q4_fwd(const Q4Args& a, int group, hipStream_t s);
 
 // ---- sampling ----
 constexpr int kSampleBins = 512;
+constexpr int kSampleChunks = 16;   // of a row, at most
+constexpr int kSampleList = 4096;   // tokens that a row's questions are answered from
+
+// What a row's questions need, and where they start from.
+struct SamplePlan {
+  unsigned long long lo[3], hi[3];           // places of the tokens to gather, and their bins
+  int32_t bin0[3], bin1[3];
+  uint32_t ranges;                           // 0: too many tokens
+  uint32_t upto;                             // tokens from the row's largest on to the last of them
+  uint32_t count, arrived;                   // gathered tokens, blocks of the launch that are done
+};
 
 struct SampleArgs {
   const void* x;
@@ -130,13 +141,18 @@ struct SampleArgs {
   unsigned long long* w_bins; // [kSampleBins] weights
   uint32_t* n_bins;           // [kSampleBins] tokens
   float* least;               // least finite logit
+  float* most;                // [B][groups] largest logit of each 64
+  int64_t groups;
+  unsigned long long* lists;  // [B][kSampleList] gathered tokens
+  SamplePlan* plan;           // [B]
+  unsigned long long* sums;   // [B][kSampleBins][2] running sums by bin: weights, tokens
 };
 // Fills chunk and chunks, and the workspace's pointers from ws; returns its bytes.
 inline size_t sample_split(SampleArgs& a, char* ws) {
-  // a few blocks per CU from all rows together, of 2048 logits at least
+  // a few blocks per CU from all rows together, of 4096 logits at least
   int64_t most = 1024 / (a.B > 0 ? a.B : 1);
-  most = most < 4 ? 4 : most > 32 ? 32 : most;
-  a.chunk = ((a.V + most - 1) / most + 2047) / 2048 * 2048;
+  most = most < 4 ? 4 : most > kSampleChunks ? kSampleChunks : most;
+  a.chunk = ((a.V + most - 1) / most + 4095) / 4096 * 4096;
   a.chunks = (a.V + a.chunk - 1) / a.chunk;
   const size_t n = (size_t)a.B * (size_t)a.chunks;
   size_t off = 0;
@@ -151,6 +167,11 @@ inline size_t sample_split(SampleArgs& a, char* ws) {
   a.w_bins = (unsigned long long*)part(n * kSampleBins * 8);
   a.n_bins = (uint32_t*)part(n * kSampleBins * 4);
   a.least = (float*)part(n * 4);
+  a.groups = (a.V + 63) / 64;
+  a.most = (float*)part((size_t)a.B * (size_t)a.groups * 4);
+  a.lists = (unsigned long long*)part((size_t)a.B * kSampleList * 8);
+  a.plan = (SamplePlan*)part((size_t)a.B * sizeof(SamplePlan));
+  a.sums = (unsigned long long*)part((size_t)a.B * kSampleBins * 16);
   return off;
 }
 hipError_t launch_sample(const SampleArgs& a, bool bf16, bool vec, hipStream_t s);
