@@ -39,7 +39,7 @@ constexpr double kOne = 1099511627776.0; // 2^40, the weight of the largest logi
 struct Row {                             // what is known of a row once its largest logit is
   double top;
   double c;                              // log2(e) / temperature
-  double per_bin;                        // bins per unit of (x - top) * c
+  float per_fine;                        // fine bins per unit of top - x
   bool inf;                              // the largest is infinite: its equals weigh 2^40, the others nothing
 };
 
@@ -144,32 +144,40 @@ __device__ __forceinline__ double scaled(const Row& r, float x) {
   if (r.inf) return x == (float)r.top ? 0.0 : -__builtin_inf();
   return x == kNegInf ? -__builtin_inf() : ((double)x - r.top) * r.c;
 }
-__device__ __forceinline__ int bin_of(const Row& r, double t) { return min((int)(-t * r.per_bin), kBins - 1); }
-
-// 2^40 * 2^t rounded to a whole number, t <= 0.  2^f for |f| <= 1/2 by its Taylor sum: the first term left out
-// is below 2^-57.  Adding 2^52 rounds to a whole number, half to even.
-__device__ __forceinline__ u64 weight(double t) {
-  if (!(t > -41.0)) return 0;
-  const double n = rint(t), f = t - n;
-  double p = 2.5678435993488196e-11;                       // (ln 2)^12 / 12!
-  p = __builtin_fma(p, f, 4.4455382718708102e-10);
-  p = __builtin_fma(p, f, 7.0549116208011211e-09);
-  p = __builtin_fma(p, f, 1.0178086009239696e-07);
-  p = __builtin_fma(p, f, 1.3215486790144305e-06);
-  p = __builtin_fma(p, f, 1.5252733804059838e-05);
-  p = __builtin_fma(p, f, 1.5403530393381606e-04);
-  p = __builtin_fma(p, f, 1.3333558146428441e-03);
-  p = __builtin_fma(p, f, 9.6181291076284771e-03);
-  p = __builtin_fma(p, f, 5.5504108664821576e-02);
-  p = __builtin_fma(p, f, 2.4022650695910070e-01);
-  p = __builtin_fma(p, f, 6.9314718055994531e-01);
-  p = __builtin_fma(p, f, 1.0);
-  const double w = ldexp(p, 40 + (int)n) + 4503599627370496.0;
-  return (u64)__double_as_longlong(w) & 0xFFFFFFFFFFFFFull;
+// The logit's place among kBins^2 fine bins of the row's range, kBins of them to a bin: any steps that rise as x falls
+// will do, so fp32 is enough.  NaN (equals of an infinite top) counts as 0.
+__device__ __forceinline__ int fine_of(const Row& r, float x) {
+  return (int)__builtin_amdgcn_fmed3f(((float)r.top - x) * r.per_fine, 0.f, (float)(kBins * kBins - 1));
 }
 
+// 2^40 * 2^t rounded to a whole number, t <= 0 (NaN: 0).  2^f for |f| <= 1/2 is a polynomial through the eleven
+// Chebyshev points, 2.4e-16 off at most, its coefficients times 2^40.  Adding 1.5 * 2^52 rounds to a whole number, half
+// to even, in a double's low bits; 2^n goes straight into the exponent.
+__device__ __forceinline__ u64 weight(double t) {
+  const double magic = 6755399441055744.0;
+  t = __builtin_fmax(t, -60.0);
+  const double m = t + magic, f = t - (m - magic);
+  double p = 0x1.e6063f7217bc6p+12;
+  p = __builtin_fma(p, f, 0x1.b675bca4eeebbp+16);
+  p = __builtin_fma(p, f, 0x1.62bfd47773353p+20);
+  p = __builtin_fma(p, f, 0x1.ffcb54062e698p+23);
+  p = __builtin_fma(p, f, 0x1.430913096fd9fp+27);
+  p = __builtin_fma(p, f, 0x1.5d87fe9d7a584p+30);
+  p = __builtin_fma(p, f, 0x1.3b2ab6fba1ddap+33);
+  p = __builtin_fma(p, f, 0x1.c6b08d703ce49p+35);
+  p = __builtin_fma(p, f, 0x1.ebfbdff82c598p+37);
+  p = __builtin_fma(p, f, 0x1.62e42fefa3a19p+39);
+  p = __builtin_fma(p, f, 0x1.0p+40);
+  uint2 bits = __builtin_bit_cast(uint2, p);
+  bits.y += __builtin_bit_cast(uint2, m).x << 20;
+  bits = __builtin_bit_cast(uint2, __builtin_bit_cast(double, bits) + magic);
+  return (u64)(bits.y & 0x7FFFFu) << 32 | bits.x;
+}
+__device__ __forceinline__ u64 weight_of(const Row& r, float x) { return weight(scaled(r, x)); }
+
 struct Settings {
-  double temp, p, min_p;
+  double temp, p;
+  u64 min_w;                             // what min-p keeps, in weights; 0: off
   int64_t k;                             // 0: off
   bool greedy;
 };
@@ -181,7 +189,7 @@ __device__ __forceinline__ Settings settings_of(const SampleArgs& a, int64_t b) 
   s.greedy = !(t > 0.f);
   s.temp = t;
   s.p = p < 1.f ? max((double)p, 0.0) : 1.0;               // NaN: off
-  s.min_p = m > 0.f ? (double)m : 0.0;
+  s.min_w = m > 0.f ? (u64)ceil(fmin((double)m, 2.0) * kOne) : 0;
   s.k = k > 0 && k < a.V ? k : 0;
   return s;
 }
@@ -205,9 +213,9 @@ __device__ __forceinline__ Row row_of_extremes(const Extremes& e, const Settings
   r.top = x;
   r.inf = x == __builtin_inff();
   r.c = 1.4426950408889634 / s.temp;
-  const double range = r.inf ? 0.0 : fmin(((double)x - least) * r.c, 41.0);
-  r.per_bin = range > 0.0 ? kBins / range : 0.0;
-  if (!(r.per_bin < 1e30)) r.per_bin = 0.0;                // too narrow to be told apart: one bin
+  // over what weighs anything, or what there is; too narrow to be told apart: one bin
+  const float per_fine = (float)(kBins * kBins / fmin((double)x - least, 41.0 / r.c));
+  r.per_fine = per_fine < 1e30f && !r.inf ? per_fine : 0.f;
   return r;
 }
 
@@ -255,40 +263,24 @@ struct Range {                           // of places, both ends included
   u64 lo, hi;
 };
 
-// Whether a falling() value's logit weighs something and lies in a bin up to `bin`.
-__device__ __forceinline__ bool reaches(const Row& r, uint64_t key, int bin) {
-  const float x = from_falling((uint32_t)key);
-  const double t = scaled(r, x);
-  return x == x && weight(t) > 0 && bin_of(r, t) <= bin;
-}
-// Largest falling() value that reaches up to a bin; the row's largest logit always does.  The lanes of a wave try 64
-// values at a time.
+// Largest falling() value whose logit weighs something and lies in a bin up to `bin`; the row's largest logit
+// always does.  The lanes of a wave try 64 values at a time.
 __device__ __forceinline__ u64 key_end(const Row& r, int bin) {
   const int lane = threadIdx.x & 63;
   uint64_t lo = falling((float)r.top), hi = (uint64_t)1 << 32;   // lo does, hi does not
   while (hi - lo > 1) {
     const uint64_t step = (hi - lo + 63) >> 6, at = lo + lane * step;
-    const uint64_t mask = __ballot(at < hi && reaches(r, at, bin));
+    const float x = from_falling((uint32_t)at);
+    const uint64_t mask = __ballot(at < hi && x == x && weight_of(r, x) > 0 && fine_of(r, x) / kBins <= bin);
     const int last = 63 - __clzll((long long)mask);
     hi = min(hi, lo + (last + 1) * step);
     lo += last * step;
   }
   return lo;
 }
-// Places of the tokens of bins bin0 to bin1.  Half of the lanes try the 32 values around where each end should be.
-__device__ __forceinline__ Range places_of(const Row& r, int bin0, int bin1) {
-  const int lane = threadIdx.x & 63;
-  const bool upper = lane >= 32;
-  const int bin = upper ? bin1 : max(bin0 - 1, 0);
-  const uint64_t top = falling((float)r.top);
-  const double t = r.per_bin > 0.0 && bin < kBins - 1 ? fmin((bin + 1) / r.per_bin, 41.0) : 41.0;
-  const uint64_t guess = r.inf ? top : falling((float)(r.top - t / r.c));
-  const uint64_t at = min(max(guess, top + 16) - 16, ((uint64_t)1 << 32) - 32) + (lane & 31);
-  const uint64_t mask = __ballot(reaches(r, at, bin));
-  const uint32_t m0 = (uint32_t)mask, m1 = (uint32_t)(mask >> 32);
-  const u64 end0 = (m0 & 1) && !(m0 >> 31) ? lane_value((u64)at, 31 - __clz((int)m0)) : key_end(r, max(bin0 - 1, 0));
-  const u64 end1 = (m1 & 1) && !(m1 >> 31) ? lane_value((u64)at, 63 - __clz((int)m1)) : key_end(r, bin1);
-  return {(bin0 ? end0 + 1 : top) << 32, end1 << 32 | 0xFFFFFFFFu};
+__device__ __forceinline__ Range places_of(const Row& r, int bin) {
+  const u64 first = bin ? key_end(r, bin - 1) + 1 : falling((float)r.top);
+  return {first << 32, key_end(r, bin) << 32 | 0xFFFFFFFFu};
 }
 
 template <bool BF, bool VEC>
@@ -372,7 +364,7 @@ __device__ __forceinline__ bool last_to_arrive(uint32_t* arrived, uint32_t block
 // Which tokens of a row the questions need: bins, at most kList tokens in all, or none if they are more.  With k or
 // top-p the sums that the later questions start from are known to within a bin only, so theirs may lie in one of
 // a few bins.
-__device__ __forceinline__ void make_plan(SamplePlan* plan, const Row& r, const Settings& st, u64 sum_m, double u,
+__device__ __forceinline__ void make_plan(SamplePlan* plan, const Settings& st, u64 sum_m, double u,
                                           const Pair* bins) {
   const Pair none = {0, 0};
   const Pair all = bins[kBins - 1];
@@ -395,7 +387,7 @@ __device__ __forceinline__ void make_plan(SamplePlan* plan, const Row& r, const 
     b0[n] = bin0;
     b1[n++] = bin1;
   }
-  if (st.min_p > 0.0) {
+  if (st.min_w) {
     lo = min(lo, max(sum_m, (u64)kOne));
     hi = min(hi, max(sum_m, (u64)kOne));
   }
@@ -422,16 +414,12 @@ __device__ __forceinline__ void make_plan(SamplePlan* plan, const Row& r, const 
   u64 tokens = 0;
   for (int i = 0; i <= m; ++i) tokens += upto(b1[i]).n - upto(b0[i] - 1).n;
   n = tokens <= kList ? m + 1 : 0;
-  for (int i = 0; i < n; ++i) {
-    const Range g = places_of(r, b0[i], b1[i]);
-    if (threadIdx.x == 0) {
-      plan->lo[i] = g.lo;
-      plan->hi[i] = g.hi;
-      plan->bin0[i] = b0[i];
-      plan->bin1[i] = b1[i];
-    }
-  }
   if (threadIdx.x == 0) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      plan->bin0[i] = i < n ? b0[i] : 1;                     // none
+      plan->bin1[i] = i < n ? b1[i] : 0;
+    }
     plan->ranges = n;
     plan->upto = (uint32_t)min(upto(last).n, (u64)0xFFFFFFFFu);
     plan->count = 0;
@@ -472,8 +460,7 @@ __global__ __launch_bounds__(kThreads) void sample_hist_kernel(SampleArgs a) {
   __syncthreads();
   const void* row = row_of<BF>(a, b);
   const int64_t i0 = (int64_t)blockIdx.x * a.chunk, i1 = min(i0 + a.chunk, a.V);
-  const double min_w = st.min_p * kOne;
-  const float top = (float)r.top;
+  const float top = (float)r.top, per_bin = r.per_fine / kBins;
   double e = 0.0;                                          // sum of exp(x - top)
   u64 least_sum = 0;                                       // of the weights that min_p keeps
   for (int64_t at = i0; at < i1; at += 2 * kStep) {
@@ -484,19 +471,32 @@ __global__ __launch_bounds__(kThreads) void sample_hist_kernel(SampleArgs a) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       if (at + k * kStep >= i1) break;
-      finish8_masked<BF, VEC>(row, i + k * kStep, a.V, v[k]);
+      finish8<BF, VEC>(row, i + k * kStep, a.V, v[k]);
+      float d[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) d[j] = top - v[k][j];
+      if (a.logprob) {
+        // eight at a time in fp32, unless one of them is 1, next to which small ones were lost, or NaN
+        float some = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) some += __builtin_amdgcn_exp2f(d[j] * -1.44269504f);
+        if (some < 1.f) {
+          e += some;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            e += v[k][j] == top ? 1.0 : d[j] > 0.f && !r.inf ? (double)__builtin_amdgcn_exp2f(d[j] * -1.44269504f) : 0.0;
+        }
+      }
+      if (st.greedy) continue;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float x = v[k][j];
-        if (a.logprob) e += r.inf ? (x == top ? 1.0 : 0.0) : (double)__builtin_amdgcn_exp2f((x - top) * 1.44269504f);
-        if (st.greedy) continue;
-        const double t = scaled(r, x);
-        const u64 w = weight(t);
+        const u64 w = r.inf ? weight_of(r, v[k][j]) : weight(((double)v[k][j] - r.top) * r.c);
         if (w) {
-          const int bin = bin_of(r, t);
+          const int bin = (int)__builtin_amdgcn_fmed3f(d[j] * per_bin, 0.f, (float)(kBins - 1));   // as in fine_of
           atomicAdd(&w_bin[bin], w);
           atomicAdd(&n_bin[bin], 1u);
-          if ((double)w >= min_w) least_sum += w;
+          if (st.min_w && w >= st.min_w) least_sum += w;
         }
       }
     }
@@ -542,7 +542,7 @@ __global__ __launch_bounds__(kThreads) void sample_hist_kernel(SampleArgs a) {
   bins[tid] = sum;
   ((ulonglong2*)a.sums)[b * kBins + tid] = make_ulonglong2(sum.w, sum.n);
   __syncthreads();
-  if (tid < 64) make_plan(a.plan + b, r, st, sum_m, u, bins);
+  if (tid < 64) make_plan(a.plan + b, st, sum_m, u, bins);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -566,24 +566,11 @@ struct Shared {                          // a block's memory
 };
 
 struct Head {                            // of a plan
-  Range range[3];
   int bin0[3], bin1[3];
   uint32_t ranges, upto;
 };
 
-struct Bounds {                          // the logits of a range: a little wider where it ends among equals
-  float lo, hi;
-};
-__device__ __forceinline__ Bounds bounds_of(const Range& g) {
-  const uint32_t key0 = (uint32_t)(g.lo >> 32), key1 = (uint32_t)(g.hi >> 32);
-  // the value of -0, which no logit has, is above +0's: a range must not reach back to it
-  return {from_falling(key1), from_falling(key0 == 0x80000000u ? key0 + 1 : key0)};
-}
-__device__ __forceinline__ bool inside(const Bounds& b, float x) {     // a NaN equals nothing
-  return __builtin_amdgcn_fmed3f(x, b.lo, b.hi) == x;
-}
-
-// Appends to the list the logits of eight per lane, from index i on, that ok(x, place) says yes to.
+// Appends to the list the logits of eight per lane, from index i on, that ok(x) says yes to.
 template <class F>
 __device__ __forceinline__ void append(Shared& s, const float v[8], int64_t i, F&& ok) {
   const int lane = threadIdx.x & 63;
@@ -591,7 +578,7 @@ __device__ __forceinline__ void append(Shared& s, const float v[8], int64_t i, F
   uint32_t all = 0;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    mask[j] = __ballot(ok(v[j], place(v[j], i + j)));
+    mask[j] = __ballot(ok(v[j]));
     all += __popcll(mask[j]);
   }
   if (!all) return;
@@ -607,18 +594,46 @@ __device__ __forceinline__ void append(Shared& s, const float v[8], int64_t i, F
   }
 }
 
-// The list: the tokens of the plan's one range, few enough for one block to read the groups of 64 logits again whose
-// largest reaches it, eight lanes to each.
+// The plan's bins as bounds on (top - x) * per_fine, which is no number where there is one bin alone and x or top
+// infinite, and the least logit that weighs anything.
+struct Named {
+  float lo[3], hi[3], least;
+};
+__device__ __forceinline__ Named named_by(const Row& r, const Head& plan) {
+  Named n;
+  bool light = r.per_fine == 0.f;        // what weighs nothing is in the last bin, or in the only one
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const bool last = plan.bin1[i] == kBins - 1;
+    light |= last;
+    n.lo[i] = (float)(plan.bin0[i] * kBins);
+    // the largest number below the next bin; of no range: below its first
+    n.hi[i] = last ? __builtin_inff() : __uint_as_float(__float_as_uint((float)((plan.bin1[i] + 1) * kBins)) - 1);
+  }
+  n.least = light ? from_falling((uint32_t)key_end(r, kBins - 1)) : kNegInf;
+  return n;
+}
+__device__ __forceinline__ bool is_named(const Row& r, const Named& n, float x) {   // a NaN is not
+  const float y = ((float)r.top - x) * r.per_fine;
+  bool out = true;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) out &= y < n.lo[i] || y > n.hi[i];
+  return !out && x >= n.least;
+}
+
+// Whether one block reads a row's tokens: few enough to look for them only in groups of 64 logits whose largest
+// is in their bins.
 __device__ __forceinline__ bool few_groups(const SampleArgs& a, const Head& plan) {
   return plan.ranges == 1 && (int64_t)plan.upto * 128 <= a.V;
 }
+// The list: the plan's tokens from such groups, eight lanes to each.
 template <bool BF, bool VEC>
-__device__ __forceinline__ void gather_groups(const SampleArgs& a, int64_t b, const Head& plan, Shared& s) {
+__device__ __forceinline__ void gather_groups(const SampleArgs& a, int64_t b, const Row& r, const Head& plan, Shared& s) {
   const int tid = threadIdx.x;
   const void* row = row_of<BF>(a, b);
-  const Bounds bd = bounds_of(plan.range[0]);
-  uint32_t* groups = (uint32_t*)s.split;                     // room for kAll
-  constexpr int kAll = 4 * kThreads;
+  const Named named = named_by(r, plan);
+  uint32_t* groups = (uint32_t*)s.split;
+  constexpr int kAll = 4 * kThreads, kAhead = 2, kTeams = kThreads / 8;
   static_assert(sizeof(s.split) >= kAll * 4, "a round's groups fit");
   const float* most = a.most + b * a.groups;
   for (int64_t g0 = 0; g0 < a.groups; g0 += kAll) {
@@ -630,30 +645,37 @@ __device__ __forceinline__ void gather_groups(const SampleArgs& a, int64_t b, co
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int64_t i = g0 + k * kThreads + tid;
-      if (i < a.groups && m[k] >= bd.lo) groups[atomicAdd(&s.at, 1u)] = (uint32_t)i;
+      if (i < a.groups && !(((float)r.top - m[k]) * r.per_fine > named.hi[0])) groups[atomicAdd(&s.at, 1u)] = (uint32_t)i;
     }
     __syncthreads();
     const int n = s.at;
-    for (int k0 = 0; k0 < n; k0 += kThreads / 8) {
-      const int k = k0 + (tid >> 3);
-      const int64_t i = k < n ? (int64_t)groups[k] * 64 + (tid & 7) * 8 : a.V;
-      float v[8];
-      load8_raw<BF, VEC>(row, i, a.V, v);
-      finish8<BF, VEC>(row, i, a.V, v);
-      append(s, v, i, [&](float x, u64) { return inside(bd, x); });
+    for (int k0 = 0; k0 < n; k0 += kAhead * kTeams) {
+      float v[kAhead][8];
+      int64_t i[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int at = k0 + k * kTeams + (tid >> 3);
+        i[k] = at < n ? (int64_t)groups[at] * 64 + (tid & 7) * 8 : a.V;
+        load8_raw<BF, VEC>(row, i[k], a.V, v[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (k0 + k * kTeams >= n) break;
+        finish8<BF, VEC>(row, i[k], a.V, v[k]);
+        append(s, v[k], i[k], [&](float x) { return is_named(r, named, x); });
+      }
     }
     __syncthreads();
   }
 }
 
-// The list: this block's chunk of the tokens that the plan names.
+// The list: the plan's tokens of one chunk.
 template <bool BF, bool VEC>
-__device__ __forceinline__ void gather_chunk(const SampleArgs& a, int64_t b, const Head& plan, Shared& s) {
+__device__ __forceinline__ void gather_chunk(const SampleArgs& a, int64_t b, int64_t part, const Row& r, const Head& plan,
+                                             Shared& s) {
   const void* row = row_of<BF>(a, b);
-  const int64_t i0 = (int64_t)blockIdx.x * a.chunk, i1 = min(i0 + a.chunk, a.V);
-  const bool more = plan.ranges > 1, third = plan.ranges > 2;
-  const Bounds b0 = bounds_of(plan.range[0]), b1 = more ? bounds_of(plan.range[1]) : b0,
-               b2 = third ? bounds_of(plan.range[2]) : b0;
+  const Named named = named_by(r, plan);
+  const int64_t i0 = part * a.chunk, i1 = min(i0 + a.chunk, a.V);
   for (int64_t at = i0; at < i1; at += 2 * kStep) {
     const int64_t i = at + threadIdx.x * 8;
     float v[2][8];
@@ -663,35 +685,31 @@ __device__ __forceinline__ void gather_chunk(const SampleArgs& a, int64_t b, con
     for (int k = 0; k < 2; ++k) {
       if (at + k * kStep >= i1) break;
       finish8<BF, VEC>(row, i + k * kStep, i1, v[k]);        // a chunk is a multiple of eight, but for the row's end
-      append(s, v[k], i + k * kStep, [&](float x, u64) {
-        return inside(b0, x) || (more && inside(b1, x)) || (third && inside(b2, x));   // ranges do not meet
-      });
+      append(s, v[k], i + k * kStep, [&](float x) { return is_named(r, named, x); });
     }
   }
   __syncthreads();
 }
 
-// Calls f(v, i) for eight logits of a lane from index i on where any lane of the wave has one within the range's
-// bounds: the whole row, by one block.
-template <bool BF, bool VEC, class F>
+// Calls f(in, place) for the lanes' logits where any lane's is in the range: the whole row, by one block.  A NaN's
+// place is outside of what weighs anything.
+template <bool BF, class F>
 __device__ __forceinline__ void each(const SampleArgs& a, int64_t b, const Range& g, F&& f) {
-  constexpr int kRing = 4;
+  constexpr int kAhead = 4;
   const void* row = row_of<BF>(a, b);
-  const Bounds bd = bounds_of(g);
-  float v[kRing][8];
-  const int64_t first = threadIdx.x * 8;
+  for (int64_t at = 0; at < a.V; at += kAhead * kThreads) {
+    float v[kAhead];
 #pragma unroll
-  for (int u = 0; u < kRing; ++u) load8_raw<BF, VEC>(row, first + u * kStep, a.V, v[u]);
-  for (int64_t at = 0; at < a.V; at += kRing * kStep) {
+    for (int k = 0; k < kAhead; ++k) {
+      const int64_t i = min(at + k * kThreads + threadIdx.x, a.V - 1);
+      v[k] = BF ? __uint_as_float((uint32_t)((const uint16_t*)row)[i] << 16) : ((const float*)row)[i];
+    }
 #pragma unroll
-    for (int u = 0; u < kRing; ++u) {
-      const int64_t i = at + u * kStep + first;
-      finish8<BF, VEC>(row, i, a.V, v[u]);
-      bool any = false;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) any |= inside(bd, v[u][j]);
-      if (__any(any)) f(v[u], i);
-      load8_raw<BF, VEC>(row, i + kRing * kStep, a.V, v[u]);
+    for (int k = 0; k < kAhead; ++k) {
+      const int64_t i = at + k * kThreads + threadIdx.x;
+      const u64 p = place(v[k], i);
+      const bool in = i < a.V && p >= g.lo && p <= g.hi;
+      if (__any(in)) f(in, p);
     }
   }
 }
@@ -705,9 +723,16 @@ struct Few {
 __device__ __forceinline__ Few sort_few(const Row& r, const u64* places, int n) {
   const int lane = threadIdx.x & 63;
   const u64 p = lane < n ? places[lane] : ~0ull;
-  const u64 w = lane < n ? weight(scaled(r, logit_at(p))) : 0;
-  int rank = lane < n ? 0 : lane;
-  for (int j = 0; j < n; ++j) rank += lane_value(p, j) < p && lane < n;
+  const u64 w = lane < n ? weight_of(r, logit_at(p)) : 0;
+  int rank = 0;
+  for (int j0 = 0; j0 < n; j0 += 8) {                        // reads at places past n find anything, and do not count
+    u64 other[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) other[j] = places[j0 + j];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) rank += j0 + j < n && other[j] < p;
+  }
+  if (lane >= n) rank = lane;
   const uint32_t token = __builtin_amdgcn_ds_permute(rank * 4, (int)(uint32_t)p);
   const uint32_t w0 = __builtin_amdgcn_ds_permute(rank * 4, (int)(uint32_t)w);
   const uint32_t w1 = __builtin_amdgcn_ds_permute(rank * 4, (int)(uint32_t)(w >> 32));
@@ -739,7 +764,7 @@ __device__ __forceinline__ Found among_some(const Row& r, const Asked& q, int n,
 __device__ __forceinline__ void split_add(const Row& r, Shared& s, bool in, u64 p, uint32_t part) {
   const uint64_t mask = __ballot(in);
   if (!mask) return;
-  const u64 w = weight(scaled(r, logit_at(p)));
+  const u64 w = weight_of(r, logit_at(p));
   const int first = __ffsll((unsigned long long)mask) - 1;
   const uint32_t part1 = lane_value(part, first), key1 = lane_value((uint32_t)(p >> 32), first);
   if (__ballot(in && part == part1 && (uint32_t)(p >> 32) == key1) == mask) {
@@ -765,87 +790,89 @@ __device__ __forceinline__ int split_choose(const Asked& q, Shared& s, Pair* bef
   return k;
 }
 
-// The answer wherever it lies.  The list holds the tokens of the plan's ranges.
-template <bool BF, bool VEC>
-__device__ __forceinline__ Found answer(const SampleArgs& a, int64_t b, const Row& r, const Asked& q,
-                                        Head& plan, Shared& s) {
+// The plan's tokens, a few to a thread: their places, fine bins (-1: none) and weights.
+constexpr int kEach = kList / kThreads;
+struct Mine {
+  u64 p[kEach], w[kEach];
+  int fine[kEach];
+};
+
+// The answer from the plan's tokens: those of the bin, by its fine bins if they are many.  False if too many share a
+// fine bin.
+__device__ __forceinline__ bool answer_mine(const Row& r, const Asked& q, const Mine& t, int bin, Pair before, u64 n,
+                                            Shared& s, Found* found) {
   const int tid = threadIdx.x;
-  const Pair none = {0, 0};
-  const int bin = first_bin(q, s.bins, none);
-  bool listed = false;
+  __syncthreads();
+  s.split[tid] = {0, 0};
+  if (tid == 0) s.few_n = 0;
+  __syncthreads();
+  int part = -1;                         // of the bin; -1: all of it
+  if (n > kSmall) {
 #pragma unroll
-  for (int i = 0; i < 3; ++i) listed |= i < (int)plan.ranges && plan.bin0[i] <= bin && bin <= plan.bin1[i];
-  Pair before = bin ? s.bins[bin - 1] : none;
-  u64 n = s.bins[bin].n - before.n;
-  if (listed) {
-    // the list's tokens of the bin, by bins within the bin if they are many
-    auto bin_at = [&](u64 p) { return bin_of(r, scaled(r, logit_at(p))); };
-    if (n <= kSmall) return among_some(r, q, (int)n, before, s, [&](u64 p) { return bin_at(p) == bin; });
-    auto part_at = [&](u64 p) {
-      const double y = -scaled(r, logit_at(p)) * r.per_bin;
-      return min(max((int)((y - bin) * kBins), 0), kBins - 1);   // the last bin's may lie past it
-    };
-    const Pair outside = before;
-    u64 few = n;
-    __syncthreads();
-    s.split[tid] = none;
-    __syncthreads();
-    for (int i0 = 0; i0 < (int)s.count; i0 += kThreads) {
-      const u64 p = s.list[min(i0 + tid, (int)s.count - 1)];
-      const bool in = i0 + tid < (int)s.count && bin_at(p) == bin;
-      split_add(r, s, in, p, in ? part_at(p) : 0);
+    for (int i = 0; i < kEach; ++i) {
+      if (t.fine[i] >= 0 && t.fine[i] / kBins == bin) {
+        atomicAdd(&s.split[t.fine[i] % kBins].w, t.w[i]);
+        atomicAdd(&s.split[t.fine[i] % kBins].n, 1ull);
+      }
     }
-    const int part = split_choose(q, s, &before, &few);
-    if (few <= kSmall)
-      return among_some(r, q, (int)few, before, s, [&](u64 p) { return bin_at(p) == bin && part_at(p) == part; });
-    before = outside;
+    part = split_choose(q, s, &before, &n);
+    if (n > kSmall) return false;
   }
-  // by places, nine bits at a time, down to a single token if need be
-  if (!listed) plan.ranges = 0;          // the list is written over
-  Range g = places_of(r, bin, bin);
+#pragma unroll
+  for (int i = 0; i < kEach; ++i)
+    if (t.fine[i] >= 0 && (part < 0 ? t.fine[i] / kBins == bin : t.fine[i] == bin * kBins + part))
+      s.few[atomicAdd(&s.few_n, 1u)] = t.p[i];
+  __syncthreads();
+  *found = among_few(q, sort_few(r, s.few, (int)n), before);
+  return true;
+}
+
+// The answer from the row itself, read by this block: its bin by places, nine bits at a time, down to a single token
+// if need be; from LDS once its tokens fit.
+template <bool BF>
+__device__ __forceinline__ Found answer_row(const SampleArgs& a, int64_t b, const Row& r, const Asked& q, int bin,
+                                            Pair before, u64 n, Shared& s) {
+  const int tid = threadIdx.x;
+  Range g = places_of(r, bin);
+  auto in = [&](u64 p) { return p >= g.lo && p <= g.hi; };
+  auto gather = [&] {
+    __syncthreads();
+    if (tid == 0) s.count = 0;
+    __syncthreads();
+    each<BF>(a, b, g, [&](bool is, u64 p) {
+      if (is) {
+        const uint32_t at = atomicAdd(&s.count, 1u);
+        if (at < kList) s.list[at] = p;
+      }
+    });
+    __syncthreads();
+  };
+  bool listed = false;
   while (n > kSmall) {
     if (!listed && n <= kList) {
-      __syncthreads();
-      if (tid == 0) s.count = 0;
-      __syncthreads();
-      each<BF, VEC>(a, b, g, [&](const float* v, int64_t i) {
-        append(s, v, i, [&](float, u64 p) { return p >= g.lo && p <= g.hi; });
-      });
+      gather();
       listed = true;
     }
     const int bits = 64 - __clzll((long long)(g.hi - g.lo)), shift = max(bits - 9, 0);
     static_assert(kBins == 512, "nine bits");
     __syncthreads();
-    s.split[tid] = none;
+    s.split[tid] = {0, 0};
     __syncthreads();
     auto part_at = [&](u64 p) { return (uint32_t)((p - g.lo) >> shift); };
     if (listed) {
       for (int i0 = 0; i0 < (int)s.count; i0 += kThreads) {
         const u64 p = s.list[min(i0 + tid, (int)s.count - 1)];
-        const bool in = i0 + tid < (int)s.count && p >= g.lo && p <= g.hi;
-        split_add(r, s, in, p, in ? part_at(p) : 0);
+        const bool is = i0 + tid < (int)s.count && in(p);
+        split_add(r, s, is, p, is ? part_at(p) : 0);
       }
     } else {
-      each<BF, VEC>(a, b, g, [&](const float* v, int64_t i) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const u64 p = place(v[j], i + j);
-          const bool in = p >= g.lo && p <= g.hi;
-          split_add(r, s, in, p, in ? part_at(p) : 0);
-        }
-      });
+      each<BF>(a, b, g, [&](bool is, u64 p) { split_add(r, s, is, p, is ? part_at(p) : 0); });
     }
     const int k = split_choose(q, s, &before, &n);
     g.lo += (u64)k << shift;
     g.hi = min(g.hi, g.lo + (((u64)1 << shift) - 1));
   }
-  auto in = [&](u64 p) { return p >= g.lo && p <= g.hi; };
-  if (!listed) {
-    __syncthreads();
-    if (tid == 0) s.count = 0;
-    __syncthreads();
-    each<BF, VEC>(a, b, g, [&](const float* v, int64_t i) { append(s, v, i, [&](float, u64 p) { return in(p); }); });
-  }
+  if (!listed) gather();
   return among_some(r, q, (int)n, before, s, in);
 }
 
@@ -854,6 +881,8 @@ __global__ __launch_bounds__(kThreads) void sample_draw_kernel(SampleArgs a) {
   __shared__ Shared s;
   const int tid = threadIdx.x;
   const int64_t b = blockIdx.y;
+  // workgroups are dealt to the XCDs in turn, so a row's first chunk is on another one than the last row's
+  const int64_t part = (blockIdx.x + blockIdx.y) % a.chunks;
   const int chunk = min<int64_t>(tid & 63, a.chunks - 1);
   const Settings st = settings_of(a, b);
   const Extremes ex = row_extremes(a, b);
@@ -863,7 +892,6 @@ __global__ __launch_bounds__(kThreads) void sample_draw_kernel(SampleArgs a) {
   plan.upto = plan_at->upto;
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
-    plan.range[i] = {plan_at->lo[i], plan_at->hi[i]};
     plan.bin0[i] = plan_at->bin0[i];
     plan.bin1[i] = plan_at->bin1[i];
   }
@@ -876,44 +904,88 @@ __global__ __launch_bounds__(kThreads) void sample_draw_kernel(SampleArgs a) {
   int64_t token = masked ? -1 : (int64_t)(uint32_t)best;
   const bool draws = !st.greedy && !masked;
   const bool alone = !draws || plan.ranges == 0 || few_groups(a, plan);   // one block does it all
-  if (alone && blockIdx.x > 0) return;
+  if (alone && part > 0) return;
   if (draws) {
     if (tid == 0) s.count = 0;
     s.bins[tid] = {mine.x, mine.y};
     __syncthreads();
-    if (plan.ranges && alone) gather_groups<BF, VEC>(a, b, plan, s);
-    if (!alone) {
-      gather_chunk<BF, VEC>(a, b, plan, s);
-      if (a.chunks > 1) {                // the row's list, by whichever block is last
+    const u64* elsewhere = nullptr;
+    uint32_t tokens = 0;
+    if (plan.ranges) {
+      if (alone) gather_groups<BF, VEC>(a, b, r, plan, s);
+      else gather_chunk<BF, VEC>(a, b, part, r, plan, s);
+      tokens = s.count;
+      if (!alone && a.chunks > 1) {      // the row's list, by whichever block is last
         u64* const lists = a.lists + b * kList;
-        const uint32_t n = s.count;
-        if (tid == 0 && n)
-          s.at = __hip_atomic_fetch_add(&plan_at->count, n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (tid == 0 && tokens)
+          s.at = __hip_atomic_fetch_add(&plan_at->count, tokens, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         __syncthreads();
-        for (uint32_t i = tid; i < n; i += kThreads)
+        for (uint32_t i = tid; i < tokens; i += kThreads)
           if (s.at + i < kList) put(lists + s.at + i, s.list[i]);
         if (!last_to_arrive(&plan_at->arrived, (uint32_t)a.chunks, &s.last)) return;
-        const uint32_t all = min(get(&plan_at->count), (uint32_t)kList);
-        for (uint32_t i = tid; i < all; i += kThreads) s.list[i] = get(lists + i);
-        if (tid == 0) s.count = all;
-        __syncthreads();
+        tokens = get(&plan_at->count);
+        elsewhere = lists;
       }
+      tokens = min(tokens, (uint32_t)kList);
+    }
+    Mine t;
+    if (elsewhere) {
+#pragma unroll
+      for (int i = 0; i < kEach; ++i)
+        if (i * kThreads < tokens) t.p[i] = get(elsewhere + min(i * kThreads + tid, (int)tokens - 1));
+    } else {
+#pragma unroll
+      for (int i = 0; i < kEach; ++i)
+        if (i * kThreads < tokens) t.p[i] = s.list[min(i * kThreads + tid, (int)tokens - 1)];
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      t.fine[i] = -1;
+      if (i * kThreads >= tokens) continue;
+      const float x = logit_at(t.p[i]);
+      t.w[i] = weight_of(r, x);
+      t.fine[i] = i * kThreads + tid < tokens ? fine_of(r, x) : -1;
+    }
+    const bool small = plan.ranges == 1 && tokens <= kSmall;     // one order answers all questions
+    Few few = {0, 0, 0};
+    if (small) {
+      if (tid < (int)tokens) s.few[tid] = t.p[0];
+      __syncthreads();
+      few = sort_few(r, s.few, (int)tokens);
     }
     sum_m = wave_all((tid & 63) < a.chunks ? sum_m : 0, (u64)0, Add());
     const Pair all = s.bins[kBins - 1];
     const u64 k = st.k && (u64)st.k < all.n ? (u64)st.k : 0;
-    const bool small = plan.ranges == 1 && s.count <= kSmall;    // one order answers all questions
-    Few few = {0, 0, 0};
-    if (small) few = sort_few(r, s.list, s.count);
-    const Pair above = small && plan.bin0[0] ? s.bins[plan.bin0[0] - 1] : Pair{0, 0};
-    auto ask = [&](const Asked& q) { return small ? among_few(q, few, above) : answer<BF, VEC>(a, b, r, q, plan, s); };
-    u64 sum = all.w;
-    if (k) sum = ask({kCount, k, 0.0, 0}).sum;
-    if (st.p < 1.0) sum = min(sum, ask({kGoal, 0, st.p * (double)sum, 0}).sum);
-    if (st.min_p > 0.0) sum = min(sum, max(sum_m, (u64)kOne));
     const double u = a.u[b];
-    const double at = u > 0.0 ? fmin(u, 1.0) * (double)sum : 0.0;     // NaN: 0
-    token = ask({kPass, 0, 0.0, min((u64)at, sum - 1)}).token;
+    u64 sum = all.w;
+    // the questions in turn by the same code, which is fetched once
+#pragma unroll 1
+    for (int question = k ? kCount : st.p < 1.0 ? kGoal : kPass; question <= kPass; ++question) {
+      Asked q = {(Question)question, k, st.p * (double)sum, 0};
+      if (question == kGoal && !(st.p < 1.0)) continue;
+      if (question == kPass) {
+        if (st.min_w) sum = min(sum, max(sum_m, (u64)kOne));
+        const double at = u > 0.0 ? fmin(u, 1.0) * (double)sum : 0.0;   // NaN: 0
+        q.r = min((u64)at, sum - 1);
+      }
+      const int bin = small ? plan.bin0[0] : first_bin(q, s.bins, {0, 0});
+      const Pair before = bin ? s.bins[bin - 1] : Pair{0, 0};
+      const u64 n = s.bins[bin].n - before.n;
+      Found f;
+      bool held = plan.ranges > 0;
+      if (small) {
+        f = among_few(q, few, before);
+      } else {
+        bool named = false;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) named |= plan.bin0[i] <= bin && bin <= plan.bin1[i];
+        held = held && named && answer_mine(r, q, t, bin, before, n, s, &f);
+        if (!held) f = answer_row<BF>(a, b, r, q, bin, before, n, s);
+      }
+      sum = min(sum, f.sum);
+      token = f.token;
+    }
+    token = min(token, a.V - 1);         // within the row whatever a workspace that two calls write at once may hold
   }
   if (tid >= 64) return;
   exps = wave_all(tid < a.chunks ? exps : 0.0, 0.0, Add());

@@ -116,8 +116,7 @@ constexpr int kSampleList = 4096;   // tokens that a row's questions are answere
 
 // What a row's questions need, and where they start from.
 struct SamplePlan {
-  unsigned long long lo[3], hi[3];           // places of the tokens to gather, and their bins
-  int32_t bin0[3], bin1[3];
+  int32_t bin0[3], bin1[3];                  // bins of the tokens to gather
   uint32_t ranges;                           // 0: too many tokens
   uint32_t upto;                             // tokens from the row's largest on to the last of them
   uint32_t count, arrived;                   // gathered tokens, blocks of the launch that are done
