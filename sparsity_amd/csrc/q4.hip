@@ -27,7 +27,7 @@ namespace {
 
 constexpr int kWaves = 8;
 constexpr int kAhead = 4;            // 128-column blocks asked for at a time
-constexpr int kLds = 78 * 1024;      // two blocks per CU
+constexpr int kLds = 40 * 1024;      // four blocks per CU
 
 // ---------------------------------------------------------------------------------------------
 // packing
@@ -74,43 +74,47 @@ __global__ __launch_bounds__(256) void q4_pack_kernel(Q4PackArgs a) {
 // product
 // ---------------------------------------------------------------------------------------------
 
-template <int G>
-struct Q4Scales {                                          // of a lane's four rows in a block
-  uint32_t w[128 / G * 2];
-};
+typedef int v2i __attribute__((ext_vector_type(2)));
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
-template <int G, int NT, int RT>
-__global__ __launch_bounds__(64 * kWaves) void q4_fwd_kernel(Q4Args a) {
+// The MFMA's sums start from the bits of 1.5 * 2^23: what comes out, read as a float, is that number plus the sum,
+// which is below 2^22, and a subtraction takes the place of a conversion.
+constexpr float kBias = 12582912.f;
+constexpr int kBiasBits = 0x4B400000;
+
+// Four rows' sums of a token, from row o on.
+__device__ __forceinline__ void put_rows(const Q4Args& a, int t, int64_t o, const float sum[4]) {
+  if (o >= a.n) return;
+  const float s = a.x_scale[t] * 0.0625f;
+  float* y = a.y + (size_t)t * a.n + o;
+  if (a.n % 4 == 0) {
+    *(float4*)y = make_float4(sum[0] * s, sum[1] * s, sum[2] * s, sum[3] * s);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (o + e < a.n) y[e] = sum[e] * s;
+  }
+}
+
+// Up to 16 tokens: few registers and little LDS, so that many waves are there to wait for memory.
+template <int G>
+__global__ __launch_bounds__(64 * kWaves) void q4_narrow_kernel(Q4Args a) {
   constexpr int NG = 128 / G;
-  extern __shared__ __attribute__((aligned(16))) int8_t sm_x[];      // [tokens][chunk + 16]
+  constexpr int U = G == 32 ? 32 : 64;                     // columns of one MFMA
+  extern __shared__ __attribute__((aligned(16))) int8_t sm_x[];      // [chunk / U][tokens][U]
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int q = lane >> 4, r = lane & 15;
-  // token tiles of the same rows run side by side on one XCD (workgroups are dealt round-robin)
-  const int tt = a.token_tiles;
-  const int64_t id = blockIdx.x;
-  const int64_t rows_at = id / (8 * tt) * 8 + id % 8;
-  const int token0 = (int)(id / 8 % tt) * 16 * NT;
-  const int tokens = min(a.T - token0, 16 * NT);
+  const int tokens = a.T;
   const int ks = a.ksplit, part = wave % ks;
-  const int64_t tile0 = (rows_at * (kWaves / ks) + wave / ks) * RT;
-  if (rows_at * (kWaves / ks) * RT >= a.tiles) return;     // a padding block: all of it
-  const bool busy = tile0 < a.tiles;
-  const int stride = a.chunk + 16;
+  const int64_t tile = (int64_t)blockIdx.x * (kWaves / ks) + wave / ks;
+  const bool busy = tile < a.tiles;
+  const int64_t from = min(tile, a.tiles - 1);
+  const v4i* codes = (const v4i*)a.codes + from * a.blocks * 64 + lane;
+  const v2u* scales = (const v2u*)a.scales + (from * a.blocks * 4 + q) * NG;
+  const int8_t* x = sm_x + min(r, tokens - 1) * U + U / 4 * q;       // a spare token repeats the last one
 
-  const v4i* codes[RT];
-  const uint32_t* scales[RT];
-#pragma unroll
-  for (int i = 0; i < RT; ++i) {                           // a spare tile repeats the last one, stores nothing
-    const int64_t t = min(tile0 + i, a.tiles - 1);
-    codes[i] = (const v4i*)a.codes + t * a.blocks * 64 + lane;
-    scales[i] = (const uint32_t*)a.scales + (t * a.blocks * 4 + q) * (NG * 2);
-  }
-  const int8_t* x[NT];
-#pragma unroll
-  for (int j = 0; j < NT; ++j)                             // a spare token repeats the last one
-    x[j] = sm_x + min(16 * j + r, tokens - 1) * stride + (G == 32 ? 8 : 16) * q;
-
-  float sum[RT][NT][4] = {};
+  const v4i bias = {kBiasBits, kBiasBits, kBiasBits, kBiasBits};
+  float sum[4] = {};
   for (int c0 = 0; c0 < a.blocks; c0 += a.chunk / 128) {   // blocks whose columns are in LDS
     const int cn = min(a.chunk / 128, a.blocks - c0);
     if (c0) __syncthreads();
@@ -119,74 +123,50 @@ __global__ __launch_bounds__(64 * kWaves) void q4_fwd_kernel(Q4Args a) {
       const int per = cols / 16;                           // K % 32 == 0
       for (int i = threadIdx.x; i < tokens * per; i += 64 * kWaves) {
         const int t = i / per, c = (i - t * per) * 16;
-        *(int4*)(sm_x + t * stride + c) = *(const int4*)(a.xq + (size_t)(token0 + t) * a.K + c0 * 128 + c);
+        *(v4i*)(sm_x + ((c / U) * tokens + t) * U + c % U) = *(const v4i*)(a.xq + (size_t)t * a.K + c0 * 128 + c);
       }
     }
     __syncthreads();
     if (!busy) continue;
     for (int b0 = part; b0 < cn; b0 += ks * kAhead) {
-      v4i code[kAhead][RT];
-      Q4Scales<G> sc[kAhead][RT];
+      v4i code[kAhead];
+      v2u scale[kAhead][NG];
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
         const int64_t b = c0 + min(b0 + u * ks, cn - 1);
+        code[u] = __builtin_nontemporal_load(codes + b * 64);
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          code[u][i] = __builtin_nontemporal_load(codes[i] + b * 64);
-          const uint32_t* p = scales[i] + b * 4 * (NG * 2);
-          if constexpr (G == 128) {
-            *(uint2*)sc[u][i].w = *(const uint2*)p;
-          } else {
-            *(uint4*)sc[u][i].w = *(const uint4*)p;
-            if constexpr (G == 32) *(uint4*)(sc[u][i].w + 4) = *(const uint4*)(p + 4);
-          }
-        }
+        for (int g = 0; g < NG; ++g) scale[u][g] = scales[b * 4 * NG + g];
       }
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
         const int b = b0 + u * ks;
         if (b >= cn) break;
+        v4i av[2];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t d = (uint32_t)code[u][w];
+          av[w >> 1][(w & 1) * 2] = (int)((d << 4) & 0xF0F0F0F0u);
+          av[w >> 1][(w & 1) * 2 + 1] = (int)(d & 0xF0F0F0F0u);
+        }
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
+          const int8_t* p = x + (b * 128 + g * G) * tokens;
+          v4i acc;
+          if constexpr (G == 32) {
+            const v2i half = {av[g >> 1][(g & 1) * 2], av[g >> 1][(g & 1) * 2 + 1]};
+            acc = __builtin_amdgcn_mfma_i32_16x16x32_i8(__builtin_bit_cast(long, half),
+                                                        __builtin_bit_cast(long, *(const v2i*)p), bias, 0, 0, 0);
+          } else if constexpr (G == 64) {
+            acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(av[g], *(const v4i*)p, bias, 0, 0, 0);
+          } else {
+            acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(av[0], *(const v4i*)p, bias, 0, 0, 0);
+            acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(av[1], *(const v4i*)(p + 64 * tokens), acc, 0, 0, 0);
+          }
 #pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            const int8_t* xb = x[j] + b * 128 + g * G;
-            if constexpr (G == 32) {
-              const int2 xv = *(const int2*)xb;
-#pragma unroll
-              for (int i = 0; i < RT; ++i) {
-                const uint32_t d = (uint32_t)code[u][i][g];
-                const uint2 lo_hi = {(d << 4) & 0xF0F0F0F0u, d & 0xF0F0F0F0u};
-                const v4i acc = __builtin_amdgcn_mfma_i32_16x16x32_i8(__builtin_bit_cast(long, lo_hi),
-                                                                      __builtin_bit_cast(long, xv), v4i{}, 0, 0, 0);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const uint32_t w = sc[u][i].w[g * 2 + (e >> 1)];
-                  sum[i][j][e] = __builtin_fmaf((float)acc[e], (e & 1) ? bf16_hi(w) : bf16_lo(w), sum[i][j][e]);
-                }
-              }
-            } else {
-              v4i xv[G / 64];
-#pragma unroll
-              for (int h = 0; h < G / 64; ++h) xv[h] = *(const v4i*)(xb + 64 * h);
-#pragma unroll
-              for (int i = 0; i < RT; ++i) {
-                v4i acc = {};
-#pragma unroll
-                for (int h = 0; h < G / 64; ++h) {
-                  const int w0 = (G == 64 ? 2 * g : 2 * h);
-                  const uint32_t d0 = (uint32_t)code[u][i][w0], d1 = (uint32_t)code[u][i][w0 + 1];
-                  const v4i av = {(int)((d0 << 4) & 0xF0F0F0F0u), (int)(d0 & 0xF0F0F0F0u),
-                                  (int)((d1 << 4) & 0xF0F0F0F0u), (int)(d1 & 0xF0F0F0F0u)};
-                  acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(av, xv[h], acc, 0, 0, 0);
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const uint32_t w = sc[u][i].w[g * 2 + (e >> 1)];
-                  sum[i][j][e] = __builtin_fmaf((float)acc[e], (e & 1) ? bf16_hi(w) : bf16_lo(w), sum[i][j][e]);
-                }
-              }
-            }
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t s = scale[u][g][e >> 1];
+            sum[e] = __builtin_fmaf(__int_as_float(acc[e]) - kBias, (e & 1) ? bf16_hi(s) : bf16_lo(s), sum[e]);
           }
         }
       }
@@ -197,74 +177,186 @@ __global__ __launch_bounds__(64 * kWaves) void q4_fwd_kernel(Q4Args a) {
     float* red = (float*)sm_x;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) red[((wave * RT + i) * NT + j) * 256 + e * 64 + lane] = sum[i][j][e];
+    for (int e = 0; e < 4; ++e) red[wave * 256 + e * 64 + lane] = sum[e];
     __syncthreads();
     if (part) return;
     for (int p = 1; p < ks; ++p)
 #pragma unroll
-      for (int i = 0; i < RT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sum[i][j][e] += red[(((wave + p) * RT + i) * NT + j) * 256 + e * 64 + lane];
+      for (int e = 0; e < 4; ++e) sum[e] += red[(wave + p) * 256 + e * 64 + lane];
   }
-  if (!busy) return;
+  if (busy && r < tokens) put_rows(a, r, tile * 16 + 4 * q, sum);
+}
+
+// More than 16 tokens: the same product with the tokens' rows in two LDS buffers of kWide blocks of 128 columns.  While a
+// buffer is multiplied, the next one is filled past the registers and the next weights are on their way; one barrier
+// and one wait per buffer.  KS waves share a tile's columns, kWide / KS blocks of a buffer each.
+constexpr int kWide = 4;
+
+template <int G, int NT, int KS>
+__global__ __launch_bounds__(64 * kWaves, 4) void q4_wide_kernel(Q4Args a) {
+  constexpr int NG = 128 / G, A = kWide / KS;
+  constexpr int U = G == 32 ? 32 : 64;
+  constexpr int kBuffer = 16 * NT * kWide * 128;
+  __shared__ __attribute__((aligned(16))) int8_t sm[2][kBuffer];     // [columns / U][tokens][U]
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int q = lane >> 4, r = lane & 15;
+  const int tt = a.token_tiles;
+  const int64_t id = blockIdx.x;
+  const int64_t rows_at = id / (8 * tt) * 8 + id % 8;
+  const int token0 = (int)(id / 8 % tt) * 16 * NT;
+  const int tokens = min(a.T - token0, 16 * NT);
+  const int part = wave % KS;
+  const int64_t tile = rows_at * (kWaves / KS) + wave / KS;
+  if (rows_at * (kWaves / KS) >= a.tiles) return;          // a padding block: all of it
+  const int64_t from = min(tile, a.tiles - 1);             // a spare wave repeats the last tile, stores nothing
+  const v4i* codes = (const v4i*)a.codes + from * a.blocks * 64 + lane;
+  const v2u* scales = (const v2u*)a.scales + (from * a.blocks * 4 + q) * NG;
+
+  // Sixteen bytes per lane and turn, in the order in which they lie in LDS; where the tokens are fewer than the
+  // buffer's, or the columns past K (which meet codes of zero), some are read twice.
+  constexpr int kTurns = kBuffer / (16 * 64 * kWaves);
+  auto fill = [&](int c0, int8_t* to) {
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int t = token0 + 16 * j + r;
-    if (16 * j + r >= tokens) continue;
-    const float s = a.x_scale[t] * 0.0625f;
+    for (int k = 0; k < kTurns; ++k) {
+      const int i = (k * kWaves + wave) * 64 + lane;
+      const int at = i / (U / 16), step = at / (16 * NT), t = at % (16 * NT);
+      const int c = c0 * 128 + step * U + i % (U / 16) * 16;
+      lds_dma16(a.xq + (size_t)(token0 + min(t, tokens - 1)) * a.K + min(c, a.K - 16),
+                lds_offset(to) + (uint32_t)__builtin_amdgcn_readfirstlane((k * kWaves + wave) * 1024));
+    }
+  };
+  v4i code[A];
+  v2u scale[A][NG];
+  auto load = [&](int c0) {
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const int64_t o = (tile0 + i) * 16 + 4 * q;
-      if (o >= a.n) continue;
-      float* y = a.y + (size_t)t * a.n + o;
-      if (a.n % 4 == 0) {
-        *(float4*)y = make_float4(sum[i][j][0] * s, sum[i][j][1] * s, sum[i][j][2] * s, sum[i][j][3] * s);
-      } else {
+    for (int u = 0; u < A; ++u) {
+      const int64_t b = min(c0 + part + u * KS, a.blocks - 1);
+      const uint32_t live = c0 + part + u * KS < a.blocks ? ~0u : 0u;   // past the last block: scales of 0
+      code[u] = __builtin_nontemporal_load(codes + b * 64);
+#pragma unroll
+      for (int g = 0; g < NG; ++g) scale[u][g] = scales[b * 4 * NG + g] & live;
+    }
+  };
+
+  const v4i bias = {kBiasBits, kBiasBits, kBiasBits, kBiasBits};
+  float sum[NT][4] = {};
+  fill(0, sm[0]);
+  load(0);
+  for (int c0 = 0, turn = 0; c0 < a.blocks; c0 += kWide, turn ^= 1) {
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(0));            // this buffer and its weights
+    v4i now[A];
+    v2u now_scale[A][NG];
+#pragma unroll
+    for (int u = 0; u < A; ++u) {
+      now[u] = code[u];
+#pragma unroll
+      for (int g = 0; g < NG; ++g) now_scale[u][g] = scale[u][g];
+    }
+    block_barrier_nofence();                               // and the other buffer has been read
+    if (c0 + kWide < a.blocks) {
+      fill(c0 + kWide, sm[turn ^ 1]);
+      load(c0 + kWide);
+    }
+    const int8_t* x = sm[turn] + r * U + U / 4 * q;
+#pragma unroll
+    for (int u = 0; u < A; ++u) {
+      const int8_t* xb = x + (part + u * KS) * 128 * 16 * NT;
+      v4i av[2];
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t d = (uint32_t)now[u][w];
+        av[w >> 1][(w & 1) * 2] = (int)((d << 4) & 0xF0F0F0F0u);
+        av[w >> 1][(w & 1) * 2 + 1] = (int)(d & 0xF0F0F0F0u);
+      }
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        float sv[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (o + e < a.n) y[e] = sum[i][j][e] * s;
+          sv[e] = (e & 1) ? bf16_hi(now_scale[u][g][e >> 1]) : bf16_lo(now_scale[u][g][e >> 1]);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const int8_t* p = xb + (g * G * NT + j * U) * 16;
+          v4i acc;
+          if constexpr (G == 32) {
+            const v2i half = {av[g >> 1][(g & 1) * 2], av[g >> 1][(g & 1) * 2 + 1]};
+            acc = __builtin_amdgcn_mfma_i32_16x16x32_i8(__builtin_bit_cast(long, half),
+                                                        __builtin_bit_cast(long, *(const v2i*)p), bias, 0, 0, 0);
+          } else if constexpr (G == 64) {
+            acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(av[g], *(const v4i*)p, bias, 0, 0, 0);
+          } else {
+            acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(av[0], *(const v4i*)p, bias, 0, 0, 0);
+            acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(av[1], *(const v4i*)(p + 64 * 16 * NT), acc, 0, 0, 0);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum[j][e] = __builtin_fmaf(__int_as_float(acc[e]) - kBias, sv[e], sum[j][e]);
+        }
       }
+      __builtin_amdgcn_sched_barrier(0);                   // a block at a time: its weights unpacked are enough registers
     }
+  }
+
+  if constexpr (KS > 1) {                                  // parts of a tile, joined by its first wave in order
+    float* red = (float*)sm;
+    static_assert(sizeof(sm) >= kWaves * NT * 1024, "partial sums fit");
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) red[(wave * NT + j) * 256 + e * 64 + lane] = sum[j][e];
+    __syncthreads();
+    if (part) return;
+    for (int p = 1; p < KS; ++p)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[j][e] += red[((wave + p) * NT + j) * 256 + e * 64 + lane];
+  }
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int t = 16 * j + r;
+    if (t < tokens) put_rows(a, token0 + t, tile * 16 + 4 * q, sum[j]);
   }
 }
 
-template <int G, int NT, int RT>
-hipError_t fwd(Q4Args a, hipStream_t s) {
-  const int tokens = std::min(a.T, 16 * NT);
-  // columns in LDS at a time: even parts of K
-  const int most = (kLds / tokens - 16) / 128 * 128;
-  const int chunks = (a.blocks * 128 + most - 1) / most;
-  a.chunk = (a.blocks + chunks - 1) / chunks * 128;
-  // waves on one tile's columns: until there are two waves per SIMD, or no columns to share
-  a.token_tiles = (a.T + 16 * NT - 1) / (16 * NT);
-  a.ksplit = 1;
-  while (a.ksplit < kWaves && a.tiles / RT * a.token_tiles * a.ksplit < 2048 && a.ksplit * 2 <= a.chunk / 128)
-    a.ksplit *= 2;
-  const int64_t per = kWaves / a.ksplit * RT;
+template <int G, int NT, int KS>
+hipError_t wide(Q4Args a, hipStream_t s) {
+  constexpr int per = kWaves / KS;
   const int64_t row_blocks = (a.tiles + per - 1) / per;
   const int64_t grid = (row_blocks + 7) / 8 * 8 * a.token_tiles;
-  size_t lds = (size_t)tokens * (a.chunk + 16);
-  if (a.ksplit > 1) lds = std::max(lds, (size_t)kWaves * RT * NT * 1024);
-  if (lds > 64 * 1024) {
-    const hipError_t e = hipFuncSetAttribute((const void*)q4_fwd_kernel<G, NT, RT>,
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
-    if (e != hipSuccess) return e;
-  }
-  q4_fwd_kernel<G, NT, RT><<<(unsigned)grid, 64 * kWaves, lds, s>>>(a);
+  q4_wide_kernel<G, NT, KS><<<(unsigned)grid, 64 * kWaves, 0, s>>>(a);
   return hipGetLastError();
 }
 
 template <int G>
-hipError_t fwd_tokens(const Q4Args& a, hipStream_t s) {
-  if (a.T <= 16) return fwd<G, 1, 1>(a, s);
-  if (a.T <= 32) return fwd<G, 2, 1>(a, s);
-  return fwd<G, 4, 1>(a, s);
+hipError_t narrow(Q4Args a, hipStream_t s) {
+  // columns in LDS at a time: even parts of K
+  const int most = kLds / a.T / 128 * 128;
+  const int chunks = (a.blocks * 128 + most - 1) / most;
+  a.chunk = (a.blocks + chunks - 1) / chunks * 128;
+  // waves on one tile's columns: until there are two waves per SIMD, or no columns to share
+  a.ksplit = 1;
+  while (a.ksplit < kWaves && a.tiles * a.ksplit < 8192 && a.ksplit * 2 <= a.chunk / 128) a.ksplit *= 2;
+  const int64_t per = kWaves / a.ksplit;
+  size_t lds = (size_t)a.T * a.chunk;
+  if (a.ksplit > 1) lds = std::max(lds, (size_t)kWaves * 1024);
+  q4_narrow_kernel<G><<<(unsigned)((a.tiles + per - 1) / per), 64 * kWaves, lds, s>>>(a);
+  return hipGetLastError();
+}
+
+template <int G, int NT>
+hipError_t wide_split(Q4Args a, hipStream_t s) {
+  a.token_tiles = (a.T + 16 * NT - 1) / (16 * NT);
+  const int64_t waves = a.tiles * a.token_tiles;
+  if (G > 32 && (waves >= 2048 || a.blocks < 2)) return wide<G, NT, 1>(a, s);
+  if (waves >= 1024 || a.blocks < 4) return wide<G, NT, 2>(a, s);
+  return wide<G, NT, 4>(a, s);
+}
+
+template <int G>
+hipError_t fwd(const Q4Args& a, hipStream_t s) {
+  if (a.T <= 16) return narrow<G>(a, s);
+  return a.T <= 32 ? wide_split<G, 2>(a, s) : wide_split<G, 4>(a, s);
 }
 
 }  // namespace
@@ -283,9 +375,9 @@ hipError_t launch_q4_pack(const Q4PackArgs& a, bool bf16, hipStream_t s) {
 }
 
 hipError_t launch_q4_fwd(const Q4Args& a, int group, hipStream_t s) {
-  if (group == 32) return fwd_tokens<32>(a, s);
-  if (group == 64) return fwd_tokens<64>(a, s);
-  return fwd_tokens<128>(a, s);
+  if (group == 32) return fwd<32>(a, s);
+  if (group == 64) return fwd<64>(a, s);
+  return fwd<128>(a, s);
 }
 
 }  // namespace bl
