@@ -8,19 +8,20 @@
 // Gradient: tokens are sorted by id, so that a row's tokens are a run of sorted positions, and each run
 // is summed in the order of its tokens: results do not vary from run to run, and nothing is added by
 // atomics.  Launches:
-//   sort   blocks sort a chunk of tokens each in LDS; where the gradient is overwritten, the other blocks
-//          of the launch clear it meanwhile (most of the bytes of a large table)
+//   sort   blocks sort a chunk of tokens each, in registers and LDS
 //   rank   (several chunks) an element's place is its place in its chunk plus, by bisection, what the
 //          other chunks hold before it
 //   sum    a wave takes 16 sorted positions and 512 columns; it sums every run that starts there, up to
 //          32 positions of it, and writes the row; of a longer run, what lies inside its 16 goes to the
-//          workspace
+//          workspace.  Where the gradient is overwritten, the other blocks of the launch clear the rows that
+//          no token names (most of the bytes of a large table; the first are cleared beside the sort)
 //   join   the pieces of long runs, in order
 #include <algorithm>
 
 #include "block_ops.hpp"
 #include "device_common.hpp"
 #include "step_ops.hpp"
+#include "wave_ops.hpp"
 
 namespace bl {
 
@@ -64,7 +65,12 @@ __global__ __launch_bounds__(256) void embed_kernel(EmbedArgs a) {
 // ---------------------------------------------------------------------------------------------
 
 constexpr uint32_t kNone = 0xFFFFFFFFu;      // an id outside the table: sorted last, never summed
-constexpr int kFillBlocks = 2048;
+constexpr int kChunk = kEmbedChunk;
+constexpr int kSortThreads = kChunk / 2;
+constexpr int kFillRows = 8;                 // rows that a wave of a fill block looks up
+// Bytes of the gradient that are cleared beside the sort, whose few blocks leave most of the chip idle for 9 us.
+constexpr int64_t kFillSort = 40 << 20;
+constexpr unsigned kFillBlocks = 512;
 
 struct Sorted {                              // the workspace's arrays
   uint32_t *chunk_id, *chunk_tok, *id, *tok;
@@ -73,86 +79,179 @@ struct Sorted {                              // the workspace's arrays
   int32_t chunks;
 };
 
-// Chunk blockIdx.x of CH tokens by id, then token; the blocks behind clear the gradient.
-template <int CH, int THREADS>
-__global__ __launch_bounds__(THREADS) void embed_sort_kernel(EmbedBwdArgs a, Sorted s) {
-  __shared__ uint64_t key[CH];
-  const int tid = threadIdx.x;
+// One step of a bitonic network inside a wave: the lane's key against the one at distance d.
+template <class Key>
+__device__ __forceinline__ Key exchange(Key v, int d, bool up) {
+  Key w;
+  if constexpr (sizeof(Key) == 8) w = (Key)__shfl_xor((long long)v, d, 64);
+  else if (d == 1) w = lane_move<0xB1, 0xF>(v, v);           // within rows of lanes in registers
+  else if (d == 2) w = lane_move<0x4E, 0xF>(v, v);
+  else if (d == 8) w = lane_move<0x128, 0xF>(v, v);
+  else w = (Key)__shfl_xor((int)v, d, 64);
+  const bool low = (threadIdx.x & d) == 0;
+  return (v < w) == (low == up) ? v : w;
+}
+
+// Clears the gradient's first rows, whatever comes to stand there: block `at` of `blocks`.
+__device__ __forceinline__ void fill_first(const EmbedBwdArgs& a, int64_t rows, int64_t at, int64_t blocks) {
+  float4* out = (float4*)a.dtable;
+  const int64_t i1 = rows * a.K / 4;
+  for (int64_t i = at * blockDim.x + threadIdx.x; i < i1; i += blocks * blockDim.x)
+    out[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
+// Chunk blockIdx.x of the tokens by id, then token.  A key is the id over the bits of the token's place in the
+// chunk: 32 bits in all for tables of less than 2^21 rows.  Two keys to a thread; distances below 64 inside a wave.
+template <class Key>
+__global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(EmbedBwdArgs a, Sorted s, int64_t fill) {
+  __shared__ Key key[kChunk];
   if ((int)blockIdx.x >= s.chunks) {
-    const int64_t n = a.V * a.K / 4;
-    const int64_t step = (int64_t)(gridDim.x - s.chunks) * THREADS;
-    float4* out = (float4*)a.dtable;
-    for (int64_t i = (int64_t)(blockIdx.x - s.chunks) * THREADS + tid; i < n; i += step)
-      out[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    fill_first(a, fill, blockIdx.x - s.chunks, gridDim.x - s.chunks);
     return;
   }
-  const int64_t t0 = (int64_t)blockIdx.x * CH;
+  constexpr int kBits = kEmbedChunkBits;
+  const int tid = threadIdx.x;
+  const int64_t t0 = (int64_t)blockIdx.x * kChunk;
+  const Key none = (Key)~(Key)0 >> kBits;
   if (blockIdx.x == 0 && tid == 0) s.runs[0] = 0;
-  for (int i = tid; i < CH; i += THREADS) {
-    const int64_t t = t0 + i;
-    uint32_t id = kNone;
-    if (t < a.T) {
-      const int32_t v = a.ids[t];
-      if (v >= 0 && v < a.V) id = (uint32_t)v;
-    }
-    key[i] = ((uint64_t)id << 32) | (uint32_t)i;
+  Key v[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int i = h * kSortThreads + tid;
+    const int32_t id = t0 + i < a.T ? a.ids[t0 + i] : -1;
+    v[h] = (id >= 0 && id < a.V ? (Key)id : none) << kBits | (Key)i;
   }
-  __syncthreads();
-  // bitonic network: after the step of size n, runs of n are in order, every other one reversed
-  for (int n = 2; n <= CH; n <<= 1) {
-    for (int d = n >> 1; d > 0; d >>= 1) {
-      for (int i = tid; i < CH / 2; i += THREADS) {
-        const int lo = ((i & ~(d - 1)) << 1) | (i & (d - 1)), hi = lo | d;
-        const uint64_t x = key[lo], y = key[hi];
+  for (int n = 2; n <= kChunk; n <<= 1) {    // runs of n in order, every other one reversed
+    if (n > 64) {
+      __syncthreads();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) key[h * kSortThreads + tid] = v[h];
+      __syncthreads();
+      for (int d = n >> 1; d >= 64; d >>= 1) {
+        const int lo = ((tid & ~(d - 1)) << 1) | (tid & (d - 1)), hi = lo | d;
+        const Key x = key[lo], y = key[hi];
         if ((x > y) == ((lo & n) == 0)) {
           key[lo] = y;
           key[hi] = x;
         }
+        __syncthreads();
       }
-      __syncthreads();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) v[h] = key[h * kSortThreads + tid];
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) {
+      if (d >= n) continue;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) v[h] = exchange(v[h], d, ((h * kSortThreads + tid) & n) == 0);
     }
   }
-  for (int i = tid; i < CH; i += THREADS) {
-    s.chunk_id[t0 + i] = (uint32_t)(key[i] >> 32);
-    s.chunk_tok[t0 + i] = (uint32_t)t0 + (uint32_t)key[i];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int i = h * kSortThreads + tid;
+    s.chunk_id[t0 + i] = v[h] >> kBits == none ? kNone : (uint32_t)(v[h] >> kBits);
+    s.chunk_tok[t0 + i] = (uint32_t)t0 + (uint32_t)(v[h] & (kChunk - 1));
   }
 }
 
 // Places of the sorted chunks' elements among all of them: chunks before count what is not above, the
-// ones behind what is below, so equal ids stay in the order of their tokens.
-template <int CH>
-__global__ __launch_bounds__(256) void embed_rank_kernel(int64_t T, Sorted s) {
-  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int mine = (int)(e / CH);
+// ones behind what is below, so equal ids stay in the order of their tokens.  The chunks' ids are searched in
+// LDS, four chunks at a time.
+constexpr int kRankChunks = 16;              // in LDS at a time
+constexpr int kRankThreads = 512;
+__global__ __launch_bounds__(kRankThreads) void embed_rank_kernel(int64_t T, Sorted s) {
+  __shared__ __attribute__((aligned(16))) uint32_t k[kRankChunks * kChunk];
+  const int64_t e = (int64_t)blockIdx.x * kRankThreads + threadIdx.x;
+  const int mine = (int)(e / kChunk);
   const uint32_t id = s.chunk_id[e], tok = s.chunk_tok[e];
-  int64_t place = e - (int64_t)mine * CH;
-#pragma unroll 4
-  for (int c = 0; c < s.chunks; ++c) {
-    if (c == mine) continue;
-    const uint32_t* k = s.chunk_id + (int64_t)c * CH;
-    const uint64_t bar = (uint64_t)id + (c < mine);   // what is below this comes first
-    int n = 0;
+  int64_t place = e - (int64_t)mine * kChunk;
+  for (int c0 = 0; c0 < s.chunks; c0 += kRankChunks) {
+    const int n = min(kRankChunks, s.chunks - c0);
+    __syncthreads();
+    for (int i = threadIdx.x; i < n * kChunk / 4; i += kRankThreads)
+      ((uint4*)k)[i] = ((const uint4*)s.chunk_id)[(int64_t)c0 * (kChunk / 4) + i];
+    __syncthreads();
+    for (int c = 0; c < n; c += 4) {
+      int at[4] = {};
+      uint64_t bar[4];
+      const uint32_t* in[4];
 #pragma unroll
-    for (int d = CH / 2; d > 0; d >>= 1)
-      if (k[n + d - 1] < bar) n += d;
-    if (k[n] < bar) ++n;
-    place += n;
+      for (int j = 0; j < 4; ++j) {
+        bar[j] = (uint64_t)id + (c0 + c + j < mine);         // what is below this comes first
+        in[j] = k + min(c + j, n - 1) * kChunk;
+      }
+#pragma unroll
+      for (int d = kChunk / 2; d > 0; d >>= 1)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) at[j] += in[j][at[j] + d - 1] < bar[j] ? d : 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        at[j] += in[j][at[j]] < bar[j];
+        if (c + j < n && c0 + c + j != mine) place += at[j];
+      }
+    }
   }
-  if (tok < T && place < T) {
+  if (tok < T) {
     s.id[place] = id;
     s.tok[place] = tok;
   }
 }
 
-// One wave: kEmbedTile sorted positions, 512 columns.
+// Rows of a fill block: a few waves' where they are short.
+__host__ __device__ inline int fill_rows_of_block(int K) { return K <= 1024 ? 4 * kFillRows : kFillRows; }
+
+// Clears the rows from r0 on that no token names.  Eight lanes look one row up among the sorted ids, eight places at a time.
+__device__ __forceinline__ void fill_rows(const EmbedBwdArgs& a, const Sorted& s, int64_t r0, int rows) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  __shared__ uint8_t named[4 * kFillRows];
+  const int mine = wave * kFillRows + (lane >> 3);
+  if (mine < rows) {
+    const uint32_t row = (uint32_t)(r0 + mine);
+    int64_t lo = 0, hi = a.T;                // the first place whose id is not below the row's
+    while (hi > lo) {
+      const int64_t step = (hi - lo + 7) >> 3, at = lo + (lane & 7) * step;
+      const bool below = at < hi && s.id[at] < row;
+      const uint32_t mask = (uint32_t)(__ballot(below) >> (lane & 56)) & 0xFF;
+      if (mask == 0) break;                  // s.id[lo] is not
+      const int last = 31 - __clz((int)mask);
+      hi = min(hi, lo + (last + 1) * step);
+      lo += last * step + 1;
+    }
+    if ((lane & 7) == 0) named[mine] = lo < a.T && s.id[lo] == row;
+  }
+  __syncthreads();
+  const int k4 = a.K / 4;
+  int w = 256;                               // threads to a row
+  while (w / 2 >= k4) w >>= 1;
+  for (int r = tid / w; r < rows; r += 256 / w) {
+    if (r0 + r >= a.V || named[r]) continue;
+    float4* out = (float4*)(a.dtable + (size_t)(r0 + r) * a.K);
+    for (int c = tid & (w - 1); c < k4; c += w) out[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+}
+
+// One wave: kEmbedTile sorted positions, 512 columns.  The blocks behind the sums' clear the other rows.
 template <bool DBF, bool ACC>
-__global__ __launch_bounds__(256) void embed_sum_kernel(EmbedBwdArgs a, Sorted s) {
+__global__ __launch_bounds__(256) void embed_sum_kernel(EmbedBwdArgs a, Sorted s, int64_t sum_blocks, int slices,
+                                                        int64_t filled) {
   constexpr int U = ACC ? 4 : 8;             // rows in flight
+  if constexpr (!ACC) {
+    if ((int64_t)blockIdx.x >= sum_blocks) {
+      const int rows = fill_rows_of_block(a.K);
+      const int64_t step = gridDim.x - sum_blocks;
+      for (int64_t b = blockIdx.x - sum_blocks; filled + b * rows < a.V; b += step) {
+        fill_rows(a, s, filled + b * rows, rows);
+        __syncthreads();
+      }
+      return;
+    }
+  }
   const int lane = threadIdx.x & 63;
-  const int64_t tile = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int slice = blockIdx.x % slices;
+  const int64_t tile = (int64_t)(blockIdx.x / slices) * 4 + (threadIdx.x >> 6);
   const int64_t p0 = tile * kEmbedTile;
   if (p0 >= a.T) return;
-  const int col = blockIdx.y * 512 + lane * 8;
+  const int col = slice * 512 + lane * 8;
   const bool live = col < a.K;
   // ids and tokens of the 64 positions from p0 on, ids of the 64 before
   const uint32_t id = p0 + lane < a.T ? s.id[p0 + lane] : kNone;
@@ -187,7 +286,7 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedBwdArgs a, Sorted s
     if (!is_head && stop - start > kEmbedLong) {
       end = kEmbedTile;
       piece = true;
-      if (lane == 0 && blockIdx.y == 0) {    // the list's order is irrelevant: its runs are independent
+      if (lane == 0 && slice == 0) {         // the list's order is irrelevant: its runs are independent
         const uint32_t k = atomicAdd(s.runs, 1u);
         s.runs[1 + 2 * k] = (uint32_t)(p0 + start);
         s.runs[2 + 2 * k] = (uint32_t)__builtin_amdgcn_readlane((int)id, at);
@@ -251,11 +350,13 @@ __global__ __launch_bounds__(1024) void embed_join_kernel(EmbedBwdArgs a, Sorted
   for (uint32_t k = blockIdx.x; k < n; k += gridDim.x) {
     const int64_t start = s.runs[1 + 2 * k];
     const uint32_t id = s.runs[2 + 2 * k];
-    int64_t lo = start, hi = a.T;            // s.id[lo] is the run's, s.id[hi] is not
+    int64_t lo = start, hi = a.T;            // s.id[lo] is the run's, s.id[hi] is not: 64 places at a time
     while (hi - lo > 1) {
-      const int64_t m = (lo + hi) >> 1;
-      if (s.id[m] == id) lo = m;
-      else hi = m;
+      const int64_t step = (hi - lo + 63) >> 6, at = lo + lane * step;
+      const uint64_t same = __ballot(at < hi && s.id[at] == id);
+      const int last = 63 - __clzll((long long)same);
+      hi = min(hi, lo + (last + 1) * step);
+      lo += last * step;
     }
     const int64_t t0 = start / kEmbedTile, t1 = lo / kEmbedTile;   // tiles of its first and last piece
     float acc[8] = {};
@@ -306,33 +407,34 @@ hipError_t launch_embed_bwd(const EmbedBwdArgs& a, bool dy_bf16, hipStream_t s) 
   so.runs = (uint32_t*)(a.ws + w.runs);
   so.part = (float*)(a.ws + w.part);
   so.chunks = (int32_t)w.chunks;
-  const int64_t n = a.V * a.K / 4;
-  const bool wide = w.chunk == 4096;
-  const int threads = wide ? 1024 : 256;
-  const unsigned fill = a.accumulate ? 0 : (unsigned)std::min<int64_t>(kFillBlocks, (n + threads - 1) / threads);
-  const unsigned blocks = (unsigned)w.chunks + fill;
-  if (blocks == 0) return hipSuccess;
-  if (wide) embed_sort_kernel<4096, 1024><<<blocks, 1024, 0, s>>>(a, so);
-  else embed_sort_kernel<1024, 256><<<blocks, 256, 0, s>>>(a, so);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.T == 0) return e;
-  if (w.chunks > 1) {
-    const unsigned grid = (unsigned)(w.chunks * w.chunk / 256);
-    if (wide) embed_rank_kernel<4096><<<grid, 256, 0, s>>>(a.T, so);
-    else embed_rank_kernel<1024><<<grid, 256, 0, s>>>(a.T, so);
+  hipError_t e = hipSuccess;
+  int64_t filled = 0;
+  if (a.T > 0) {
+    const unsigned sorts = (unsigned)w.chunks;
+    filled = a.accumulate ? 0 : std::min<int64_t>(a.V, kFillSort / (a.K * 4));
+    const unsigned some = filled ? kFillBlocks : 0;
+    if (a.V < ((int64_t)1 << (32 - kEmbedChunkBits))) embed_sort_kernel<uint32_t><<<sorts + some, kSortThreads, 0, s>>>(a, so, filled);
+    else embed_sort_kernel<uint64_t><<<sorts + some, kSortThreads, 0, s>>>(a, so, filled);
     if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (w.chunks > 1) {
+      embed_rank_kernel<<<(unsigned)w.chunks * (kChunk / kRankThreads), kRankThreads, 0, s>>>(a.T, so);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
   }
-  const unsigned slices = (unsigned)((a.K + 511) / 512);
-  const dim3 grid((unsigned)((w.tiles + 3) / 4), slices);
+  const int slices = (a.K + 511) / 512;
+  const int64_t sums = (w.tiles + 3) / 4 * slices;
+  const int fill = fill_rows_of_block(a.K);
+  const int64_t blocks = sums + (a.accumulate ? 0 : std::min<int64_t>((a.V - filled + fill - 1) / fill, 1 << 20));
+  if (blocks == 0) return hipSuccess;
   if (dy_bf16) {
-    if (a.accumulate) embed_sum_kernel<true, true><<<grid, 256, 0, s>>>(a, so);
-    else embed_sum_kernel<true, false><<<grid, 256, 0, s>>>(a, so);
+    if (a.accumulate) embed_sum_kernel<true, true><<<(unsigned)blocks, 256, 0, s>>>(a, so, sums, slices, filled);
+    else embed_sum_kernel<true, false><<<(unsigned)blocks, 256, 0, s>>>(a, so, sums, slices, filled);
   } else {
-    if (a.accumulate) embed_sum_kernel<false, true><<<grid, 256, 0, s>>>(a, so);
-    else embed_sum_kernel<false, false><<<grid, 256, 0, s>>>(a, so);
+    if (a.accumulate) embed_sum_kernel<false, true><<<(unsigned)blocks, 256, 0, s>>>(a, so, sums, slices, filled);
+    else embed_sum_kernel<false, false><<<(unsigned)blocks, 256, 0, s>>>(a, so, sums, slices, filled);
   }
   if ((e = hipGetLastError()) != hipSuccess || a.T <= kEmbedLong) return e;
-  const dim3 jgrid((unsigned)std::min<int64_t>(64, a.T / (kEmbedLong + 1)), slices);
+  const dim3 jgrid((unsigned)std::min<int64_t>(64, a.T / (kEmbedLong + 1)), (unsigned)slices);
   if (a.accumulate) embed_join_kernel<true><<<jgrid, 1024, 0, s>>>(a, so);
   else embed_join_kernel<false><<<jgrid, 1024, 0, s>>>(a, so);
   return hipGetLastError();

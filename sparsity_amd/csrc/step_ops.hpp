@@ -41,24 +41,25 @@ struct EmbedArgs {
 hipError_t launch_embed(const EmbedArgs& a, bool table_bf16, bool y_bf16, hipStream_t s);
 
 // Workspace of the gradient, segments 256-byte aligned:
-//   chunk_id, chunk_tok  [chunks * chunk] ids of a chunk of tokens in order, and their tokens
+//   chunk_id, chunk_tok  [chunks * kEmbedChunk] ids of a chunk of tokens in order, and their tokens
 //   id, tok              [T] the same of all tokens (one chunk: the two are one)
 //   runs                 [1 + 2 * (T / kEmbedLong + 1)] long runs: their number, then first position and id
 //   part                 [tiles][2][K] sums of the pieces of long runs
+constexpr int kEmbedChunkBits = 11;
+constexpr int kEmbedChunk = 1 << kEmbedChunkBits;   // tokens that a block sorts
 constexpr int kEmbedTile = 16;      // sorted positions a wave takes
 constexpr int kEmbedLong = 32;      // a run of more positions is summed in pieces
 
 struct EmbedBwdWs {
-  int64_t chunk, chunks, tiles;
+  int64_t chunks, tiles;
   size_t chunk_id, chunk_tok, id, tok, runs, part, total;
 };
 inline EmbedBwdWs embed_bwd_ws(int64_t T, int64_t K) {
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   EmbedBwdWs w = {};
-  w.chunk = T <= 16384 ? 1024 : 4096;
-  w.chunks = (T + w.chunk - 1) / w.chunk;
+  w.chunks = (T + kEmbedChunk - 1) / kEmbedChunk;
   w.tiles = (T + kEmbedTile - 1) / kEmbedTile;
-  const size_t all = up((size_t)(w.chunks * w.chunk) * 4);
+  const size_t all = up((size_t)(w.chunks * kEmbedChunk) * 4);
   size_t off = 0;
   w.chunk_id = off; off += all;
   w.chunk_tok = off; off += all;

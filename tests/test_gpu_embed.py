@@ -137,6 +137,33 @@ def test_gradient_of_many_tokens(T, V, K, kind):
     _grad_check(rng(T), T, V, K, "bf16", kind)
 
 
+@pytest.mark.parametrize("V", [(1 << 21) - 1, 1 << 21, (1 << 24) + 3])
+@pytest.mark.parametrize("accum", [False, True])
+def test_gradient_of_tables_of_many_rows(V, accum):
+    """Around the change of the sort's keys, first and last rows among the tokens'."""
+    import torch
+    g = rng(V)
+    T, K = 3000, 8
+    ids = g.integers(0, V, T).astype(np.int32)
+    ids[:40] = [0, V - 1, V - 2, 1] * 10
+    ids[50:90] = -1
+    ids[90:130] = np.minimum(V + np.arange(40), 2 ** 31 - 1)
+    dy, ref = _float(g, (T, K), "f32")
+    out = torch.ones((V, K), device="cuda") if accum else torch.full((V, K), float("nan"), device="cuda")
+    out = S.embed_bwd(dy, dev(ids), V, accumulate=accum, out=out)
+    ok = (ids >= 0) & (ids < V)
+    rows, at = np.unique(ids[ok], return_inverse=True)
+    want, mag = np.full((len(rows), K), float(accum)), np.full((len(rows), K), float(accum))
+    np.add.at(want, at, ref[ok].astype(np.float64))
+    np.add.at(mag, at, np.abs(ref[ok].astype(np.float64)))
+    index = torch.from_numpy(rows).cuda().long()
+    got = host(out[index]).astype(np.float64)
+    n = np.bincount(at)[:, None]
+    assert np.all(np.abs(got - want) <= (n + 1) * U * mag * (1 + 2.0 ** -8))
+    out[index] = float(accum)
+    assert bool((out == float(accum)).all())
+
+
 def test_gradient_where_no_id_has_a_row():
     import torch
     ids = torch.tensor([-1, 9, 2 ** 31 - 1, -7] * 20, dtype=torch.int32, device="cuda")
