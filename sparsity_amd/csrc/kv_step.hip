@@ -12,6 +12,7 @@
 // kRowsHere token rows a second launch writes them with all CUs.
 #include "device_common.hpp"
 #include "step_ops.hpp"
+#include "wave_ops.hpp"
 
 namespace bl {
 
@@ -30,11 +31,8 @@ struct Pair {
 // thread past its use of `waves`.
 __device__ __forceinline__ Pair block_scan(Pair v, Pair* waves, Pair* total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int64_t x = __shfl_up(v.a, o, 64), y = __shfl_up(v.b, o, 64);
-    if (lane >= o) { v.a += x; v.b += y; }
-  }
+  auto add = [](int64_t x, int64_t y) { return x + y; };
+  v = {wave_scan(v.a, (int64_t)0, add), wave_scan(v.b, (int64_t)0, add)};
   if (lane == 63) waves[wave] = v;
   __syncthreads();
   Pair all = {0, 0};
