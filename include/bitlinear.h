@@ -707,7 +707,8 @@ int bitlinear_embed(const void* table, int table_dtype, int64_t V, int64_t K, co
  * [T][K]), added to what dtable holds with BL_EMBED_ACCUM (rows without a token are not touched then).
  * Ids outside [0, V) have no row.  Sums are fp32 in a fixed order: results do not vary from run to run.
  * ws: bitlinear_embed_bwd_workspace_bytes of device scratch (256-byte aligned; contents on entry
- * irrelevant).  dtable and ws may overlap nothing.  T == 0 writes zeros (or, accumulating, nothing).
+ * irrelevant); calls that share one must be ordered, on one stream or by events.  dtable and ws may overlap
+ * nothing.  T == 0 writes zeros (or, accumulating, nothing).
  * Two to four launches. */
 #define BL_EMBED_ACCUM 1
 int bitlinear_embed_bwd_workspace_bytes(int64_t T, int64_t K, size_t* ws_bytes);
@@ -736,7 +737,7 @@ int bitlinear_embed_bwd(const void* dy, int dy_dtype, const int32_t* ids, int64_
  *   scales  bf16 at ((i * NB + j) * 4 + h) * (512 / group) + 4 g + r: row 16 i + 4 h + r, columns from
  *           128 j + group * g on
  * codes and scales are 16-byte aligned, of the sizes that bitlinear_q4_bytes gives.  1 <= n <= 2^27, K <= 2^16,
- * T < 2^22, ceil(n / 128) * ceil(T / 64) < 2^22. */
+ * ceil(n / 16) * ceil(K / 128) < 2^24 (2^35 weights), T < 2^22, ceil(n / 128) * ceil(T / 64) < 2^21. */
 int bitlinear_q4_bytes(int64_t n, int64_t K, int group, size_t* code_bytes, size_t* scale_bytes);
 
 /* Packs W (w_dtype [n][K]).  One launch. */
@@ -769,7 +770,8 @@ int bitlinear_q4_fwd(const int8_t* xq, const float* x_scale, int64_t T, int64_t 
  * and logprob -inf.
  *
  * token is int32 [B]; token, logprob_opt and ws may overlap nothing.  ws: bitlinear_sample_workspace_bytes of device
- * scratch (256-byte aligned; contents on entry irrelevant).  0 <= B <= 65535, 1 <= V < 2^31.  Three launches. */
+ * scratch (256-byte aligned; contents on entry irrelevant); calls that share one must be ordered, on one stream or
+ * by events.  0 <= B <= 65535, 1 <= V < 2^24 (the sums of weights are 64 bits).  Three launches. */
 int bitlinear_sample_workspace_bytes(int64_t B, int64_t V, size_t* ws_bytes);
 int bitlinear_sample(const void* x, int x_dtype, int64_t B, int64_t V, int64_t row_stride,
                      const float* temperature_opt, const int32_t* top_k_opt, const float* top_p_opt,

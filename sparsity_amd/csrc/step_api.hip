@@ -24,7 +24,7 @@ bool clash(const Span (&in)[NI], const Span (&out)[NO], const int (&same)[NO]) {
 }
 
 constexpr int64_t kQ4MaxN = (int64_t)1 << 27, kQ4MaxK = (int64_t)1 << 16;
-constexpr int64_t kSampleMaxB = 65535;
+constexpr int64_t kSampleMaxB = 65535, kSampleMaxV = ((int64_t)1 << 24) - 1;   // sums of weights stay below 2^64
 
 }  // namespace
 
@@ -104,6 +104,7 @@ int bitlinear_q4_bytes(int64_t n, int64_t K, int group, size_t* code_bytes, size
   if (group != 32 && group != 64 && group != 128) return BL_ENOTSUP;
   if (n < 1 || n > kQ4MaxN || K < group || K > kQ4MaxK || K % group || !code_bytes || !scale_bytes) return BL_EINVAL;
   const size_t blocks = (size_t)((n + 15) / 16) * (size_t)((K + 127) / 128);
+  if (blocks >= (size_t)1 << 24) return BL_EINVAL;         // a launch's threads: 256 for each of them
   *code_bytes = blocks * 1024;
   *scale_bytes = blocks * (size_t)(2048 / group) * 2;
   return BL_OK;
@@ -128,7 +129,7 @@ int bitlinear_q4_fwd(const int8_t* xq, const float* x_scale, int64_t T, int64_t 
   size_t cb = 0, sb = 0;
   const int st = bitlinear_q4_bytes(n, K, group, &cb, &sb);
   if (st != BL_OK) return st;
-  if (T < 0 || T > kMaxTokens || (n + 127) / 128 * ((T + 63) / 64) >= ((int64_t)1 << 22)) return BL_EINVAL;
+  if (T < 0 || T > kMaxTokens || (n + 127) / 128 * ((T + 63) / 64) >= ((int64_t)1 << 21)) return BL_EINVAL;
   if (T == 0) return BL_OK;
   if (!aligned(xq, 16) || !aligned(x_scale, 4) || !aligned(codes, 16) || !aligned(scales, 16) || !aligned(y, 16))
     return BL_EINVAL;
@@ -141,7 +142,7 @@ int bitlinear_q4_fwd(const int8_t* xq, const float* x_scale, int64_t T, int64_t 
 }
 
 int bitlinear_sample_workspace_bytes(int64_t B, int64_t V, size_t* ws_bytes) {
-  if (B < 0 || B > kSampleMaxB || V < 1 || V > INT32_MAX || !ws_bytes) return BL_EINVAL;
+  if (B < 0 || B > kSampleMaxB || V < 1 || V > kSampleMaxV || !ws_bytes) return BL_EINVAL;
   bl::SampleArgs a = {};
   a.B = B;
   a.V = V;

@@ -4,8 +4,8 @@ first block's input, and the last block's output into the next token ids.
 Raw calls mirror the C ABI (``include/bitlinear.h``): ``bitlinear_kv_step``, ``bitlinear_embed``,
 ``bitlinear_embed_bwd_workspace_bytes``, ``bitlinear_embed_bwd``, ``bitlinear_q4_bytes``,
 ``bitlinear_q4_pack``, ``bitlinear_q4_fwd``, ``bitlinear_sample_workspace_bytes``, ``bitlinear_sample``.
-``kv_step`` / ``embed`` / ``embed_bwd`` / ``q4_pack`` / ``q4_fwd`` / ``sample`` take torch tensors, check them (the C ABI receives bare pointers), allocate outputs that
-are not given and enqueue on torch's current stream.  Every step runs in HIP kernels.
+``kv_step`` / ``embed`` / ``embed_bwd`` / ``q4_pack`` / ``q4_fwd`` / ``sample`` take torch tensors, check them (the
+C ABI receives bare pointers), allocate outputs that are not given and enqueue on torch's current stream.  Every step runs in HIP kernels.
 """
 from __future__ import annotations
 
@@ -38,8 +38,9 @@ def _lib():
         L.bitlinear_q4_fwd.argtypes = [_VP, _VP, _I64, _I64, _VP, _VP, _I32, _I64, _VP, _VP]
         L.bitlinear_sample_workspace_bytes.argtypes = [_I64, _I64, szp]
         L.bitlinear_sample.argtypes = [_VP, _I32, _I64, _I64, _I64, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]
-        for f in (L.bitlinear_sample_workspace_bytes, L.bitlinear_sample, L.bitlinear_q4_bytes, L.bitlinear_q4_pack, L.bitlinear_q4_fwd, L.bitlinear_kv_step, L.bitlinear_embed, L.bitlinear_embed_bwd_workspace_bytes,
-                  L.bitlinear_embed_bwd):
+        for f in (L.bitlinear_kv_step, L.bitlinear_embed, L.bitlinear_embed_bwd_workspace_bytes, L.bitlinear_embed_bwd,
+                  L.bitlinear_q4_bytes, L.bitlinear_q4_pack, L.bitlinear_q4_fwd, L.bitlinear_sample_workspace_bytes,
+                  L.bitlinear_sample):
             f.restype = ctypes.c_int
         _fns = L
     return _fns
@@ -191,7 +192,7 @@ def embed_bwd(dy, ids, V: int, scale: float = 1.0, accumulate: bool = False, out
     """Gradient of ``embed`` for its table: fp32 [V][K] of scale * (the sum of the rows dy[t] of each id).
 
     dy [T][K] fp32 or bf16; ids outside [0, V) have no row.  ``accumulate`` adds to ``out``, which must
-    be given then.  ``ws`` may supply a uint8 workspace.  Results do not vary from run to run.
+    be given then.  ``ws`` may supply a uint8 workspace, for one call at a time.  Results do not vary from run to run.
     """
     import torch
     T, K = _table(dy, "dy")
@@ -274,7 +275,7 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, want
     settings, tensors [B]: temperature (fp32; 0: the largest logit), top_k (int32; 0: off), top_p (fp32; 1: off), min_p
     (fp32; 0: off), applied in this order; None: 1, and off.  Logits that are -inf or NaN are masked; a row of
     them gives -1.  The log probability (fp32 [B]) is that of the token under the logits themselves.  ``out``
-    may supply (tokens, log probabilities or None), ``ws`` a uint8 workspace.
+    may supply (tokens, log probabilities or None), ``ws`` a uint8 workspace, for one call at a time.
     """
     import torch
     shape = logits.shape

@@ -221,7 +221,8 @@ def test_embed_reference_by_differences():
 @pytest.mark.parametrize("n,cols,group,want", [
     (16, 128, 64, 0), (1, 32, 32, 0), (0, 128, 64, EINVAL), (-1, 128, 64, EINVAL), ((1 << 27) + 1, 128, 64, EINVAL),
     (16, 0, 64, EINVAL), (16, 96, 64, EINVAL), (16, 64, 128, EINVAL), (16, 1 << 17, 128, EINVAL), (16, 128, 16, ENOTSUP),
-    (16, 128, 0, ENOTSUP), (16, 128, 256, ENOTSUP)])
+    (16, 128, 0, ENOTSUP), (16, 128, 256, ENOTSUP), (1 << 27, 128, 32, 0), (1 << 27, 256, 64, EINVAL),
+    (1 << 22, 1 << 16, 128, EINVAL)])
 def test_q4_sizes(n, cols, group, want):
     st, codes, scales = K.bitlinear_q4_bytes(n, cols, group)
     assert st == want
@@ -253,7 +254,7 @@ def _q4_fwd(**kw):
 
 @pytest.mark.parametrize("kw,want", [
     (dict(group=1), ENOTSUP), (dict(n=0), EINVAL), (dict(K=0), EINVAL), (dict(K=160), EINVAL), (dict(T=-1), EINVAL),
-    (dict(T=1 << 22), EINVAL), (dict(T=1 << 20, n=1 << 20), EINVAL), (dict(xq=None), EINVAL), (dict(xq=P + 8), EINVAL),
+    (dict(T=1 << 22), EINVAL), (dict(T=1 << 20, n=1 << 20), EINVAL), (dict(T=1 << 14, n=1 << 20), EINVAL), (dict(xq=None), EINVAL), (dict(xq=P + 8), EINVAL),
     (dict(xs=None), EINVAL), (dict(xs=P + SLOT + 2), EINVAL), (dict(codes=None), EINVAL), (dict(codes=P + 2 * SLOT + 8), EINVAL),
     (dict(scales=P + 3 * SLOT + 8), EINVAL), (dict(scales=None), EINVAL), (dict(y=None), EINVAL), (dict(y=P + 4 * SLOT + 8), EINVAL),
     (dict(y=P), EINVAL), (dict(y=P + SLOT), EINVAL), (dict(y=P + 2 * SLOT + 14 * 1024 - 16), EINVAL), (dict(y=P + 3 * SLOT), EINVAL),
@@ -308,7 +309,8 @@ def test_q4_reference_layout_by_hand():
 # ---- sampling ----
 
 @pytest.mark.parametrize("B,V,want", [(1, 1, 0), (65535, 1000, 0), (0, 10, 0), (-1, 10, EINVAL), (65536, 10, EINVAL),
-                                      (1, 0, EINVAL), (1, -5, EINVAL), (1, 1 << 31, EINVAL)])
+                                      (1, 0, EINVAL), (1, -5, EINVAL), (1, 1 << 31, EINVAL),
+                                      (1, (1 << 24) - 1, 0), (1, 1 << 24, EINVAL)])    # sums of 2^24 * 2^40 overflow
 def test_sample_workspace(B, V, want):
     st, n = K.bitlinear_sample_workspace_bytes(B, V)
     assert st == want and (st or n % 256 == 0 and (n > 0) == (B > 0))
