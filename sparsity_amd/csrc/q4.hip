@@ -8,10 +8,10 @@
 // which is 16 times its value: one shift and two masks for eight weights, and the 16 leaves with the token's
 // scale.
 //
-// A wave takes RT tiles of 16 rows and NT tiles of 16 tokens; KS waves of a block share a tile's columns when
-// the rows alone are too few waves, and add up their sums in LDS in a fixed order.  The tokens' rows lie in LDS,
-// as many columns at a time as fit.  Codes are laid out as the instruction takes them: one 16-byte load per lane
-// is 16 rows x 128 columns (the layout is in bitlinear.h).
+// Few tokens: a wave takes a tile of 16 rows and all tokens, whose rows lie in LDS, as many columns at a time as fit.
+// More: a block's waves share two LDS buffers of the tokens' rows, NT tiles of 16.  KS waves of a block share a tile's
+// columns when the rows alone are too few waves, and add up their sums in LDS in a fixed order.  Codes are laid out as
+// the instruction takes them: one 16-byte load per lane is 16 rows x 128 columns (the layout is in bitlinear.h).
 //
 // Bound by memory: half a byte per weight and 2 / group of scales, read once, as long as one block holds all
 // tokens (64).
@@ -96,7 +96,7 @@ __device__ __forceinline__ void put_rows(const Q4Args& a, int t, int64_t o, cons
   }
 }
 
-// Up to 16 tokens: few registers and little LDS, so that many waves are there to wait for memory.
+// A few tokens (16 at most): few registers and little LDS, so that many waves are there to wait for memory.
 template <int G>
 __global__ __launch_bounds__(64 * kWaves) void q4_narrow_kernel(Q4Args a) {
   constexpr int NG = 128 / G;
@@ -187,16 +187,14 @@ __global__ __launch_bounds__(64 * kWaves) void q4_narrow_kernel(Q4Args a) {
   if (busy && r < tokens) put_rows(a, r, tile * 16 + 4 * q, sum);
 }
 
-// More than 16 tokens: the same product with the tokens' rows in two LDS buffers of kWide blocks of 128 columns.  While a
+// More tokens: the same product with the tokens' rows in two LDS buffers of W blocks of 128 columns.  While a
 // buffer is multiplied, the next one is filled past the registers and the next weights are on their way; one barrier
-// and one wait per buffer.  KS waves share a tile's columns, kWide / KS blocks of a buffer each.
-constexpr int kWide = 4;
-
-template <int G, int NT, int KS>
-__global__ __launch_bounds__(64 * kWaves, 4) void q4_wide_kernel(Q4Args a) {
-  constexpr int NG = 128 / G, A = kWide / KS;
+// and one wait per buffer.  KS waves share a tile's columns, W / KS blocks of a buffer each.
+template <int G, int NT, int KS, int W>
+__global__ __launch_bounds__(64 * kWaves, W <= 4 ? 4 : 2) void q4_wide_kernel(Q4Args a) {
+  constexpr int NG = 128 / G, A = W / KS;
   constexpr int U = G == 32 ? 32 : 64;
-  constexpr int kBuffer = 16 * NT * kWide * 128;
+  constexpr int kBuffer = 16 * NT * W * 128;
   __shared__ __attribute__((aligned(16))) int8_t sm[2][kBuffer];     // [columns / U][tokens][U]
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int q = lane >> 4, r = lane & 15;
@@ -242,7 +240,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void q4_wide_kernel(Q4Args a) {
   float sum[NT][4] = {};
   fill(0, sm[0]);
   load(0);
-  for (int c0 = 0, turn = 0; c0 < a.blocks; c0 += kWide, turn ^= 1) {
+  for (int c0 = 0, turn = 0; c0 < a.blocks; c0 += W, turn ^= 1) {
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(0));            // this buffer and its weights
     v4i now[A];
     v2u now_scale[A][NG];
@@ -253,9 +251,9 @@ __global__ __launch_bounds__(64 * kWaves, 4) void q4_wide_kernel(Q4Args a) {
       for (int g = 0; g < NG; ++g) now_scale[u][g] = scale[u][g];
     }
     block_barrier_nofence();                               // and the other buffer has been read
-    if (c0 + kWide < a.blocks) {
-      fill(c0 + kWide, sm[turn ^ 1]);
-      load(c0 + kWide);
+    if (c0 + W < a.blocks) {
+      fill(c0 + W, sm[turn ^ 1]);
+      load(c0 + W);
     }
     const int8_t* x = sm[turn] + r * U + U / 4 * q;
 #pragma unroll
@@ -319,12 +317,12 @@ __global__ __launch_bounds__(64 * kWaves, 4) void q4_wide_kernel(Q4Args a) {
   }
 }
 
-template <int G, int NT, int KS>
+template <int G, int NT, int KS, int W>
 hipError_t wide(Q4Args a, hipStream_t s) {
   constexpr int per = kWaves / KS;
   const int64_t row_blocks = (a.tiles + per - 1) / per;
   const int64_t grid = (row_blocks + 7) / 8 * 8 * a.token_tiles;
-  q4_wide_kernel<G, NT, KS><<<(unsigned)grid, 64 * kWaves, 0, s>>>(a);
+  q4_wide_kernel<G, NT, KS, W><<<(unsigned)grid, 64 * kWaves, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -334,9 +332,10 @@ hipError_t narrow(Q4Args a, hipStream_t s) {
   const int most = kLds / a.T / 128 * 128;
   const int chunks = (a.blocks * 128 + most - 1) / most;
   a.chunk = (a.blocks + chunks - 1) / chunks * 128;
-  // waves on one tile's columns: until there are two waves per SIMD, or no columns to share
+  // Waves on one tile's columns: as many as leave all waves there at once.  One token, by 1, 2, 4 and 8 waves to a tile:
+  // 32000 x 2560 16.9, 11.9, 10.0 and 12.8 us, 16384 x 4096 -, 13.6, 9.9 and 9.0, 70001 x 2560 21.2 and 23.0.
   a.ksplit = 1;
-  while (a.ksplit < kWaves && a.tiles * a.ksplit < 8192 && a.ksplit * 2 <= a.chunk / 128) a.ksplit *= 2;
+  while (a.ksplit < kWaves && a.tiles * a.ksplit * 2 <= 8192 && a.ksplit * 2 <= a.chunk / 128) a.ksplit *= 2;
   const int64_t per = kWaves / a.ksplit;
   size_t lds = (size_t)a.T * a.chunk;
   if (a.ksplit > 1) lds = std::max(lds, (size_t)kWaves * 1024);
@@ -344,19 +343,43 @@ hipError_t narrow(Q4Args a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// How many waves share a tile's columns: a block's time is about 1 / KS of its columns, and there are KS times as many
+// blocks.  The CU that gets the most of them is done last, one block alone is not faster than two, and each doubling costs
+// a tenth or more, for the tokens' rows that each block reads.  16 tokens by 1, 2, 4 and 8 waves: 2560 x 6912 26.5, 17.4,
+// 14.1 and 8.7 us, 32000 x 2560 13.9, 11.5, 12.1 and 15.3, 50000 x 2560 17.3, 19.0, 17.4 and 22.3, 100003 x 4096 47.5,
+// 43.2, 47.8 and 57; 64 tokens: 2560 x 6912 37, 25, 19.5 and 15.8, 16384 x 4096 28.5, 20.1, 19.8 and 41, 131072 x 2560 64,
+// 73, 103 and 223.  In groups of 32 one wave's sums and weights are more registers than there are.
 template <int G, int NT>
 hipError_t wide_split(Q4Args a, hipStream_t s) {
   a.token_tiles = (a.T + 16 * NT - 1) / (16 * NT);
-  const int64_t waves = a.tiles * a.token_tiles;
-  if (G > 32 && (waves >= 2048 || a.blocks < 2)) return wide<G, NT, 1>(a, s);
-  if (waves >= 1024 || a.blocks < 4) return wide<G, NT, 2>(a, s);
-  return wide<G, NT, 4>(a, s);
+  int ks = 0;
+  double least = 0.0, tax = 1.0;
+  for (int k = 1; k <= 8; k *= 2, tax *= NT == 1 ? 1.1 : 1.15) {
+    if (ks && k > a.blocks) break;
+    if (k == 1 && G == 32) continue;
+    const int64_t blocks = (a.tiles * k + kWaves - 1) / kWaves * a.token_tiles;
+    const double cost = (double)std::max<int64_t>((blocks + 255) / 256, 2) / k * tax;
+    if (!ks || cost < least) {
+      ks = k;
+      least = cost;
+    }
+  }
+  if constexpr (G > 32)
+    if (ks == 1) return wide<G, NT, 1, 4>(a, s);
+  if (ks == 2) return wide<G, NT, 2, 4>(a, s);
+  if (ks == 4) return wide<G, NT, 4, 4>(a, s);
+  return wide<G, NT, 8, 8>(a, s);
 }
 
+// Which kernel, in us: up to 4 tokens the narrow one (131072 x 2560, one token: 30.1, 33.0 by the other; 2560 x 6912 7.2
+// and 8.6), above it the other (16 tokens of 100003 x 4096 48.1 and 43.2, 32000 x 2560 14.6 and 11.5), for as many tiles
+// of 16 tokens as there are (32 of 131072 x 2560: 45 by two, 55 by four; 48: 53 by three, 59 by four).
 template <int G>
 hipError_t fwd(const Q4Args& a, hipStream_t s) {
-  if (a.T <= 16) return narrow<G>(a, s);
-  return a.T <= 32 ? wide_split<G, 2>(a, s) : wide_split<G, 4>(a, s);
+  if (a.T <= 4) return narrow<G>(a, s);
+  if (a.T <= 16) return wide_split<G, 1>(a, s);
+  if (a.T <= 32) return wide_split<G, 2>(a, s);
+  return a.T <= 48 ? wide_split<G, 3>(a, s) : wide_split<G, 4>(a, s);
 }
 
 }  // namespace

@@ -95,7 +95,7 @@ def _check(y, xq, xs, q, s, group):
     assert np.all(err <= bound), (err / (bound + 1e-300)).max()
 
 
-@pytest.mark.parametrize("T", [1, 2, 4, 15, 16, 17, 31, 33, 64, 65, 130, 200])
+@pytest.mark.parametrize("T", [1, 2, 4, 5, 15, 16, 17, 31, 33, 48, 49, 64, 65, 130, 200])
 @pytest.mark.parametrize("n,K,group", [(1, 32, 32), (15, 96, 32), (48, 128, 128), (100, 640, 64), (257, 1280, 32),
                                        (1000, 2560, 64), (513, 6912, 128), (130, 192, 64)])
 def test_products(T, n, K, group):
@@ -107,9 +107,11 @@ def test_products(T, n, K, group):
 
 
 @pytest.mark.parametrize("T,n,K,group", [(1, 40000, 256, 64), (3, 33333, 512, 128), (40, 70001, 128, 32), (64, 8200, 4224, 64),
-                                         (9, 50, 65536, 128), (64, 50, 16384, 32), (1, 17000, 4096, 32)])
+                                         (9, 50, 65536, 128), (64, 50, 16384, 32), (1, 17000, 4096, 32),
+                                         (16, 8208, 1024, 64), (5, 33000, 256, 64), (30, 20000, 640, 32),
+                                         (48, 17000, 512, 128), (48, 9000, 1152, 32), (20, 33000, 384, 128)])
 def test_products_of_many_rows_or_columns(T, n, K, group):
-    """One wave per tile, several parts of K in LDS, spare tiles at the end."""
+    """One, two, four and eight waves per tile, several parts of K in LDS, spare tiles at the end."""
     xq, xs, q, s, codes, scales = _case(rng(n + K), T, n, K, group)
     _check(host(S.q4_fwd(dev(xq), dev(xs), K, codes, scales, n, group)), xq, xs, q, s, group)
 
