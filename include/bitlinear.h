@@ -689,7 +689,7 @@ int bitlinear_paged_attn(const bl_attn_plan* plan, const void* q, int q_dtype, i
  * overlap another buffer (BL_EINVAL).  Lengths below 0 count as 0, a free_count outside [0, free_cap]
  * as the nearest of them; tables and the stack must hold page numbers of the caller's cache, which are
  * moved and multiplied, never dereferenced.  0 <= B <= 2^20, T < 2^22, page_size >= 1, B * blocks_per_seq
- * < 2^40.  One launch, two above 4096 rows. */
+ * < 2^40.  One launch, two above 8192 rows. */
 int bitlinear_kv_step(const int32_t* cached, const int32_t* fresh, int64_t B, int32_t* blocks,
                       int64_t blocks_per_seq, int64_t page_size, int32_t* free_pages,
                       int64_t free_cap, const int32_t* free_count, int32_t* free_count_out, int64_t T,
@@ -709,7 +709,7 @@ int bitlinear_embed(const void* table, int table_dtype, int64_t V, int64_t K, co
  * ws: bitlinear_embed_bwd_workspace_bytes of device scratch (256-byte aligned; contents on entry
  * irrelevant); calls that share one must be ordered, on one stream or by events.  dtable and ws may overlap
  * nothing.  T == 0 writes zeros (or, accumulating, nothing).
- * Two to four launches. */
+ * Two to five launches. */
 #define BL_EMBED_ACCUM 1
 int bitlinear_embed_bwd_workspace_bytes(int64_t T, int64_t K, size_t* ws_bytes);
 int bitlinear_embed_bwd(const void* dy, int dy_dtype, const int32_t* ids, int64_t T, int64_t V,

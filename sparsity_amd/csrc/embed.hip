@@ -10,7 +10,7 @@
 // atomics.  Launches:
 //   sort   blocks sort a chunk of tokens each, in registers and LDS
 //   rank   (several chunks) an element's place is its place in its chunk plus, by bisection, what the
-//          other chunks hold before it
+//          other chunks of its span of 65536 tokens hold before it; where there are several spans, once more
 //   sum    a wave takes 16 sorted positions and 512 columns; it sums every run that starts there, up to
 //          32 positions of it, and writes the row; of a longer run, what lies inside its 16 goes to the
 //          workspace.  Where the gradient is overwritten, the other blocks of the launch clear the rows that
@@ -68,12 +68,14 @@ constexpr uint32_t kNone = 0xFFFFFFFFu;      // an id outside the table: sorted 
 constexpr int kChunk = kEmbedChunk;
 constexpr int kSortThreads = kChunk / 2;
 constexpr int kFillRows = 8;                 // rows that a wave of a fill block looks up
-// Bytes of the gradient that are cleared beside the sort, whose few blocks leave most of the chip idle for 9 us.
-constexpr int64_t kFillSort = 40 << 20;
+// Bytes of the gradient that are cleared beside the sort, whose few blocks leave most of the chip idle.  Whole calls with
+// none, 40, 80 and 160 MB: 8192 tokens of 3200 onto 32000 rows 112, 107, 102 and 104 us, 64 of 2560 67, 64, 62 and 65,
+// 32749 of 2560 onto 131072 rows 335, 332, 329 and 332.
+constexpr int64_t kFillSort = 80 << 20;
 constexpr unsigned kFillBlocks = 512;
 
 struct Sorted {                              // the workspace's arrays
-  uint32_t *chunk_id, *chunk_tok, *id, *tok;
+  uint32_t *chunk_id, *chunk_tok, *span_id, *span_tok, *id, *tok;
   uint32_t* runs;                            // [0]: number of long runs; then {first position, id} each
   float* part;
   int32_t chunks;
@@ -154,7 +156,7 @@ __global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(EmbedBwdArgs a
   }
 }
 
-// Places of the sorted chunks' elements among all of them: chunks before count what is not above, the
+// Places of the sorted chunks' elements among those of their span: chunks before count what is not above, the
 // ones behind what is below, so equal ids stay in the order of their tokens.  The chunks' ids are searched in
 // LDS, four chunks at a time.
 constexpr int kRankChunks = 16;              // in LDS at a time
@@ -164,9 +166,10 @@ __global__ __launch_bounds__(kRankThreads) void embed_rank_kernel(int64_t T, Sor
   const int64_t e = (int64_t)blockIdx.x * kRankThreads + threadIdx.x;
   const int mine = (int)(e / kChunk);
   const uint32_t id = s.chunk_id[e], tok = s.chunk_tok[e];
-  int64_t place = e - (int64_t)mine * kChunk;
-  for (int c0 = 0; c0 < s.chunks; c0 += kRankChunks) {
-    const int n = min(kRankChunks, s.chunks - c0);
+  const int first = mine / kEmbedSpan * kEmbedSpan, end = min(first + kEmbedSpan, s.chunks);
+  int64_t place = e - (int64_t)(mine - first) * kChunk;
+  for (int c0 = first; c0 < end; c0 += kRankChunks) {
+    const int n = min(kRankChunks, end - c0);
     __syncthreads();
     for (int i = threadIdx.x; i < n * kChunk / 4; i += kRankThreads)
       ((uint4*)k)[i] = ((const uint4*)s.chunk_id)[(int64_t)c0 * (kChunk / 4) + i];
@@ -192,9 +195,39 @@ __global__ __launch_bounds__(kRankThreads) void embed_rank_kernel(int64_t T, Sor
     }
   }
   if (tok < T) {
-    s.id[place] = id;
-    s.tok[place] = tok;
+    s.span_id[place] = id;
+    s.span_tok[place] = tok;
   }
+}
+
+// The same of the spans' elements, among all: four spans at a time, from the L2.  Without spans the time of the ranks
+// grows with the square of the tokens: 2^20 tokens 3.2 ms and 2^22 45 ms, of 64 columns.
+__global__ __launch_bounds__(256) void embed_spans_kernel(int64_t T, Sorted s) {
+  constexpr int kSpan = kEmbedSpan * kChunk;
+  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (e >= T) return;
+  const int mine = (int)(e / kSpan), spans = (int)((T + kSpan - 1) / kSpan);
+  const uint32_t id = s.span_id[e];
+  int64_t place = e - (int64_t)mine * kSpan;
+  for (int c = 0; c < spans; c += 4) {
+    int at[4] = {}, n[4];
+    uint64_t bar[4];
+    const uint32_t* in[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int span = min(c + j, spans - 1);
+      bar[j] = (uint64_t)id + (span < mine);
+      in[j] = s.span_id + (int64_t)span * kSpan;
+      n[j] = c + j < spans && span != mine ? (int)min(T - (int64_t)span * kSpan, (int64_t)kSpan) : 0;
+    }
+    for (int d = kSpan; d > 0; d >>= 1)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) at[j] += at[j] + d <= n[j] && in[j][at[j] + d - 1] < bar[j] ? d : 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) place += at[j];
+  }
+  s.id[place] = id;
+  s.tok[place] = s.span_tok[e];
 }
 
 // Rows of a fill block: a few waves' where they are short.
@@ -402,6 +435,8 @@ hipError_t launch_embed_bwd(const EmbedBwdArgs& a, bool dy_bf16, hipStream_t s) 
   Sorted so;
   so.chunk_id = (uint32_t*)(a.ws + w.chunk_id);
   so.chunk_tok = (uint32_t*)(a.ws + w.chunk_tok);
+  so.span_id = (uint32_t*)(a.ws + w.span_id);
+  so.span_tok = (uint32_t*)(a.ws + w.span_tok);
   so.id = (uint32_t*)(a.ws + w.id);
   so.tok = (uint32_t*)(a.ws + w.tok);
   so.runs = (uint32_t*)(a.ws + w.runs);
@@ -418,6 +453,10 @@ hipError_t launch_embed_bwd(const EmbedBwdArgs& a, bool dy_bf16, hipStream_t s) 
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if (w.chunks > 1) {
       embed_rank_kernel<<<(unsigned)w.chunks * (kChunk / kRankThreads), kRankThreads, 0, s>>>(a.T, so);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    if (w.chunks > kEmbedSpan) {
+      embed_spans_kernel<<<(unsigned)((a.T + 255) / 256), 256, 0, s>>>(a.T, so);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
   }

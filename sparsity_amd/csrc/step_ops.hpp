@@ -42,17 +42,19 @@ hipError_t launch_embed(const EmbedArgs& a, bool table_bf16, bool y_bf16, hipStr
 
 // Workspace of the gradient, segments 256-byte aligned:
 //   chunk_id, chunk_tok  [chunks * kEmbedChunk] ids of a chunk of tokens in order, and their tokens
-//   id, tok              [T] the same of all tokens (one chunk: the two are one)
+//   span_id, span_tok    [T] the same of spans of chunks
+//   id, tok              the same of all tokens: what the last of the steps that there are wrote
 //   runs                 [1 + 2 * (T / kEmbedLong + 1)] long runs: their number, then first position and id
 //   part                 [tiles][2][K] sums of the pieces of long runs
 constexpr int kEmbedChunkBits = 11;
 constexpr int kEmbedChunk = 1 << kEmbedChunkBits;   // tokens that a block sorts
+constexpr int kEmbedSpan = 32;      // chunks
 constexpr int kEmbedTile = 16;      // sorted positions a wave takes
 constexpr int kEmbedLong = 32;      // a run of more positions is summed in pieces
 
 struct EmbedBwdWs {
   int64_t chunks, tiles;
-  size_t chunk_id, chunk_tok, id, tok, runs, part, total;
+  size_t chunk_id, chunk_tok, span_id, span_tok, id, tok, runs, part, total;
 };
 inline EmbedBwdWs embed_bwd_ws(int64_t T, int64_t K) {
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
@@ -65,8 +67,11 @@ inline EmbedBwdWs embed_bwd_ws(int64_t T, int64_t K) {
   w.chunk_tok = off; off += all;
   w.id = w.chunk_id; w.tok = w.chunk_tok;
   if (w.chunks > 1) {
-    w.id = off; off += up((size_t)T * 4);
-    w.tok = off; off += up((size_t)T * 4);
+    w.span_id = off; off += up((size_t)T * 4);
+    w.span_tok = off; off += up((size_t)T * 4);
+    if (w.chunks <= kEmbedSpan) {              // else from the spans' back into the chunks'
+      w.id = w.span_id; w.tok = w.span_tok;
+    }
   }
   w.runs = off; off += up((size_t)(1 + 2 * (T / kEmbedLong + 1)) * 4);
   w.part = off;

@@ -131,9 +131,11 @@ def test_gradient_of_runs_of_every_kind(T, dd, accum):
 
 
 @pytest.mark.parametrize("T,V,K,kind", [(16384, 31, 64, "zipf"), (16385, 5000, 64, "padded"), (40000, 3, 8, "even"),
-                                        (100003, 20000, 16, "zipf")])
+                                        (100003, 20000, 16, "zipf"), (65536, 900, 8, "padded"), (65537, 70, 8, "zipf"),
+                                        (131073, 5, 8, "padded"), (200001, 100000, 8, "even"),
+                                        (400000, 1 << 21, 8, "padded")])
 def test_gradient_of_many_tokens(T, V, K, kind):
-    """Around the change of the chunks' size, and rows of ten thousand tokens."""
+    """One span of chunks and several, and rows of ten thousand tokens."""
     _grad_check(rng(T), T, V, K, "bf16", kind)
 
 

@@ -69,7 +69,7 @@ def test_steps(B, page, per, most, T, in_place):
 
 
 @pytest.mark.parametrize("B,page,per,most,T,short", [
-    (10, 4, 6, 9, 100, 0), (10, 4, 6, 9, 100, 5), (300, 4, 6, 9, 5000, 100), (1300, 4, 3, 5, 6000, 700),
+    (10, 4, 6, 9, 100, 0), (10, 4, 6, 9, 100, 5), (300, 4, 6, 9, 5000, 100), (1300, 4, 3, 5, 6000, 700), (1300, 4, 6, 9, 9000, 700),
     (200, 8, 8, 40, 1000, None), (50, 1, 8, 8, 10, None)])
 def test_pages_or_rows_that_do_not_suffice(B, page, per, most, T, short):
     """Pages run out, or the token rows do; requests that need no new page are still served."""
@@ -125,9 +125,10 @@ def test_large_page_numbers():
 def test_steps_without_slots():
     _check(*_state(rng(5), 33, 4, 6, 5, ended=0.1), 4, 100, slot=False)
     _check(*_state(rng(6), 33, 4, 60, 200, ended=0.1), 4, 5000, slot=False)
+    _check(*_state(rng(7), 33, 4, 60, 200, ended=0.1), 4, 9000, slot=False)
 
 
-@pytest.mark.parametrize("T", [40, 5000])
+@pytest.mark.parametrize("T", [40, 5000, 9000])
 def test_steps_in_a_row_as_a_graph(T):
     """A captured step in place, replayed: lengths, tables and the stack move on as in eager steps."""
     import torch
