@@ -8,14 +8,22 @@
 //   token = the first one at which the running sum passes floor(u * S)
 // Every question about the order (where does the k-th weight end, where does a running sum pass a goal) needs
 // the sums up to a bin of close values, and the order inside one bin alone:
-//   max    blocks find largest and least logit of a chunk of a row
-//   hist   blocks count a chunk's tokens and sum their weights by bins of (x - top) / temperature
-//   pick   one block per row adds the chunks' bins up and answers the questions.  The tokens of the bins it needs
-//          are gathered into LDS: where those up to the last bin in question are kList at most (top-k and top-p as
-//          they are used), once for all questions, from the groups of 64 logits that hold any.  There the bin
-//          in question is split further by place (value, then index) until a wave can sort what is left.  A bin
-//          of more than kList tokens is split by passes over the row first.
-// Weights take an exp in fp64; 2^-41 of the largest and less are zero and leave early.
+//   max    blocks find largest and least logit of a chunk of a row, and the largest of each 64
+//   hist   blocks count a chunk's tokens and sum their weights by 1024 bins of top - x.  The last block of a row adds the
+//          chunks' bins up, finds the bins that the questions' answers lie in, and plans which tokens to gather: where
+//          those up to the first question's bin are kList at most (top-k and top-p as they are used) all of them, once
+//          for all questions, else those of each question's bin or few bins
+//   draw   tokens are gathered by one block, from the groups of 64 whose largest reaches them, or by all blocks from all
+//          logits, for the last of them.  The one that has them answers the questions: a bin by its fine bins, until a
+//          wave can sort what is left.  If more than kList tokens are planned for (equal logits above all), one block
+//          reads the row and splits bins by place (value, then index)
+// Largest and least logit bound the bins (what weighs nothing aside), so that they are as fine as the row allows: 1024
+// leave 420 tokens in the fullest of 131072 normal logits, and a plan is below kList but for odd rows; with 512 one in a
+// thousand was above it, and its call took 150 us in place of 54.
+//
+// Latency bounds one row: 131072 logits take 3.8, 13 and 9 us in the three launches, each a chain of dependent loads, a
+// hand-over between blocks (past the caches, that the XCDs do not share) and steps in LDS.  64 rows of mixed settings take
+// 8.4 (4 TB/s), 22 and 26 us: 28 vector instructions a weight, and rows that wait for their last block.
 #include <algorithm>
 
 #include "block_ops.hpp"
@@ -30,11 +38,12 @@ namespace {
 typedef unsigned long long u64;
 
 constexpr int kBins = kSampleBins;
+constexpr int kParts = 512;              // fine bins of a bin, and parts that one is split into otherwise
 constexpr int kList = kSampleList;       // tokens that are gathered
 constexpr int kThreads = 512;            // of every block
 constexpr int kWaves = kThreads / 64;
 constexpr int kStep = kThreads * 8;      // logits that a block loads at a time
-static_assert(kThreads == kBins, "a thread per bin");
+static_assert(2 * kThreads == kBins && kThreads == kParts, "two bins, and one part, to a thread");
 constexpr double kOne = 1099511627776.0; // 2^40, the weight of the largest logit
 
 struct Row {                             // what is known of a row once its largest logit is
@@ -89,12 +98,16 @@ __device__ __forceinline__ void finish8(const void* row, int64_t i, int64_t V, f
       v[j] = BF ? __uint_as_float((uint32_t)((const uint16_t*)row)[i + j] << 16) : ((const float*)row)[i + j];
   }
 }
-// The same with -inf for NaN.
-template <bool BF, bool VEC>
-__device__ __forceinline__ void finish8_masked(const void* row, int64_t i, int64_t V, float v[8]) {
-  finish8<BF, VEC>(row, i, V, v);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = v[j] == v[j] ? v[j] : kNegInf;
+// The largest and least of three numbers, none of them NaN: one instruction, where fmaxf quiets its operands first.
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float m;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(m) : "v"(x), "v"(y), "v"(z));
+  return m;
+}
+__device__ __forceinline__ float min3(float x, float y, float z) {
+  float m;
+  asm("v_min3_f32 %0, %1, %2, %3" : "=v"(m) : "v"(x), "v"(y), "v"(z));
+  return m;
 }
 template <bool BF>
 __device__ __forceinline__ const void* row_of(const SampleArgs& a, int64_t b) {
@@ -106,33 +119,36 @@ __device__ __forceinline__ double scaled(const Row& r, float x) {
   if (r.inf) return x == (float)r.top ? 0.0 : -__builtin_inf();
   return x == kNegInf ? -__builtin_inf() : ((double)x - r.top) * r.c;
 }
-// The logit's place among kBins^2 fine bins of the row's range, kBins of them to a bin: any steps that rise as x falls
+// The logit's place among the fine bins of the row's range, kParts of them to a bin: any steps that rise as x falls
 // will do, so fp32 is enough.  NaN (equals of an infinite top) counts as 0.
 __device__ __forceinline__ int fine_of(const Row& r, float x) {
-  return (int)__builtin_amdgcn_fmed3f(((float)r.top - x) * r.per_fine, 0.f, (float)(kBins * kBins - 1));
+  return (int)__builtin_amdgcn_fmed3f(((float)r.top - x) * r.per_fine, 0.f, (float)(kBins * kParts - 1));
 }
 
+// a * b + c in fp64 with c from scalar registers: a multiply-add that ends where c was would copy it there first.
+__device__ __forceinline__ double fma_const(double a, double b, double c) {
+  double d;
+  asm("v_fma_f64 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "s"(c));
+  return d;
+}
 // 2^40 * 2^t rounded to a whole number, t <= 0 (NaN: 0).  2^f for |f| <= 1/2 is a polynomial through the eleven
 // Chebyshev points, 2.4e-16 off at most, its coefficients times 2^40.  Adding 1.5 * 2^52 rounds to a whole number, half
-// to even, in a double's low bits; 2^n goes straight into the exponent.
+// to even, in a double's low bits.
 __device__ __forceinline__ u64 weight(double t) {
   const double magic = 6755399441055744.0;
   t = __builtin_fmax(t, -60.0);
   const double m = t + magic, f = t - (m - magic);
-  double p = 0x1.e6063f7217bc6p+12;
-  p = __builtin_fma(p, f, 0x1.b675bca4eeebbp+16);
-  p = __builtin_fma(p, f, 0x1.62bfd47773353p+20);
-  p = __builtin_fma(p, f, 0x1.ffcb54062e698p+23);
-  p = __builtin_fma(p, f, 0x1.430913096fd9fp+27);
-  p = __builtin_fma(p, f, 0x1.5d87fe9d7a584p+30);
-  p = __builtin_fma(p, f, 0x1.3b2ab6fba1ddap+33);
-  p = __builtin_fma(p, f, 0x1.c6b08d703ce49p+35);
-  p = __builtin_fma(p, f, 0x1.ebfbdff82c598p+37);
-  p = __builtin_fma(p, f, 0x1.62e42fefa3a19p+39);
-  p = __builtin_fma(p, f, 0x1.0p+40);
-  uint2 bits = __builtin_bit_cast(uint2, p);
-  bits.y += __builtin_bit_cast(uint2, m).x << 20;
-  bits = __builtin_bit_cast(uint2, __builtin_bit_cast(double, bits) + magic);
+  double p = fma_const(f, 0x1.e6063f7217bc6p+12, 0x1.b675bca4eeebbp+16);
+  p = fma_const(p, f, 0x1.62bfd47773353p+20);
+  p = fma_const(p, f, 0x1.ffcb54062e698p+23);
+  p = fma_const(p, f, 0x1.430913096fd9fp+27);
+  p = fma_const(p, f, 0x1.5d87fe9d7a584p+30);
+  p = fma_const(p, f, 0x1.3b2ab6fba1ddap+33);
+  p = fma_const(p, f, 0x1.c6b08d703ce49p+35);
+  p = fma_const(p, f, 0x1.ebfbdff82c598p+37);
+  p = fma_const(p, f, 0x1.62e42fefa3a19p+39);
+  p = fma_const(p, f, 0x1.0p+40);
+  const uint2 bits = __builtin_bit_cast(uint2, __builtin_ldexp(p, (int)__builtin_bit_cast(uint2, m).x) + magic);
   return (u64)(bits.y & 0x7FFFFu) << 32 | bits.x;
 }
 __device__ __forceinline__ u64 weight_of(const Row& r, float x) { return weight(scaled(r, x)); }
@@ -176,7 +192,7 @@ __device__ __forceinline__ Row row_of_extremes(const Extremes& e, const Settings
   r.inf = x == __builtin_inff();
   r.c = 1.4426950408889634 / s.temp;
   // over what weighs anything, or what there is; too narrow to be told apart: one bin
-  const float per_fine = (float)(kBins * kBins / fmin((double)x - least, 41.0 / r.c));
+  const float per_fine = (float)(kBins * kParts / fmin((double)x - least, 41.0 / r.c));
   r.per_fine = per_fine < 1e30f && !r.inf ? per_fine : 0.f;
   return r;
 }
@@ -203,18 +219,19 @@ __device__ __forceinline__ bool met(const Asked& a, const Pair& p) {
 }
 __device__ __forceinline__ Pair operator+(const Pair& a, const Pair& b) { return {a.w + b.w, a.n + b.n}; }
 
-// First bin whose running sums, behind `before`, answer the question (the last one that adds anything, if none
-// does).  Every wave finds it by itself: 64 ends of eight bins, then the eight.
+// First of N bins whose running sums, behind `before`, answer the question (the last one that adds anything, if none
+// does).  Every wave finds it by itself: 64 ends of a few bins, then the few.
+template <int N>
 __device__ __forceinline__ int first_bin(const Asked& q, const Pair* bins, const Pair& before) {
-  static_assert(kBins == 512, "64 eights");
+  constexpr int kFew = N / 64;
   const int lane = threadIdx.x & 63;
-  const u64 all = bins[kBins - 1].n;
+  const u64 all = bins[N - 1].n;
   auto yes = [&](int i) {
     const Pair p = bins[i];
     return __ballot(met(q, before + p) || p.n == all);       // rising: once it is so it stays so
   };
-  const int eight = __ffsll((unsigned long long)yes(lane * 8 + 7)) - 1;
-  return eight * 8 + __ffsll((unsigned long long)yes(eight * 8 + (lane & 7))) - 1;
+  const int few = __ffsll((unsigned long long)yes(lane * kFew + kFew - 1)) - 1;
+  return few * kFew + __ffsll((unsigned long long)yes(few * kFew + lane % kFew)) - 1;
 }
 
 // A token's place in the order: its logit as a falling number, then its index.
@@ -233,7 +250,7 @@ __device__ __forceinline__ u64 key_end(const Row& r, int bin) {
   while (hi - lo > 1) {
     const uint64_t step = (hi - lo + 63) >> 6, at = lo + lane * step;
     const float x = from_falling((uint32_t)at);
-    const uint64_t mask = __ballot(at < hi && x == x && weight_of(r, x) > 0 && fine_of(r, x) / kBins <= bin);
+    const uint64_t mask = __ballot(at < hi && x == x && weight_of(r, x) > 0 && fine_of(r, x) / kParts <= bin);
     const int last = 63 - __clzll((long long)mask);
     hi = min(hi, lo + (last + 1) * step);
     lo += last * step;
@@ -262,12 +279,15 @@ __global__ __launch_bounds__(kThreads) void sample_max_kernel(SampleArgs a) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       if (at + k * kStep >= i1) break;
-      finish8_masked<BF, VEC>(row, i + k * kStep, a.V, v[k]);
+      finish8<BF, VEC>(row, i + k * kStep, a.V, v[k]);
       float most = kNegInf;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        least = fminf(least, v[k][j] == kNegInf ? __builtin_inff() : v[k][j]);
-        most = fmaxf(most, v[k][j]);
+      for (int j = 0; j < 8; j += 2) {
+        const bool is0 = v[k][j] > kNegInf, is1 = v[k][j + 1] > kNegInf;   // neither -inf nor NaN
+        least = min3(least, is0 ? v[k][j] : __builtin_inff(), is1 ? v[k][j + 1] : __builtin_inff());
+        v[k][j] = is0 ? v[k][j] : kNegInf;
+        v[k][j + 1] = is1 ? v[k][j + 1] : kNegInf;
+        most = max3(most, v[k][j], v[k][j + 1]);
       }
       if (falling(most) < (uint32_t)(top >> 32)) {           // the first of its equals
         int j = 7;
@@ -335,15 +355,15 @@ __device__ __forceinline__ void make_plan(SamplePlan* plan, const Settings& st, 
   u64 lo = all.w, hi = all.w;                                // of the sum that is left
   int b0[3], b1[3], n = 0;
   if (k) {
-    const int bin = first_bin({kCount, k, 0.0, 0}, bins, none);
+    const int bin = first_bin<kBins>({kCount, k, 0.0, 0}, bins, none);
     lo = upto(bin - 1).w;
     hi = upto(bin).w;
     b0[0] = b1[0] = bin;
     n = 1;
   }
   if (st.p < 1.0 && !(n && upto(b1[0]).n <= kList)) {
-    const int bin0 = first_bin({kGoal, 0, st.p * (double)lo, 0}, bins, none);
-    const int bin1 = first_bin({kGoal, 0, st.p * (double)hi, 0}, bins, none);
+    const int bin0 = first_bin<kBins>({kGoal, 0, st.p * (double)lo, 0}, bins, none);
+    const int bin1 = first_bin<kBins>({kGoal, 0, st.p * (double)hi, 0}, bins, none);
     lo = min(lo, upto(bin0 - 1).w);
     hi = min(hi, upto(bin1).w);
     b0[n] = bin0;
@@ -359,8 +379,8 @@ __device__ __forceinline__ void make_plan(SamplePlan* plan, const Settings& st, 
     n = 1;
   } else {
     const double part = u > 0.0 ? fmin(u, 1.0) : 0.0;
-    b0[n] = first_bin({kPass, 0, 0.0, min((u64)(part * (double)lo), max(lo, (u64)1) - 1)}, bins, none);
-    b1[n++] = first_bin({kPass, 0, 0.0, min((u64)(part * (double)hi), hi - 1)}, bins, none);
+    b0[n] = first_bin<kBins>({kPass, 0, 0.0, min((u64)(part * (double)lo), max(lo, (u64)1) - 1)}, bins, none);
+    b1[n++] = first_bin<kBins>({kPass, 0, 0.0, min((u64)(part * (double)hi), hi - 1)}, bins, none);
   }
   const int last = b1[0];
   // one that meets the one before it joins it
@@ -403,8 +423,11 @@ __device__ __forceinline__ Pair scan(Pair v, Pair* waves) {
 
 template <bool BF, bool VEC>
 __global__ __launch_bounds__(kThreads) void sample_hist_kernel(SampleArgs a) {
-  __shared__ u64 w_bin[kBins];
-  __shared__ uint32_t n_bin[kBins];
+  // Bins of what two waves add in a turn: a sum of weights and, from bit 52 on, their number, in one addition.  2048 weights
+  // of at most 2^40 stay below.
+  constexpr int kTables = kWaves / 2, kCountAt = 52;
+  static_assert(2 * kStep / kTables <= 1 << 11 && 2 * kStep == 8192, "a turn's sums and numbers fit");
+  __shared__ __attribute__((aligned(16))) u64 tables[kTables][kBins];
   __shared__ Pair bins[kBins], waves[kWaves];
   __shared__ double s_exp[kWaves];
   __shared__ u64 s_min[kWaves];
@@ -417,50 +440,71 @@ __global__ __launch_bounds__(kThreads) void sample_hist_kernel(SampleArgs a) {
   const Row r = row_of_extremes(row_extremes(a, b), st, &best);
   if (st.greedy && !a.logprob) return;
   if (r.top == -__builtin_inf()) return;                   // nothing to draw from
-  w_bin[tid] = 0;
-  n_bin[tid] = 0;
+#pragma unroll
+  for (int t = 0; t < kTables; ++t) *(ulonglong2*)(tables[t] + 2 * tid) = make_ulonglong2(0, 0);
   __syncthreads();
   const void* row = row_of<BF>(a, b);
   const int64_t i0 = (int64_t)blockIdx.x * a.chunk, i1 = min(i0 + a.chunk, a.V);
-  const float top = (float)r.top, per_bin = r.per_fine / kBins;
+  const double dtop = r.inf ? 0.0 : r.top;
+  const float top = (float)dtop, per_bin = r.per_fine / kParts;
   double e = 0.0;                                          // sum of exp(x - top)
   u64 least_sum = 0;                                       // of the weights that min_p keeps
-  for (int64_t at = i0; at < i1; at += 2 * kStep) {
+  u64* const table = tables[tid / 128];
+  Pair mine[2] = {};                                       // of bins 2 tid and the next
+  float next[8];
+  load8_raw<BF, VEC>(row, i0 + tid * 8, a.V, next);
+  int turn = 1;
+  for (int64_t at = i0; at < i1; at += kStep, turn ^= 1) {
     const int64_t i = at + tid * 8;
-    float v[2][8];
+    float v[8];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) load8_raw<BF, VEC>(row, i + k * kStep, a.V, v[k]);
+    for (int j = 0; j < 8; ++j) v[j] = next[j];
+    load8_raw<BF, VEC>(row, i + kStep, a.V, next);         // of the next turn; past the chunk they are not used
+    finish8<BF, VEC>(row, i, a.V, v);
+    if (r.inf) {                                           // its equals as 0 below a largest of 0
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (at + k * kStep >= i1) break;
-      finish8<BF, VEC>(row, i + k * kStep, a.V, v[k]);
-      float d[8];
+      for (int j = 0; j < 8; ++j) v[j] = v[j] == __builtin_inff() ? 0.f : kNegInf;
+    }
+    float d[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) d[j] = top - v[k][j];
-      if (a.logprob) {
-        // eight at a time in fp32, unless one of them is 1, next to which small ones were lost, or NaN
-        float some = 0.f;
+    for (int j = 0; j < 8; ++j) d[j] = top - v[j];
+    if (a.logprob) {
+      // eight at a time in fp32, unless one of them is 1, next to which small ones were lost, or NaN
+      float some = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) some += __builtin_amdgcn_exp2f(d[j] * -1.44269504f);
-        if (some < 1.f) {
-          e += some;
-        } else {
+      for (int j = 0; j < 8; ++j) some += __builtin_amdgcn_exp2f(d[j] * -1.44269504f);
+      if (some < 1.f) {
+        e += some;
+      } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            e += v[k][j] == top ? 1.0 : d[j] > 0.f && !r.inf ? (double)__builtin_amdgcn_exp2f(d[j] * -1.44269504f) : 0.0;
-        }
+        for (int j = 0; j < 8; ++j)
+          e += v[j] == top ? 1.0 : d[j] > 0.f ? (double)__builtin_amdgcn_exp2f(d[j] * -1.44269504f) : 0.0;
       }
-      if (st.greedy) continue;
+    }
+    if (st.greedy) continue;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const u64 w = r.inf ? weight_of(r, v[k][j]) : weight(((double)v[k][j] - r.top) * r.c);
-        if (w) {
-          const int bin = (int)__builtin_amdgcn_fmed3f(d[j] * per_bin, 0.f, (float)(kBins - 1));   // as in fine_of
-          atomicAdd(&w_bin[bin], w);
-          atomicAdd(&n_bin[bin], 1u);
-          if (st.min_w && w >= st.min_w) least_sum += w;
-        }
+    for (int j = 0; j < 8; ++j) {
+      const u64 w = weight(((double)v[j] - dtop) * r.c);
+      if (w) {
+        const int bin = (int)__builtin_amdgcn_fmed3f(d[j] * per_bin, 0.f, (float)(kBins - 1));   // as in fine_of
+        atomicAdd(&table[bin], w | (u64)1 << kCountAt);
       }
+      if (st.min_w && w >= st.min_w) least_sum += w;
+    }
+    const bool last = at + kStep >= i1;
+    if (turn && !last) continue;
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < kTables; ++t) {
+      const ulonglong2 x = *(const ulonglong2*)(tables[t] + 2 * tid);
+      mine[0] = mine[0] + Pair{x.x & (((u64)1 << kCountAt) - 1), x.x >> kCountAt};
+      mine[1] = mine[1] + Pair{x.y & (((u64)1 << kCountAt) - 1), x.y >> kCountAt};
+    }
+    if (!last) {
+      __syncthreads();
+#pragma unroll
+      for (int t = 0; t < kTables; ++t) *(ulonglong2*)(tables[t] + 2 * tid) = make_ulonglong2(0, 0);
+      __syncthreads();
     }
   }
   e = wave_all(e, 0.0, Add());
@@ -483,26 +527,37 @@ __global__ __launch_bounds__(kThreads) void sample_hist_kernel(SampleArgs a) {
     put(a.kept + at, kept);
   }
   if (st.greedy) return;
-  put(a.w_bins + at * kBins + tid, w_bin[tid]);
-  put(a.n_bins + at * kBins + tid, n_bin[tid]);
+  put(a.w_bins + at * kBins + 2 * tid, mine[0].w);
+  put(a.w_bins + at * kBins + 2 * tid + 1, mine[1].w);
+  put((u64*)(a.n_bins + at * kBins) + tid, mine[0].n | mine[1].n << 32);
   if (!last_to_arrive(&a.plan[b].arrived, (uint32_t)a.chunks, &s_last)) return;
   // the row's bins, all chunks' sums asked for at once: running sums; and the plan
   u64 sum_m = get(a.kept + b * a.chunks + min<int64_t>(tid & 63, a.chunks - 1));
-  u64 w[kSampleChunks];
-  uint32_t n[kSampleChunks];
+  Pair sum[2] = {};
+  constexpr int kJoin = 8;                                 // of the chunks at a time
+#pragma unroll 1
+  for (int c0 = 0; c0 < a.chunks; c0 += kJoin) {
+    u64 w[kJoin][2], n[kJoin];
 #pragma unroll
-  for (int c = 0; c < kSampleChunks; ++c) {
-    const int64_t from = (b * a.chunks + min<int64_t>(c, a.chunks - 1)) * kBins + tid;
-    w[c] = get(a.w_bins + from);
-    n[c] = get(a.n_bins + from);
+    for (int c = 0; c < kJoin; ++c) {
+      const int64_t from = (b * a.chunks + min<int64_t>(c0 + c, a.chunks - 1)) * kBins;
+      w[c][0] = get(a.w_bins + from + 2 * tid);
+      w[c][1] = get(a.w_bins + from + 2 * tid + 1);
+      n[c] = get((const u64*)(a.n_bins + from) + tid);
+    }
+#pragma unroll
+    for (int c = 0; c < kJoin; ++c) {
+      if (c0 + c >= a.chunks) break;
+      sum[0] = sum[0] + Pair{w[c][0], n[c] & 0xFFFFFFFFu};
+      sum[1] = sum[1] + Pair{w[c][1], n[c] >> 32};
+    }
   }
-  Pair sum = {0, 0};
-#pragma unroll
-  for (int c = 0; c < kSampleChunks; ++c) sum = sum + (c < a.chunks ? Pair{w[c], n[c]} : Pair{0, 0});
   sum_m = wave_all((tid & 63) < a.chunks ? sum_m : 0, (u64)0, Add());
-  sum = scan(sum, waves);
-  bins[tid] = sum;
-  ((ulonglong2*)a.sums)[b * kBins + tid] = make_ulonglong2(sum.w, sum.n);
+  const Pair upto = scan(sum[0] + sum[1], waves), first = {upto.w - sum[1].w, upto.n - sum[1].n};
+  bins[2 * tid] = first;
+  bins[2 * tid + 1] = upto;
+  ((ulonglong2*)a.sums)[b * kBins + 2 * tid] = make_ulonglong2(first.w, first.n);
+  ((ulonglong2*)a.sums)[b * kBins + 2 * tid + 1] = make_ulonglong2(upto.w, upto.n);
   __syncthreads();
   if (tid < 64) make_plan(a.plan + b, st, sum_m, u, bins);
 }
@@ -521,7 +576,7 @@ struct Found {                           // the answer to a question
 struct Shared {                          // a block's memory
   u64 list[kList];                       // places of gathered tokens, in no order
   u64 few[kSmall];                       // those the answer lies among
-  Pair bins[kBins], split[kBins];        // running sums by bin: of the row, of a part of it
+  Pair bins[kBins], split[kParts];       // running sums by bin: of the row, of a part of it
   Pair waves[kWaves];
   uint32_t count, at, few_n;
   bool last;
@@ -532,27 +587,31 @@ struct Head {                            // of a plan
   uint32_t ranges, upto;
 };
 
-// Appends to the list the logits of eight per lane, from index i on, that ok(x) says yes to.
-template <class F>
-__device__ __forceinline__ void append(Shared& s, const float v[8], int64_t i, F&& ok) {
-  const int lane = threadIdx.x & 63;
-  uint64_t mask[8];
-  uint32_t all = 0;
+// Appends to the list the logits of N eights per lane, from index i[k] on, that ok(x, index) says yes to: a lane's own one after
+// another, behind those of the lanes before it.  The eights from `live` on hold none.
+template <int N, class F>
+__device__ __forceinline__ void append(Shared& s, const float v[N][8], const int i[N], int live, F&& ok) {
+  uint32_t mine = 0;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    mask[j] = __ballot(ok(v[j]));
-    all += __popcll(mask[j]);
+  for (int k = 0; k < N; ++k) {
+    if (k >= live) break;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) mine |= ok(v[k][j], i[k] + j) ? 1u << (8 * k + j) : 0u;
   }
-  if (!all) return;
+  if (!__any(mine != 0)) return;
+  const uint32_t n = __popc(mine), upto = wave_scan(n, 0u, Add()), all = lane_value(upto, 63);
   uint32_t at = 0;
-  if (lane == 0) at = atomicAdd(&s.count, all);
-  at = __builtin_amdgcn_readfirstlane(at);
+  if ((threadIdx.x & 63) == 0) at = atomicAdd(&s.count, all);
+  at = __builtin_amdgcn_readfirstlane(at) + upto - n;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if (!mask[j]) continue;
-    const uint32_t k = at + __popcll(mask[j] & (((uint64_t)1 << lane) - 1));
-    if (((mask[j] >> lane) & 1) && k < kList) s.list[k] = place(v[j], i + j);
-    at += __popcll(mask[j]);
+  for (int k = 0; k < N; ++k) {
+    if (k >= live) break;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const bool is = mine >> (8 * k + j) & 1;
+      if (is && at < kList) s.list[at] = place(v[k][j], i[k] + j);
+      at += is;
+    }
   }
 }
 
@@ -568,9 +627,9 @@ __device__ __forceinline__ Named named_by(const Row& r, const Head& plan) {
   for (int i = 0; i < 3; ++i) {
     const bool last = plan.bin1[i] == kBins - 1;
     light |= last;
-    n.lo[i] = (float)(plan.bin0[i] * kBins);
+    n.lo[i] = (float)(plan.bin0[i] * kParts);
     // the largest number below the next bin; of no range: below its first
-    n.hi[i] = last ? __builtin_inff() : __uint_as_float(__float_as_uint((float)((plan.bin1[i] + 1) * kBins)) - 1);
+    n.hi[i] = last ? __builtin_inff() : __uint_as_float(__float_as_uint((float)((plan.bin1[i] + 1) * kParts)) - 1);
   }
   n.least = light ? from_falling((uint32_t)key_end(r, kBins - 1)) : kNegInf;
   return n;
@@ -584,12 +643,12 @@ __device__ __forceinline__ bool is_named(const Row& r, const Named& n, float x) 
 }
 
 // Whether one block reads a row's tokens, looking for them only in groups of 64 logits whose largest is in their bins,
-// in place of all blocks reading all logits.  That takes it 14 ns a group more, and saves the launch's blocks a second
+// in place of all blocks reading all logits.  That takes it 10 ns a group more, and saves the launch's blocks a second
 // reading, of little cost while all of them are there at once.  131072 logits, calls with one block and with all: one
-// row, 100 tokens 25.0 and 25.3 us, 300 29.3 and 26.1; 16 rows, 100 27.8 and 29.5, 600 38.6 and 31.7; 64 rows, 300 53.7
-// and 75.6, 1500 73 and 85.
+// row, 20 tokens 22.7 and 24.4 us, 100 26.7 and 27.7, 300 29.3 and 27.9; 16 rows, 100 31.2 and 32.3, 300 33.9 and 32.4; 64
+// rows, 20 39.4 and 44.2, 300 47.9 and 48.6, 600 52.6 and 49.5.
 __device__ __forceinline__ bool few_groups(const SampleArgs& a, const Head& plan) {
-  const int64_t more = max(a.B * a.V - ((int64_t)1 << 21), (int64_t)0) >> 12;
+  const int64_t more = max(a.B * a.V - ((int64_t)1 << 21), (int64_t)0) >> 15;
   return plan.ranges == 1 && min((int64_t)plan.upto, a.groups) <= 128 + more;
 }
 // The list: the plan's tokens from such groups, eight lanes to each.
@@ -615,21 +674,34 @@ __device__ __forceinline__ void gather_groups(const SampleArgs& a, int64_t b, co
     }
     __syncthreads();
     const int n = s.at;
+    float next[kAhead][8];
+    int at[kAhead];
+    auto load = [&](int k0) {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int g = k0 + k * kTeams + (tid >> 3);
+        at[k] = g < n ? (int)groups[g] * 64 + (tid & 7) * 8 : (int)a.V;
+        load8_raw<BF, VEC>(row, at[k], a.V, next[k]);
+      }
+    };
+    load(0);
     for (int k0 = 0; k0 < n; k0 += kAhead * kTeams) {
       float v[kAhead][8];
-      int64_t i[kAhead];
+      int i[kAhead];
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        const int at = k0 + k * kTeams + (tid >> 3);
-        i[k] = at < n ? (int64_t)groups[at] * 64 + (tid & 7) * 8 : a.V;
-        load8_raw<BF, VEC>(row, i[k], a.V, v[k]);
-      }
+        i[k] = at[k];
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        if (k0 + k * kTeams >= n) break;
-        finish8<BF, VEC>(row, i[k], a.V, v[k]);
-        append(s, v[k], i[k], [&](float x) { return is_named(r, named, x); });
+        for (int j = 0; j < 8; ++j) v[k][j] = next[k][j];
       }
+      if (k0 + kAhead * kTeams < n) load(k0 + kAhead * kTeams);
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) finish8<BF, VEC>(row, i[k], a.V, v[k]);
+      // the one range; of a lone bin, whose bounds may be compared with no number, all that weighs anything
+      append<kAhead>(s, v, i, (n - k0 + kTeams - 1) / kTeams, [&](float x, int) {
+        const float y = ((float)r.top - x) * r.per_fine;
+        return !(y < named.lo[0]) & !(y > named.hi[0]) & (x >= named.least);
+      });
     }
     __syncthreads();
   }
@@ -648,11 +720,9 @@ __device__ __forceinline__ void gather_chunk(const SampleArgs& a, int64_t b, int
 #pragma unroll
     for (int k = 0; k < 2; ++k) load8_raw<BF, VEC>(row, i + k * kStep, a.V, v[k]);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (at + k * kStep >= i1) break;
-      finish8<BF, VEC>(row, i + k * kStep, i1, v[k]);        // a chunk is a multiple of eight, but for the row's end
-      append(s, v[k], i + k * kStep, [&](float x) { return is_named(r, named, x); });
-    }
+    for (int k = 0; k < 2; ++k) finish8<BF, VEC>(row, i + k * kStep, i1, v[k]);          // a chunk is a multiple of eight, but for the row's end
+    const int is[2] = {(int)i, (int)i + kStep};
+    append<2>(s, v, is, at + kStep < i1 ? 2 : 1, [&](float x, int) { return is_named(r, named, x); });
   }
   __syncthreads();
 }
@@ -749,18 +819,27 @@ __device__ __forceinline__ int split_choose(const Asked& q, Shared& s, Pair* bef
   const Pair mine = s.split[threadIdx.x], upto = scan(mine, s.waves);
   s.split[threadIdx.x] = upto;
   __syncthreads();
-  const int k = first_bin(q, s.split, *before);
+  const int k = first_bin<kParts>(q, s.split, *before);
   const Pair skip = k ? s.split[k - 1] : Pair{0, 0};
   *n = s.split[k].n - skip.n;
   *before = *before + skip;
   return k;
 }
 
-// The plan's tokens, a few to a thread: their places, fine bins (-1: none) and weights.
+// The plan's tokens, a few to a thread: their places.  What follows from them is computed again where it is asked for: kept,
+// it is more registers than leave room for two blocks on a CU (64 rows of wide settings 66 us, 54 with two).
 constexpr int kEach = kList / kThreads;
 struct Mine {
-  u64 p[kEach], w[kEach];
-  int fine[kEach];
+  u64 p[kEach];
+  int n;                                 // of all threads
+  __device__ float logit(int i) const {
+    uint32_t key = (uint32_t)(p[i] >> 32);
+    asm volatile("" : "+v"(key));                            // what follows stays where it is, and out of registers
+    return from_falling(key);
+  }
+  __device__ int fine(const Row& r, int i) const {           // bin; -1: no token
+    return i * kThreads + (int)threadIdx.x < n ? fine_of(r, logit(i)) : -1;
+  }
 };
 
 // The answer from the plan's tokens: those of the bin, by its fine bins if they are many.  False if too many share a
@@ -776,18 +855,21 @@ __device__ __forceinline__ bool answer_mine(const Row& r, const Asked& q, const 
   if (n > kSmall) {
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-      if (t.fine[i] >= 0 && t.fine[i] / kBins == bin) {
-        atomicAdd(&s.split[t.fine[i] % kBins].w, t.w[i]);
-        atomicAdd(&s.split[t.fine[i] % kBins].n, 1ull);
+      const int fine = t.fine(r, i);
+      if (fine >= 0 && fine / kParts == bin) {
+        atomicAdd(&s.split[fine % kParts].w, weight_of(r, t.logit(i)));
+        atomicAdd(&s.split[fine % kParts].n, 1ull);
       }
     }
     part = split_choose(q, s, &before, &n);
     if (n > kSmall) return false;
   }
 #pragma unroll
-  for (int i = 0; i < kEach; ++i)
-    if (t.fine[i] >= 0 && (part < 0 ? t.fine[i] / kBins == bin : t.fine[i] == bin * kBins + part))
+  for (int i = 0; i < kEach; ++i) {
+    const int fine = t.fine(r, i);
+    if (fine >= 0 && (part < 0 ? fine / kParts == bin : fine == bin * kParts + part))
       s.few[atomicAdd(&s.few_n, 1u)] = t.p[i];
+  }
   __syncthreads();
   *found = among_few(q, sort_few(r, s.few, (int)n), before);
   return true;
@@ -795,7 +877,7 @@ __device__ __forceinline__ bool answer_mine(const Row& r, const Asked& q, const 
 
 // The answer from the row itself, read by this block: its bin by places, nine bits at a time, down to a single token
 // if need be; from LDS once its tokens fit.
-template <bool BF>
+template <bool BF, bool VEC>
 __device__ __forceinline__ Found answer_row(const SampleArgs& a, int64_t b, const Row& r, const Asked& q, int bin,
                                             Pair before, u64 n, Shared& s) {
   const int tid = threadIdx.x;
@@ -805,12 +887,15 @@ __device__ __forceinline__ Found answer_row(const SampleArgs& a, int64_t b, cons
     __syncthreads();
     if (tid == 0) s.count = 0;
     __syncthreads();
-    each<BF>(a, b, g, [&](bool is, u64 p) {
-      if (is) {
-        const uint32_t at = atomicAdd(&s.count, 1u);
-        if (at < kList) s.list[at] = p;
-      }
-    });
+    const void* row = row_of<BF>(a, b);
+#pragma unroll 1
+    for (int64_t at = 0; at < a.V; at += kStep) {
+      const int i[1] = {(int)at + tid * 8};
+      float v[1][8];
+      load8_raw<BF, VEC>(row, i[0], a.V, v[0]);
+      finish8<BF, VEC>(row, i[0], a.V, v[0]);
+      append<1>(s, v, i, 1, [&](float x, int at) { return in(place(x, at)); });
+    }
     __syncthreads();
   };
   bool listed = false;
@@ -820,7 +905,7 @@ __device__ __forceinline__ Found answer_row(const SampleArgs& a, int64_t b, cons
       listed = true;
     }
     const int bits = 64 - __clzll((long long)(g.hi - g.lo)), shift = max(bits - 9, 0);
-    static_assert(kBins == 512, "nine bits");
+    static_assert(kParts == 512, "nine bits");
     __syncthreads();
     s.split[tid] = {0, 0};
     __syncthreads();
@@ -843,7 +928,7 @@ __device__ __forceinline__ Found answer_row(const SampleArgs& a, int64_t b, cons
 }
 
 template <bool BF, bool VEC>
-__global__ __launch_bounds__(kThreads) void sample_draw_kernel(SampleArgs a) {
+__global__ __launch_bounds__(kThreads, 4) void sample_draw_kernel(SampleArgs a) {
   __shared__ Shared s;
   const int tid = threadIdx.x;
   const int64_t b = blockIdx.y;
@@ -863,7 +948,8 @@ __global__ __launch_bounds__(kThreads) void sample_draw_kernel(SampleArgs a) {
   }
   double exps = a.exps[b * a.chunks + chunk];
   u64 sum_m = a.kept[b * a.chunks + chunk];
-  const ulonglong2 mine = ((const ulonglong2*)a.sums)[b * kBins + tid];
+  const ulonglong2* sums = (const ulonglong2*)a.sums + b * kBins;
+  const ulonglong2 mine0 = sums[tid], mine1 = sums[kThreads + tid];
   u64 best;
   const Row r = row_of_extremes(ex, st, &best);
   const bool masked = r.top == -__builtin_inf();
@@ -871,9 +957,12 @@ __global__ __launch_bounds__(kThreads) void sample_draw_kernel(SampleArgs a) {
   const bool draws = !st.greedy && !masked;
   const bool alone = !draws || plan.ranges == 0 || few_groups(a, plan);   // one block does it all
   if (alone && part > 0) return;
+  exps = wave_all((tid & 63) < a.chunks ? exps : 0.0, 0.0, Add());
+  sum_m = wave_all((tid & 63) < a.chunks ? sum_m : 0, (u64)0, Add());
   if (draws) {
     if (tid == 0) s.count = 0;
-    s.bins[tid] = {mine.x, mine.y};
+    s.bins[tid] = {mine0.x, mine0.y};
+    s.bins[kThreads + tid] = {mine1.x, mine1.y};
     __syncthreads();
     const u64* elsewhere = nullptr;
     uint32_t tokens = 0;
@@ -904,14 +993,7 @@ __global__ __launch_bounds__(kThreads) void sample_draw_kernel(SampleArgs a) {
       for (int i = 0; i < kEach; ++i)
         if (i * kThreads < tokens) t.p[i] = s.list[min(i * kThreads + tid, (int)tokens - 1)];
     }
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      t.fine[i] = -1;
-      if (i * kThreads >= tokens) continue;
-      const float x = logit_at(t.p[i]);
-      t.w[i] = weight_of(r, x);
-      t.fine[i] = i * kThreads + tid < tokens ? fine_of(r, x) : -1;
-    }
+    t.n = (int)tokens;
     const bool small = plan.ranges == 1 && tokens <= kSmall;     // one order answers all questions
     Few few = {0, 0, 0};
     if (small) {
@@ -919,7 +1001,6 @@ __global__ __launch_bounds__(kThreads) void sample_draw_kernel(SampleArgs a) {
       __syncthreads();
       few = sort_few(r, s.few, (int)tokens);
     }
-    sum_m = wave_all((tid & 63) < a.chunks ? sum_m : 0, (u64)0, Add());
     const Pair all = s.bins[kBins - 1];
     const u64 k = st.k && (u64)st.k < all.n ? (u64)st.k : 0;
     const double u = a.u[b];
@@ -934,7 +1015,7 @@ __global__ __launch_bounds__(kThreads) void sample_draw_kernel(SampleArgs a) {
         const double at = u > 0.0 ? fmin(u, 1.0) * (double)sum : 0.0;   // NaN: 0
         q.r = min((u64)at, sum - 1);
       }
-      const int bin = small ? plan.bin0[0] : first_bin(q, s.bins, {0, 0});
+      const int bin = small ? plan.bin0[0] : first_bin<kBins>(q, s.bins, {0, 0});
       const Pair before = bin ? s.bins[bin - 1] : Pair{0, 0};
       const u64 n = s.bins[bin].n - before.n;
       Found f;
@@ -946,7 +1027,7 @@ __global__ __launch_bounds__(kThreads) void sample_draw_kernel(SampleArgs a) {
 #pragma unroll
         for (int i = 0; i < 3; ++i) named |= plan.bin0[i] <= bin && bin <= plan.bin1[i];
         held = held && named && answer_mine(r, q, t, bin, before, n, s, &f);
-        if (!held) f = answer_row<BF>(a, b, r, q, bin, before, n, s);
+        if (!held) f = answer_row<BF, VEC>(a, b, r, q, bin, before, n, s);
       }
       sum = min(sum, f.sum);
       token = f.token;
@@ -954,7 +1035,6 @@ __global__ __launch_bounds__(kThreads) void sample_draw_kernel(SampleArgs a) {
     token = min(token, a.V - 1);         // within the row whatever a workspace that two calls write at once may hold
   }
   if (tid >= 64) return;
-  exps = wave_all(tid < a.chunks ? exps : 0.0, 0.0, Add());
   if (tid == 0) {
     a.token[b] = (int32_t)token;
     if (a.logprob) {

@@ -87,6 +87,23 @@ def test_rows_with_settings_of_their_own(B):
            g.choice([1, 0.9, 0.2, 1.5, -1, NAN], B), g.choice([0, 0.1, -1, NAN, 0.01], B))
 
 
+@pytest.mark.parametrize("B,V", [(130, 40011), (3, 300007), (129, 16390)])
+def test_rows_in_parts_of_several_turns(B, V):
+    """A block's part of a row is more than it counts at a time, and its last turn is not whole."""
+    g = rng(V)
+    x = g.standard_normal((B, V)) * 2.5
+    x[g.random((B, V)) < 0.05] = -INF
+    x[1] = np.sort(x[1])                       # all of what weighs most in one part
+    _check(x, g.random(B), g.choice([1, 0.7, 1.2, 0], B), g.choice([0, 20, 700, V // 2], B), g.choice([1, 0.9, 0.98], B),
+           g.choice([0, 0.02], B))
+
+
+def test_greedy_rows_in_parts_of_several_turns():
+    g = rng(3)
+    x = g.standard_normal((130, 40011)) * 3
+    _check(x, g.random(130), 0.0)
+
+
 @pytest.mark.parametrize("V", [5, 100, 4096, 4097, 20000, 70000])
 @pytest.mark.parametrize("kw", [dict(), dict(k=3), dict(p=0.5), dict(min_p=0.5), dict(temperature=0.0), dict(k=4500, p=0.6)])
 def test_equal_logits(V, kw):
