@@ -104,7 +104,7 @@ int bitlinear_q4_bytes(int64_t n, int64_t K, int group, size_t* code_bytes, size
   if (group != 32 && group != 64 && group != 128) return BL_ENOTSUP;
   if (n < 1 || n > kQ4MaxN || K < group || K > kQ4MaxK || K % group || !code_bytes || !scale_bytes) return BL_EINVAL;
   const size_t blocks = (size_t)((n + 15) / 16) * (size_t)((K + 127) / 128);
-  if (blocks >= (size_t)1 << 24) return BL_EINVAL;         // a launch's threads: 256 for each of them
+  if (blocks >= (size_t)1 << 24) return BL_EINVAL;         // as many waves as a launch may have, nearly
   *code_bytes = blocks * 1024;
   *scale_bytes = blocks * (size_t)(2048 / group) * 2;
   return BL_OK;
