@@ -751,8 +751,7 @@ int bitlinear_q4_fwd(const int8_t* xq, const float* x_scale, int64_t T, int64_t 
 /* ---------------------------------------------------------------------------------------------
  * A token per row of logits, drawn by one given number per row.
  *
- * x is x_dtype [B][V] with rows row_stride elements apart (row_stride >= V; any alignment of the elements;
- * 16-byte aligned rows take the vector path).  A logit that is -inf or NaN is masked.  With top the row's largest
+ * x is x_dtype [B][V] with rows row_stride elements apart (row_stride >= V; no alignment but the elements').  A logit that is -inf or NaN is masked.  With top the row's largest
  * logit and its tokens in the order of falling logits, equal ones by index (-0 equals 0):
  *   w_i    = rint(2^40 * exp((x_i - top) / temperature)), a whole number, from fp64 within a few ulp; where
  *            top is +inf, 2^40 for its equals and 0 for the others

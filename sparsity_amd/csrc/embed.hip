@@ -111,9 +111,10 @@ __device__ __forceinline__ void fill_first(const EmbedBwdArgs& a, int64_t rows, 
 }
 
 // Chunk blockIdx.x of the tokens by id, then token.  A key is the id over the bits of the token's place in the
-// chunk: 32 bits in all for tables of less than 2^21 rows.  Two keys to a thread; distances below 64 inside a wave.
+// chunk: 32 bits in all for tables of less than 2^21 rows.  Two keys to a thread; distances below 64 inside a wave.  The first
+// `top` places, a power of two, hold all tokens that there are.
 template <class Key>
-__global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(EmbedBwdArgs a, Sorted s, int64_t fill) {
+__global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(EmbedBwdArgs a, Sorted s, int64_t fill, int top) {
   __shared__ Key key[kChunk];
   if ((int)blockIdx.x >= s.chunks) {
     fill_first(a, fill, blockIdx.x - s.chunks, gridDim.x - s.chunks);
@@ -131,7 +132,7 @@ __global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(EmbedBwdArgs a
     const int32_t id = t0 + i < a.T ? a.ids[t0 + i] : -1;
     v[h] = (id >= 0 && id < a.V ? (Key)id : none) << kBits | (Key)i;
   }
-  for (int n = 2; n <= kChunk; n <<= 1) {    // runs of n in order, every other one reversed
+  for (int n = 2; n <= top; n <<= 1) {       // runs of n in order, every other one reversed
     if (n > 64) {
       __syncthreads();
 #pragma unroll
@@ -462,8 +463,10 @@ hipError_t launch_embed_bwd(const EmbedBwdArgs& a, bool dy_bf16, hipStream_t s) 
     const unsigned sorts = (unsigned)w.chunks;
     filled = a.accumulate ? 0 : std::min<int64_t>(a.V, kFillSort / (a.K * 4));
     const unsigned some = filled ? kFillBlocks : 0;
-    if (a.V < ((int64_t)1 << (32 - kEmbedChunkBits))) embed_sort_kernel<uint32_t><<<sorts + some, kSortThreads, 0, s>>>(a, so, filled);
-    else embed_sort_kernel<uint64_t><<<sorts + some, kSortThreads, 0, s>>>(a, so, filled);
+    int top = 64;
+    while (top < kChunk && top < a.T) top *= 2;
+    if (a.V < ((int64_t)1 << (32 - kEmbedChunkBits))) embed_sort_kernel<uint32_t><<<sorts + some, kSortThreads, 0, s>>>(a, so, filled, top);
+    else embed_sort_kernel<uint64_t><<<sorts + some, kSortThreads, 0, s>>>(a, so, filled, top);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if (w.chunks > 1) {
       embed_rank_kernel<<<(unsigned)w.chunks * (kChunk / kRankThreads), kRankThreads, 0, s>>>(a.T, so);

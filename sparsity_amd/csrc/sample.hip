@@ -73,12 +73,34 @@ struct Least {
   __device__ float operator()(float x, float y) const { return fminf(x, y); }
 };
 
+// Eight elements from anywhere: the loads of 16 bytes need no more than the elements' own alignment.
+typedef uint32_t v4u_of_bf16 __attribute__((ext_vector_type(4), aligned(2)));
+typedef float v4f_of_f32 __attribute__((ext_vector_type(4), aligned(4)));
+template <bool BF>
+__device__ __forceinline__ void load8_any(const void* row, int64_t i, float v[8]) {
+  if constexpr (BF) {
+    const v4u_of_bf16 w = *(const v4u_of_bf16*)((const uint16_t*)row + i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = bf16_lo(w[j]);
+      v[2 * j + 1] = bf16_hi(w[j]);
+    }
+  } else {
+    const v4f_of_f32 x = *(const v4f_of_f32*)((const float*)row + i), y = *(const v4f_of_f32*)((const float*)row + i + 4);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = x[j];
+      v[4 + j] = y[j];
+    }
+  }
+}
 // Elements i .. i + 8 of a row without a branch around a load, so that many can be in flight: vector loads of whole
-// eights (what is past them is loaded as the last one and left out below), else element by element.
+// eights (what is past them is loaded as the last one and left out below), and where a row has no eight, element by
+// element.
 template <bool BF, bool VEC>
 __device__ __forceinline__ void load8_raw(const void* row, int64_t i, int64_t V, float v[8]) {
   if constexpr (VEC) {
-    load_f8<BF>(row, max(min(i, V / 8 * 8 - 8), (int64_t)0), v);
+    load8_any<BF>(row, max(min(i, V / 8 * 8 - 8), (int64_t)0), v);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {

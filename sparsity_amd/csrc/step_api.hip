@@ -186,8 +186,7 @@ int bitlinear_sample(const void* x, int x_dtype, int64_t B, int64_t V, int64_t r
   a.token = token;
   a.logprob = logprob_opt;
   bl::sample_split(a, (char*)ws);
-  const bool vec = V >= 8 && aligned(x, 16) && (B == 1 || row_stride * e % 16 == 0);   // whole eights are loaded
-  return status_of(bl::launch_sample(a, x_dtype == BL_DTYPE_BF16, vec, (hipStream_t)stream));
+  return status_of(bl::launch_sample(a, x_dtype == BL_DTYPE_BF16, V >= 8, (hipStream_t)stream));   // whole eights are loaded
 }
 
 }  // extern "C"
