@@ -14,9 +14,9 @@
 //          those up to the first question's bin are kList at most (top-k and top-p as they are used) all of them, once
 //          for all questions, else those of each question's bin or few bins
 //   draw   tokens are gathered by one block, from the groups of 64 whose largest reaches them, or by all blocks from all
-//          logits, for the last of them.  The one that has them answers the questions: a bin by its fine bins, until a
-//          wave can sort what is left.  If more than kList tokens are planned for (equal logits above all), one block
-//          reads the row and splits bins by place (value, then index)
+//          logits, for the last of them.  The one that has them answers the questions: a bin by its fine bins, equal
+//          logits (bf16 ones above all) by place (value, then index), until a wave can sort what is left.  If more than
+//          kList tokens are planned for, one block reads the row and splits its bins by place
 // Largest and least logit bound the bins (what weighs nothing aside), so that they are as fine as the row allows: 1024
 // leave 420 tokens in the fullest of 131072 normal logits, and a plan is below kList but for odd rows; with 512 one in a
 // thousand was above it, and its call took 150 us in place of 54.
@@ -600,6 +600,7 @@ struct Shared {                          // a block's memory
   u64 few[kSmall];                       // those the answer lies among
   Pair bins[kBins], split[kParts];       // running sums by bin: of the row, of a part of it
   Pair waves[kWaves];
+  Range range;                           // of the places in question
   uint32_t count, at, few_n;
   bool last;
 };
@@ -864,37 +865,70 @@ struct Mine {
   }
 };
 
-// The answer from the plan's tokens: those of the bin, by its fine bins if they are many.  False if too many share a
-// fine bin.
-__device__ __forceinline__ bool answer_mine(const Row& r, const Asked& q, const Mine& t, int bin, Pair before, u64 n,
-                                            Shared& s, Found* found) {
+// The answer from the plan's tokens: those of the bin, by its fine bins if they are many, and where many share a fine bin
+// (equal logits) by place, until a wave can sort them.
+__device__ __forceinline__ Found answer_mine(const Row& r, const Asked& q, const Mine& t, int bin, Pair before, u64 n, Shared& s) {
   const int tid = threadIdx.x;
-  __syncthreads();
-  s.split[tid] = {0, 0};
-  if (tid == 0) s.few_n = 0;
-  __syncthreads();
   int part = -1;                         // of the bin; -1: all of it
+  Range g = {0, ~0ull};
+  auto clear = [&] {
+    __syncthreads();
+    s.split[tid] = {0, 0};
+    if (tid == 0) {
+      s.few_n = 0;
+      s.range = {~0ull, 0};
+    }
+    __syncthreads();
+  };
+  auto add = [&](int i, int to) {
+    atomicAdd(&s.split[to].w, weight_of(r, t.logit(i)));
+    atomicAdd(&s.split[to].n, 1ull);
+  };
+  auto in = [&](int i) {
+    const int fine = t.fine(r, i);
+    return fine >= 0 && (part < 0 ? fine / kParts == bin : fine == bin * kParts + part) && t.p[i] >= g.lo && t.p[i] <= g.hi;
+  };
+  clear();
   if (n > kSmall) {
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int fine = t.fine(r, i);
-      if (fine >= 0 && fine / kParts == bin) {
-        atomicAdd(&s.split[fine % kParts].w, weight_of(r, t.logit(i)));
-        atomicAdd(&s.split[fine % kParts].n, 1ull);
-      }
-    }
+    for (int i = 0; i < kEach; ++i)
+      if (in(i)) add(i, t.fine(r, i) % kParts);
     part = split_choose(q, s, &before, &n);
-    if (n > kSmall) return false;
+  }
+  if (n > kSmall) {
+    u64 lo = ~0ull, hi = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const bool is = in(i);
+      lo = is ? min(lo, t.p[i]) : lo;
+      hi = is ? max(hi, t.p[i]) : hi;
+    }
+    lo = wave_all(lo, (u64)~0ull, Least());
+    hi = ~wave_all(~hi, (u64)~0ull, Least());
+    if ((tid & 63) == 0) {
+      atomicMin(&s.range.lo, lo);
+      atomicMax(&s.range.hi, hi);
+    }
+    __syncthreads();
+    g = s.range;
+#pragma unroll 1
+    while (n > kSmall) {
+      const int shift = max(64 - __clzll((long long)(g.hi - g.lo)) - 9, 0);
+      static_assert(kParts == 512, "nine bits");
+      clear();
+#pragma unroll
+      for (int i = 0; i < kEach; ++i)
+        if (in(i)) add(i, (int)((t.p[i] - g.lo) >> shift));
+      const int k = split_choose(q, s, &before, &n);
+      g.lo += (u64)k << shift;
+      g.hi = min(g.hi, g.lo + (((u64)1 << shift) - 1));
+    }
   }
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int fine = t.fine(r, i);
-    if (fine >= 0 && (part < 0 ? fine / kParts == bin : fine == bin * kParts + part))
-      s.few[atomicAdd(&s.few_n, 1u)] = t.p[i];
-  }
+  for (int i = 0; i < kEach; ++i)
+    if (in(i)) s.few[atomicAdd(&s.few_n, 1u)] = t.p[i];
   __syncthreads();
-  *found = among_few(q, sort_few(r, s.few, (int)n), before);
-  return true;
+  return among_few(q, sort_few(r, s.few, (int)n), before);
 }
 
 // The answer from the row itself, read by this block: its bin by places, nine bits at a time, down to a single token
@@ -1041,15 +1075,15 @@ __global__ __launch_bounds__(kThreads, 4) void sample_draw_kernel(SampleArgs a) 
       const Pair before = bin ? s.bins[bin - 1] : Pair{0, 0};
       const u64 n = s.bins[bin].n - before.n;
       Found f;
-      bool held = plan.ranges > 0;
+      const bool held = plan.ranges > 0;
       if (small) {
         f = among_few(q, few, before);
       } else {
         bool named = false;
 #pragma unroll
         for (int i = 0; i < 3; ++i) named |= plan.bin0[i] <= bin && bin <= plan.bin1[i];
-        held = held && named && answer_mine(r, q, t, bin, before, n, s, &f);
-        if (!held) f = answer_row<BF, VEC>(a, b, r, q, bin, before, n, s);
+        if (held && named) f = answer_mine(r, q, t, bin, before, n, s);
+        else f = answer_row<BF, VEC>(a, b, r, q, bin, before, n, s);
       }
       sum = min(sum, f.sum);
       token = f.token;

@@ -98,6 +98,16 @@ def test_rows_in_parts_of_several_turns(B, V):
            g.choice([0, 0.02], B))
 
 
+@pytest.mark.parametrize("V,std", [(81063, 1.0), (262143, 1.0), (50000, 0.3), (131072, 5.0)])
+def test_bf16_rows_hold_many_equal_logits(V, std):
+    """Hundreds of tokens with the logit in question, not next to each other."""
+    g = rng(V)
+    x = g.standard_normal((3, V)) * std
+    for kw in [dict(temperature=1.5), dict(p=0.9), dict(k=V // 3), dict(k=V // 2, p=0.97), dict(min_p=0.001, p=0.99)]:
+        for _ in range(2):
+            _check(x, g.random(3), xd="bf16", **kw)
+
+
 def test_greedy_rows_in_parts_of_several_turns():
     g = rng(3)
     x = g.standard_normal((130, 40011)) * 3
