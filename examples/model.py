@@ -6,7 +6,7 @@
     kv_step (pages for the new tokens, ended requests' pages back) -> embed -> the blocks -> norm_quant
     -> q4_fwd (an output head in 4 bits) -> sample
 
-all on the GPU, so that it can be captured: the next step's token ids are where this one's ``sample`` wrote them.
+all on the GPU, so that it can be captured: the next step's token ids are where this one left them.
 ``train_embedding`` runs the embedding's training half, forward and backward.  Weights are random:
 
     python examples/model.py                 # 16 requests at a time, 2 blocks, 48 steps
@@ -55,9 +55,10 @@ class Model:
         self.head = S.q4_pack(torch.randn(vocab, hidden, generator=g, device=dev) * 0.02, group)
         self.xq, self.scale = empty(seqs, hidden, dtype=torch.int8), empty(seqs, dtype=torch.float32)
         self.logits = empty(seqs, vocab, dtype=torch.float32)
-        # each request's token, settings and next random number
+        # each request's token, settings and next random number; what a step draws, for rows without a request too
         self.tokens = torch.zeros(seqs, dtype=torch.int32, device=dev)
-        self.logprob = empty(seqs, dtype=torch.float32)
+        self.logprob = torch.zeros(seqs, dtype=torch.float32, device=dev)
+        self.drawn = empty(seqs), empty(seqs, dtype=torch.float32)
         self.u = torch.zeros(seqs, dtype=torch.float64, device=dev)
         self.settings = dict(temperature=torch.full((seqs,), 0.8, device=dev),
                              top_k=torch.full((seqs,), 50, dtype=torch.int32, device=dev),
@@ -66,7 +67,8 @@ class Model:
 
     def step(self, trace=None):
         """One token per request, from self.tokens and to self.tokens.  fresh is 1 for a request that goes on, -1 for
-        one that has ended (its place begins anew at length 0 with the next step's 1), 0 for an empty place."""
+        one that has ended (its place begins anew at length 0 with the next step's 1, from the token that the caller
+        puts there), 0 for an empty place.  A request that kv_step does not serve keeps its token and waits."""
         keep = (lambda n, *t: None) if trace is None else (lambda n, *t: trace.append(
             (n, [x.clone() for x in t])))
         keep("before", self.lens, self.fresh, self.tables, self.free, self.rows.count, self.tokens)
@@ -83,8 +85,10 @@ class Model:
         S.norm_quant(delta, self.norm, self.stream, out=(self.xq, self.scale, self.stream, None))
         S.q4_fwd(self.xq, self.scale, self.hidden, *self.head, self.vocab, self.group, out=self.logits)
         keep("head", self.xq, self.scale, self.logits)
-        S.sample(self.logits, self.u, **self.settings, out=(self.tokens, self.logprob), ws=self.ws)
-        keep("tokens", self.tokens, self.logprob)
+        S.sample(self.logits, self.u, **self.settings, out=self.drawn, ws=self.ws)
+        keep("tokens", *self.drawn)
+        for mine, drawn in zip((self.tokens, self.logprob), self.drawn):
+            mine.copy_(torch.where(served, drawn, mine))
         return self.tokens
 
 
@@ -123,10 +127,13 @@ def main():
     began = time.perf_counter()
     for t in range(a.steps):
         m.u.uniform_(generator=g)
+        place = t // 16 % a.seqs
         if t % 16 == 15:                   # one request ends, another takes its place with the step after
-            m.fresh[t // 16 % a.seqs] = -1
+            m.fresh[place] = -1
         graph.replay()
-        m.fresh.fill_(1)
+        if t % 16 == 15:
+            m.fresh[place] = 1
+            m.tokens[place:place + 1].random_(0, m.vocab, generator=g)
     torch.cuda.synchronize()
     took = (time.perf_counter() - began) / a.steps
     assert bool(((m.tokens >= 0) & (m.tokens < m.vocab)).all()) and bool(torch.isfinite(m.logprob).all())

@@ -215,3 +215,36 @@ def test_prompts_by_rows_of_a_step(kv):
     e = ((D + 6) * U * smag + 4 * U + 2.0 ** -17 + 24 * U)[..., None]
     assert np.all(np.abs(host(out) - ref) <= 2 * e * mag + 1e-30)
     assert not host(out)[3].any()                           # nothing cached
+
+
+@pytest.mark.parametrize("graphed", [False, True])
+def test_a_request_that_waits_keeps_its_token(graphed):
+    """A step leaves a request's token and log probability alone where it finds no page, adds nothing or has ended, and
+    puts the draw from the request's logits there where it was served."""
+    import torch
+    m, g = _model(3, pages=9)
+    step, waited = m.step, 0
+    if graphed:
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+            m.step()
+        step = graph.replay
+    m.logprob.copy_(dev(np.arange(-6, 0, dtype=np.float32)))
+    for t in range(16):
+        fresh = np.array(FRESH[t % len(FRESH)], np.int32)
+        m.fresh.copy_(dev(fresh))
+        m.u.copy_(dev(g.random(6)))
+        tokens, logprob = host(m.tokens).copy(), host(m.logprob).copy()
+        step()
+        served = np.diff(host(m.rows.starts)) > 0
+        got = host(m.tokens)
+        assert np.array_equal(got[~served], tokens[~served]) and _same(host(m.logprob)[~served], logprob[~served]), t
+        logits = host(m.logits)
+        for b in np.nonzero(served)[0]:
+            want, lp, d = R.sample_row(logits[b], float(m.u[b]), float(m.settings["temperature"][b]),
+                                       int(m.settings["top_k"][b]), float(m.settings["top_p"][b]))
+            assert got[b] == want and abs(host(m.logprob)[b] - lp) <= 2.0 ** -22 * (1 + d) + 2.0 ** -24 * abs(
+                lp), (t, b)
+        waited += int((~served & (fresh > 0)).sum())
+    assert waited == 25                                    # for a page, not by the caller's wish
