@@ -31,6 +31,8 @@ class Model:
         g = torch.Generator(device=dev)
         g.manual_seed(seed)
         self.seqs, self.page, self.vocab, self.hidden, self.group = seqs, page, vocab, hidden, group
+        per = -(-max_len // page)
+        max_len = per * page                                   # kv_step fills pages to their ends
         self.layers = [DecodeBlock(seqs, hidden, heads, kv_heads, D, ffn, page, max_len, kv, seed + 1 + i)
                        for i in range(layers)]
 
@@ -38,7 +40,6 @@ class Model:
             return torch.empty(shape, dtype=dtype, device=dev)
 
         # one table of pages for all layers, whose caches are alike; all pages are free at first
-        per = -(-max_len // page)
         pages = seqs * per if pages is None else pages
         self.tables = torch.full((seqs, per), -1, dtype=torch.int32, device=dev)
         self.free = torch.arange(pages, dtype=torch.int32, device=dev)

@@ -248,3 +248,16 @@ def test_a_request_that_waits_keeps_its_token(graphed):
                 lp), (t, b)
         waited += int((~served & (fresh > 0)).sum())
     assert waited == 25                                    # for a page, not by the caller's wish
+
+
+def test_requests_as_long_as_their_pages():
+    """A longest length inside a page: the pages' last positions have rows in the rotary table too, and a request is
+    served up to the end of its table's row."""
+    import model as E
+    m = E.Model(3, layers=1, vocab=500, hidden=256, heads=4, kv_heads=2, D=64, ffn=320, page=8, max_len=17, seed=5)
+    g = rng(5)
+    for t in range(26):
+        m.u.copy_(dev(g.random(3)))
+        m.step()
+        assert host(m.lens).tolist() == [min(t + 1, 24)] * 3
+        assert (host(m.tokens) >= 0).all() and np.isfinite(host(m.logprob)).all() and np.isfinite(host(m.logits)).all(), t
