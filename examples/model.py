@@ -27,12 +27,16 @@ from block import DecodeBlock  # noqa: E402
 class Model:
     def __init__(self, seqs, layers=2, vocab=32000, hidden=2560, heads=20, kv_heads=5, D=128, ffn=6912, page=16,
                  max_len=512, pages=None, kv="bf16", group=64, seed=0):
+        per = -(-max_len // page)
+        max_len = per * page                                   # kv_step fills pages to their ends
+        if pages is None:
+            pages = seqs * per
+        if not 0 <= pages <= seqs * per:
+            raise ValueError(f"pages: the layers' caches have {seqs * per}, got {pages}")
         dev = torch.device("cuda")
         g = torch.Generator(device=dev)
         g.manual_seed(seed)
         self.seqs, self.page, self.vocab, self.hidden, self.group = seqs, page, vocab, hidden, group
-        per = -(-max_len // page)
-        max_len = per * page                                   # kv_step fills pages to their ends
         self.layers = [DecodeBlock(seqs, hidden, heads, kv_heads, D, ffn, page, max_len, kv, seed + 1 + i)
                        for i in range(layers)]
 
@@ -40,7 +44,6 @@ class Model:
             return torch.empty(shape, dtype=dtype, device=dev)
 
         # one table of pages for all layers, whose caches are alike; all pages are free at first
-        pages = seqs * per if pages is None else pages
         self.tables = torch.full((seqs, per), -1, dtype=torch.int32, device=dev)
         self.free = torch.arange(pages, dtype=torch.int32, device=dev)
         self.lens, self.fresh = torch.zeros(seqs, dtype=torch.int32, device=dev), torch.ones(seqs, dtype=torch.int32,

@@ -375,3 +375,15 @@ def test_sample_reference_by_hand():
     assert draw(0.999, temperature=0.0) == 1
     assert abs(R.sample_row(x, 0.6)[1] - np.log(0.25)) < 1e-12
     assert R.sample_row([-np.inf, np.nan], 0.5)[:2] == (-1, -np.inf)
+
+
+def test_model_example_rejects_pages_that_its_caches_lack():
+    """Before it asks for a GPU: the stack would hand out pages in which no key is kept."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import model as E
+    for kw in (dict(pages=37), dict(pages=31, page=5, max_len=25), dict(pages=-1)):
+        with pytest.raises(ValueError, match="pages"):
+            E.Model(6, **dict(dict(layers=1, vocab=100, hidden=256, heads=4, kv_heads=2, D=64, ffn=320, page=4,
+                                   max_len=24), **kw))
