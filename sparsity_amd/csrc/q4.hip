@@ -5,8 +5,8 @@
 //
 // A group's inner sum is an int32 sum of one or two int8 MFMAs, exact; groups are joined in fp32.  The MFMA
 // takes 16 weight rows and 16 tokens.  A nibble becomes int8 by moving it into the upper half of its byte,
-// which is 16 times its value: one shift and two masks for eight weights, and the 16 leaves with the token's
-// scale.
+// which is 16 times its value: one shift and two masks for eight weights, and the 16 leaves where the sum is read as a
+// float.
 //
 // Few tokens: a wave takes a tile of 16 rows and all tokens, whose rows lie in LDS, as many columns at a time as fit.
 // More: a block's waves share two LDS buffers of the tokens' rows, NT tiles of 16.  KS waves of a block share a tile's
@@ -92,15 +92,16 @@ __global__ __launch_bounds__(256) void q4_pack_kernel(Q4PackArgs a) {
 typedef int v2i __attribute__((ext_vector_type(2)));
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
-// The MFMA's sums start from the bits of 1.5 * 2^23: what comes out, read as a float, is that number plus the sum,
-// which is below 2^22, and a subtraction takes the place of a conversion.
-constexpr float kBias = 12582912.f;
-constexpr int kBiasBits = 0x4B400000;
+// The MFMA's sums start from the bits of 1.5 * 2^19, a float whose last bit is 1 / 16: what comes out, 16 times the group's
+// sum and below 2^22, read as a float is that number plus the sum itself, and a subtraction takes the place of a conversion.
+// No factor of 16 is left to overflow in the joined sums or to cost the smallest scales of tokens their bits.
+constexpr float kBias = 786432.f;
+constexpr int kBiasBits = 0x49400000;
 
 // Four rows' sums of a token, from row o on.
 __device__ __forceinline__ void put_rows(const Q4Args& a, int t, int64_t o, const float sum[4]) {
   if (o >= a.n) return;
-  const float s = a.x_scale[t] * 0.0625f;
+  const float s = a.x_scale[t];
   float* y = a.y + (size_t)t * a.n + o;
   if (a.n % 4 == 0) {
     *(float4*)y = make_float4(sum[0] * s, sum[1] * s, sum[2] * s, sum[3] * s);

@@ -156,3 +156,24 @@ def test_a_captured_product():
         x.copy_(dev(xq))
         graph.replay()
         _check(host(y), xq, xs, q, s, 32)
+
+
+@pytest.mark.parametrize("T", [1, 4, 5, 20, 40, 64])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_products_of_the_largest_weights_and_the_smallest_scales(T, group):
+    """Sums of groups up to fp32's largest number, and scales of tokens below its normal ones: as long as the joined sum
+    is finite and the result normal, the bound is that of any other product."""
+    g = rng(T + group)
+    n, K = 40, 512
+    W = _weights(g, n, K)
+    top = np.float32(3.2e38) * np.exp2(-g.integers(0, 6, n)).astype(np.float32)
+    W[:, :group] = 0.0
+    W[np.arange(n), g.integers(0, group, n)] = top * g.choice([-1, 1], n)     # code 7 or -7, scale of top / 7
+    q, s = R.q4_quantize(W, group)
+    codes, scales = S.q4_pack(dev(W), group)
+    xq = g.integers(-127, 128, (T, K)).astype(np.int8)
+    xq[:, :group] = g.choice([-1, 1], (T, 1))
+    assert np.abs(s[:, 0] * 7).max() < np.finfo(np.float32).max * (1 - 2.0 ** -8)
+    for xs in (0.01 + g.random(T), (1 + g.random(T)) * 2.0 ** -126, np.ldexp(1 + g.integers(0, 32, T) / 32, -140)):
+        xs = xs.astype(np.float32)
+        _check(host(S.q4_fwd(dev(xq), dev(xs), K, codes, scales, n, group)), xq, xs, q, s, group)
