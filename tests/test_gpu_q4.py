@@ -177,3 +177,35 @@ def test_products_of_the_largest_weights_and_the_smallest_scales(T, group):
     for xs in (0.01 + g.random(T), (1 + g.random(T)) * 2.0 ** -126, np.ldexp(1 + g.integers(0, 32, T) / 32, -140)):
         xs = xs.astype(np.float32)
         _check(host(S.q4_fwd(dev(xq), dev(xs), K, codes, scales, n, group)), xq, xs, q, s, group)
+
+
+@pytest.mark.parametrize("T", [1, 2, 4, 5, 16, 32, 48, 64, 65])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("code,x", [(-8, -128), (-8, 127), (7, 127), (7, -128), (-7, -128)])
+def test_inner_sums_at_their_ends(T, group, code, x):
+    """The largest groups' sums, codes of -8 written into the layout among them: whole numbers below 2^24, so exact."""
+    n, K = 40, 512
+    q = np.full((n, K), code, np.int8)
+    q[::3, ::2] = 0
+    codes, scales = R.q4_pack(q, np.ones((n, K // group), np.float32), group)
+    xq = np.full((T, K), x, np.int8)
+    xq[1::2, 1::2] = -x - 1                                # -128 and 127 in turn
+    import torch
+    y = host(S.q4_fwd(dev(xq), dev(np.ones(T, np.float32)), K, dev(codes),
+                      dev(scales.view(np.int16)).view(torch.bfloat16), n, group))
+    assert np.array_equal(y, xq.astype(np.int64) @ q.T.astype(np.int64))
+
+
+@pytest.mark.parametrize("T", [3, 16, 30, 48, 64, 100])
+@pytest.mark.parametrize("n,K", [(300, 512), (2560, 1280), (9000, 256)])
+def test_other_tokens_of_a_call_do_not_touch_a_token(T, n, K):
+    """At one number of tokens, whatever the other rows and scales of the call are: NaN scales and full rows too."""
+    import torch
+    g = rng(T + n)
+    xq, xs, q, s, codes, scales = _case(g, T, n, K, 64)
+    first = S.q4_fwd(dev(xq), dev(xs), K, codes, scales, n)
+    _check(host(first), xq, xs, q, s, 64)
+    for t in sorted({0, 1, T // 2, T - 1}):
+        other, os = g.integers(-128, 128, (T, K)).astype(np.int8), np.full(T, np.nan, np.float32)
+        other[t], os[t] = xq[t], xs[t]
+        assert torch.equal(first[t], S.q4_fwd(dev(other), dev(os), K, codes, scales, n)[t])
