@@ -21,9 +21,10 @@
 // leave 420 tokens in the fullest of 131072 normal logits, and a plan is below kList but for odd rows; with 512 one in a
 // thousand was above it, and its call took 150 us in place of 54.
 //
-// Latency bounds one row: 131072 logits take 3.8, 13 and 9 us in the three launches, each a chain of dependent loads, a
+// Latency bounds one row: 131072 logits take 3.8, 14 and 9 us in the three launches, each a chain of dependent loads, a
 // hand-over between blocks (past the caches, that the XCDs do not share) and steps in LDS.  64 rows of mixed settings take
-// 8.4 (4 TB/s), 22 and 26 us: 28 vector instructions a weight, and rows that wait for their last block.
+// 8.4 (4 TB/s), 25.5 and 26 us: 28 vector instructions a weight and 15 for the log probability, and rows that wait for their
+// last block.
 #include <algorithm>
 
 #include "block_ops.hpp"
@@ -172,6 +173,23 @@ __device__ __forceinline__ u64 weight(double t) {
   p = fma_const(p, f, 0x1.0p+40);
   const uint2 bits = __builtin_bit_cast(uint2, __builtin_ldexp(p, (int)__builtin_bit_cast(uint2, m).x) + magic);
   return (u64)(bits.y & 0x7FFFFu) << 32 | bits.x;
+}
+// 2^t, t <= 0 (NaN, and what is below 2^-1000: nothing that counts), for sums of exp(x - top): a polynomial of (2^f - 1) / f
+// through the seven Chebyshev points, the result within 2^-33 of itself; exp2 in fp32 was off by the rounding of t, 10^-6 of
+// a term 13 below the largest, which showed where one token holds most of the probability (64 rows of 131072, mixed
+// settings: 25.5 us in the second launch, 22 by exp2).
+__device__ __forceinline__ double power(double t) {
+  const double magic = 6755399441055744.0;
+  t = __builtin_fmax(t, -1000.0);
+  const double m = t + magic, f = t - (m - magic);
+  double p = fma_const(f, 0x1.00a5814a072d8p-16, 0x1.443fffcad88f1p-13);
+  p = fma_const(p, f, 0x1.5d879ead1ff74p-10);
+  p = fma_const(p, f, 0x1.3b2a1b71506d0p-7);
+  p = fma_const(p, f, 0x1.c6b08d883db6cp-5);
+  p = fma_const(p, f, 0x1.ebfbe045f4d65p-3);
+  p = fma_const(p, f, 0x1.62e42fefa39efp-1);
+  p = fma_const(p, f, 1.0);
+  return __builtin_ldexp(p, (int)__builtin_bit_cast(uint2, m).x);
 }
 __device__ __forceinline__ u64 weight_of(const Row& r, float x) { return weight(scaled(r, x)); }
 
@@ -491,17 +509,8 @@ __global__ __launch_bounds__(kThreads) void sample_hist_kernel(SampleArgs a) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) d[j] = top - v[j];
     if (a.logprob) {
-      // eight at a time in fp32, unless one of them is 1, next to which small ones were lost, or NaN
-      float some = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) some += __builtin_amdgcn_exp2f(d[j] * -1.44269504f);
-      if (some < 1.f) {
-        e += some;
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          e += v[j] == top ? 1.0 : d[j] > 0.f ? (double)__builtin_amdgcn_exp2f(d[j] * -1.44269504f) : 0.0;
-      }
+      for (int j = 0; j < 8; ++j) e += power(((double)v[j] - dtop) * 1.4426950408889634);
     }
     if (st.greedy) continue;
 #pragma unroll

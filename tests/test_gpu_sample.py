@@ -258,3 +258,28 @@ def test_a_captured_draw():
         assert torch.equal(token, want[0]) and torch.equal(lp, want[1])
         for b in range(B):
             assert int(token[b]) == R.sample_row(host(x)[b], float(u[b]), float(temp[b]), int(k[b]))[0]
+
+
+@pytest.mark.parametrize("V", [300, 40011, 131072])
+@pytest.mark.parametrize("xd", ["f32", "bf16"])
+@pytest.mark.parametrize("tail", ["equal", "narrow", "wide", "masked"])
+def test_log_probabilities_of_confident_rows(V, xd, tail):
+    """A token above a tail that weighs from a hundredth to ten times as much: the sum's error shows in a small result.
+    A term of the sum is within 2^-33 of itself, so the sum's logarithm is off by 2^-33 tail / (1 + tail), at most 2^-33
+    of the result; doubled for what fp64 adds, besides its roundings next to 1 (2^-50 for all of them); and the result is
+    rounded once."""
+    g = rng(V)
+    x = {"equal": np.zeros((8, V)), "narrow": g.standard_normal((8, V)) * 0.05 - 0.37,
+         "wide": g.standard_normal((8, V)) * 2 - 2, "masked": g.standard_normal((8, V)) * 0.3}[tail]
+    if tail == "masked":
+        x[:, ::3], x[:, 1::3] = -INF, np.finfo(np.float32).min
+    x[:, V // 3] = np.log(V) + np.linspace(-2.3, 4.6, 8)
+    t, x = _upload(x + 7.3, xd)
+    import torch
+    for temperature in (0.0, 0.7):
+        token, lp = S.sample(t, dev(np.full(8, 0.3)), torch.full((8,), temperature, device="cuda"), want_logprob=True)
+        token, lp = host(token), host(lp).astype(np.float64)
+        for b in range(8):
+            want, ref, _ = R.sample_row(x[b], 0.3, float(np.float32(temperature)))
+            assert token[b] == want
+            assert abs(lp[b] - ref) <= (2.0 ** -24 + 2.0 ** -32) * abs(ref) + 2.0 ** -50, (b, lp[b], ref)
