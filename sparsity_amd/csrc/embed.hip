@@ -9,13 +9,14 @@
 // Gradient: tokens are sorted by id, so that a row's tokens are a run of sorted positions, and each run
 // is summed in the order of its tokens: results do not vary from run to run, and nothing is added by
 // atomics.  Launches:
-//   sort   blocks sort a chunk of tokens each, in registers and LDS
+//   sort   blocks sort a chunk of tokens each, in registers and LDS; where the gradient is overwritten, others clear its
+//          first rows
 //   rank   (several chunks) an element's place is its place in its chunk plus, by bisection, what the
 //          other chunks of its span of 65536 tokens hold before it; where there are several spans, once more
 //   sum    a wave takes 16 sorted positions and 512 columns; it sums every run that starts there, up to
 //          32 positions of it, and writes the row; of a longer run, what lies inside its 16 goes to the
-//          workspace.  Where the gradient is overwritten, the other blocks of the launch clear the rows that
-//          no token names (most of the bytes of a large table; the first are cleared beside the sort)
+//          workspace.  Where the gradient is overwritten, the other blocks of the launch clear those of the remaining
+//          rows that no token names
 //   join   the pieces of long runs, in order
 // Bound by memory in the sums: 8192 bf16 tokens of 3200 written over 32000 rows, 457 MB, take 16 (84 MB cleared), 5, 64 and 5
 // us; 32749 fp32 tokens of 2560 added to a table of 131072 rows, 579 MB, 11, 11, 130 (4.5 TB/s, the rate of a copy) and 11.
@@ -77,6 +78,13 @@ constexpr int kFillRows = 8;                 // rows that a wave of a fill block
 // 32749 of 2560 onto 131072 rows 335, 332, 329 and 332.
 constexpr int64_t kFillSort = 80 << 20;
 constexpr unsigned kFillBlocks = 512;
+// Where tokens can name an eighth of the rows at most, all is cleared there but for as much as hides the sums, and without
+// looking rows up: named ones are written twice, little of the whole.  Blocks of 256 threads with one store each write 6.6
+// TB/s (1.26 GB; blocks of 1024 6.1, pieces of 64 KB and more, as those of a row's block, 5.0).  Whole calls with 80 MB in
+// 512 blocks, and with all but 128, 64 and 0 MB: 64 tokens of 2400 onto 131072 rows 247, 198, 196 and 198 us (zeros and an
+// addition by index 204), 8192 of 2400 254, 217, 221 and 227, 4000 of 2560 onto 32000 67, 63, 68 and 74.
+constexpr int kPieceThreads = 256;
+constexpr int64_t kFillSum = 128 << 20;
 
 struct Sorted {                              // the workspace's arrays
   uint32_t *chunk_id, *chunk_tok, *span_id, *span_tok, *id, *tok;
@@ -111,10 +119,11 @@ __device__ __forceinline__ void fill_first(const EmbedBwdArgs& a, int64_t rows, 
 }
 
 // Chunk blockIdx.x of the tokens by id, then token.  A key is the id over the bits of the token's place in the
-// chunk: 32 bits in all for tables of less than 2^21 rows.  Two keys to a thread; distances below 64 inside a wave.  The first
-// `top` places, a power of two, hold all tokens that there are.
-template <class Key>
-__global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(EmbedBwdArgs a, Sorted s, int64_t fill, int top) {
+// chunk: 32 bits in all for tables of less than 2^21 rows.  A few keys to a thread; distances below 64 inside a wave.  The
+// first `top` places, a power of two, hold all tokens that there are.
+template <class Key, int kThreads>
+__global__ __launch_bounds__(kThreads) void embed_sort_kernel(EmbedBwdArgs a, Sorted s, int64_t fill, int top) {
+  constexpr int kKeys = kChunk / kThreads;
   __shared__ Key key[kChunk];
   if ((int)blockIdx.x >= s.chunks) {
     fill_first(a, fill, blockIdx.x - s.chunks, gridDim.x - s.chunks);
@@ -125,10 +134,10 @@ __global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(EmbedBwdArgs a
   const int64_t t0 = (int64_t)blockIdx.x * kChunk;
   const Key none = (Key)~(Key)0 >> kBits;
   if (blockIdx.x == 0 && tid == 0) s.runs[0] = 0;
-  Key v[2];
+  Key v[kKeys];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int i = h * kSortThreads + tid;
+  for (int h = 0; h < kKeys; ++h) {
+    const int i = h * kThreads + tid;
     const int32_t id = t0 + i < a.T ? a.ids[t0 + i] : -1;
     v[h] = (id >= 0 && id < a.V ? (Key)id : none) << kBits | (Key)i;
   }
@@ -136,30 +145,33 @@ __global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(EmbedBwdArgs a
     if (n > 64) {
       __syncthreads();
 #pragma unroll
-      for (int h = 0; h < 2; ++h) key[h * kSortThreads + tid] = v[h];
+      for (int h = 0; h < kKeys; ++h) key[h * kThreads + tid] = v[h];
       __syncthreads();
       for (int d = n >> 1; d >= 64; d >>= 1) {
-        const int lo = ((tid & ~(d - 1)) << 1) | (tid & (d - 1)), hi = lo | d;
-        const Key x = key[lo], y = key[hi];
-        if ((x > y) == ((lo & n) == 0)) {
-          key[lo] = y;
-          key[hi] = x;
+#pragma unroll
+        for (int h = 0; h < kKeys / 2; ++h) {
+          const int i = h * kThreads + tid, lo = ((i & ~(d - 1)) << 1) | (i & (d - 1)), hi = lo | d;
+          const Key x = key[lo], y = key[hi];
+          if ((x > y) == ((lo & n) == 0)) {
+            key[lo] = y;
+            key[hi] = x;
+          }
         }
         __syncthreads();
       }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) v[h] = key[h * kSortThreads + tid];
+      for (int h = 0; h < kKeys; ++h) v[h] = key[h * kThreads + tid];
     }
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) {
       if (d >= n) continue;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) v[h] = exchange(v[h], d, ((h * kSortThreads + tid) & n) == 0);
+      for (int h = 0; h < kKeys; ++h) v[h] = exchange(v[h], d, ((h * kThreads + tid) & n) == 0);
     }
   }
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int i = h * kSortThreads + tid;
+  for (int h = 0; h < kKeys; ++h) {
+    const int i = h * kThreads + tid;
     s.chunk_id[t0 + i] = v[h] >> kBits == none ? kNone : (uint32_t)(v[h] >> kBits);
     s.chunk_tok[t0 + i] = (uint32_t)t0 + (uint32_t)(v[h] & (kChunk - 1));
   }
@@ -461,12 +473,26 @@ hipError_t launch_embed_bwd(const EmbedBwdArgs& a, bool dy_bf16, hipStream_t s) 
   int64_t filled = 0;
   if (a.T > 0) {
     const unsigned sorts = (unsigned)w.chunks;
-    filled = a.accumulate ? 0 : std::min<int64_t>(a.V, kFillSort / (a.K * 4));
-    const unsigned some = filled ? kFillBlocks : 0;
+    const int64_t row = (int64_t)a.K * 4, rest = a.V * row - kFillSum;
+    const bool pieces = !a.accumulate && a.T <= a.V / 8 && rest > kFillSort;
+    unsigned some = 0;                       // blocks that clear
+    if (pieces) {
+      filled = rest / row;
+      some = (unsigned)std::min<int64_t>((filled * row / 16 + kPieceThreads - 1) / kPieceThreads, 1 << 22);
+    } else if (!a.accumulate) {
+      filled = std::min<int64_t>(a.V, kFillSort / row);
+      some = kFillBlocks;
+    }
     int top = 64;
     while (top < kChunk && top < a.T) top *= 2;
-    if (a.V < ((int64_t)1 << (32 - kEmbedChunkBits))) embed_sort_kernel<uint32_t><<<sorts + some, kSortThreads, 0, s>>>(a, so, filled, top);
-    else embed_sort_kernel<uint64_t><<<sorts + some, kSortThreads, 0, s>>>(a, so, filled, top);
+    const bool small = a.V < ((int64_t)1 << (32 - kEmbedChunkBits));
+    if (pieces) {
+      if (small) embed_sort_kernel<uint32_t, kPieceThreads><<<sorts + some, kPieceThreads, 0, s>>>(a, so, filled, top);
+      else embed_sort_kernel<uint64_t, kPieceThreads><<<sorts + some, kPieceThreads, 0, s>>>(a, so, filled, top);
+    } else {
+      if (small) embed_sort_kernel<uint32_t, kSortThreads><<<sorts + some, kSortThreads, 0, s>>>(a, so, filled, top);
+      else embed_sort_kernel<uint64_t, kSortThreads><<<sorts + some, kSortThreads, 0, s>>>(a, so, filled, top);
+    }
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if (w.chunks > 1) {
       embed_rank_kernel<<<(unsigned)w.chunks * (kChunk / kRankThreads), kRankThreads, 0, s>>>(a.T, so);

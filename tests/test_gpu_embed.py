@@ -233,3 +233,27 @@ def test_a_captured_gradient(accum):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, eager)
+
+
+@pytest.mark.parametrize("T,V,K,kind", [(1, 70000, 1024, "even"), (33, 70000, 1024, "one"), (2047, 30000, 2056, "zipf"),
+                                        (3749, 30000, 2056, "padded"), (3750, 30000, 2056, "even"), (3751, 30000, 2056, "even"),
+                                        (8750, 70000, 1024, "runs"), (70000, 560000, 104, "padded"), (5, 8, 32768, "even"),
+                                        (4100, (1 << 21) + 5, 40, "zipf"), (9, 2000, 32768, "even")])
+def test_gradient_of_large_tables(T, V, K, kind):
+    """Few tokens over tables of hundreds of MB, on both sides of what clears them first: rows at their places, the last
+    and the first row among them, everything else zero."""
+    import torch
+    g = rng(T + V)
+    ids = _ids(g, T, V, kind)
+    ids[-1], ids[T // 2] = V - 1, 0
+    dy, ref = _float(g, (T, K), "bf16", 2.0 ** -6)
+    print(T, V, K, kind, flush=True)
+    out = S.embed_bwd(dy, dev(ids), V, scale=3.0, out=torch.full((V, K), float("nan"), device="cuda"))
+    ok = (ids >= 0) & (ids < V)
+    rows, at = np.unique(ids[ok], return_inverse=True)
+    want, mag, n = R.embed_grad(ref[ok], at, len(rows), 3.0)
+    index = torch.from_numpy(rows).cuda().long()
+    got = host(out[index]).astype(np.float64)
+    assert np.all(np.abs(got - want) <= (n[:, None] + 1) * U * mag * (1 + 2.0 ** -8))
+    out[index] = 0
+    assert bool((out == 0).all())
