@@ -283,3 +283,18 @@ def test_log_probabilities_of_confident_rows(V, xd, tail):
             want, ref, _ = R.sample_row(x[b], 0.3, float(np.float32(temperature)))
             assert token[b] == want
             assert abs(lp[b] - ref) <= (2.0 ** -24 + 2.0 ** -32) * abs(ref) + 2.0 ** -50, (b, lp[b], ref)
+
+
+@pytest.mark.parametrize("V,std,mask", [(262144, 0.5, None), (200000, 1.0, None), (131072, 1.0, -1e4),
+                                        (131072, 1.0, np.finfo(np.float32).min), (131072, 1.0, -60.0)])
+def test_wide_questions_of_large_rows(V, std, mask):
+    """Top-k of a good part of the row and top-p behind it: together their bins hold more tokens than are listed, on
+    flat rows, and where a finite mask or one far logit makes the bins wide."""
+    g = rng(V + int(std * 10))
+    x = g.standard_normal((2, V)) * std
+    if mask == -60.0:
+        x[:, 5] = mask
+    elif mask is not None:
+        x[g.random((2, V)) < 0.5] = mask
+    for kw in [dict(k=V // 2, p=0.98), dict(k=V // 4, p=0.9), dict(p=0.95), dict(k=V // 2, p=0.95, min_p=0.05)]:
+        _check(x, g.random(2), temperature=1.5, **kw)
