@@ -9,7 +9,7 @@
 // request with many pages or tokens costs no more than many with one.
 //
 // Bound by latency: a chain of loads, scans and dependent stores, 8.3 us for 64 requests.  Above kRowsHere token rows a
-// second launch writes them with all CUs (65536 rows of 500 requests: 8.1 us).
+// second launch writes them, four to a thread (65536 rows of 500 requests, 64 blocks: 8.3 us).
 #include "device_common.hpp"
 #include "step_ops.hpp"
 #include "wave_ops.hpp"

@@ -21,8 +21,9 @@
 // leave 420 tokens in the fullest of 131072 normal logits.  The questions' bins hold more than kList tokens where a wide
 // top-k (a quarter of the row or more) meets top-p, each question known to within a few bins of the one before: on flat rows
 // from about 200000 logits on (262144 with a deviation of 1/2, top-k of half and top-p 0.98: one row that fits 50 us, 16 some
-// of which do not 200), and where many finite masks or a far logit widen the bins (131072 logits, half of them -10000, top-k
-// of 32768 and top-p 0.9: 124 us, 38 with -inf in their place).
+// of which do not 200), and where many finite masks widen the bins (131072 logits, half of them -10000, top-k of 32768 and
+// top-p 0.9: 124 us, 38 with -inf in their place); and for top-p alone where one far logit does (16 rows of 131072 with one
+// at -60 93 us, 38 without).
 //
 // Latency bounds one row: 131072 logits take 3.8, 14 and 9 us in the three launches, each a chain of dependent loads, a
 // hand-over between blocks (past the caches, that the XCDs do not share) and steps in LDS.  64 rows of mixed settings take
